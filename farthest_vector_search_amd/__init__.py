@@ -18,6 +18,16 @@ Functions (same names as the C entry points):
     vs_diversity_step(C, last_pick, mask_bits)         -> (idx, score)
     vs_diversity_gram(C)                               -> G (n x ldg Gram matrix)
     vs_diversity_step_gram(G, n, last_pick, mask_bits) -> (idx, score)
+    vs_group_rows(ids, n_groups)                       -> (order, offsets, slot)
+    vs_row_lookup(T, ids, scale)                       -> Y
+    vs_row_lookup_backward(dY, ids, order, offsets, scale) -> dT
+    vs_route_rows(X, slot, offsets, k)                 -> Xs (rows in unit order)
+    vs_route_rows_backward(dXs, slot, k)               -> dX
+    vs_combine_rows(Ys, slot, weights)                 -> Y
+    vs_combine_rows_backward(dY, Ys, slot, weights, offsets) -> (dYs, dweights)
+    vs_q4_quantize(T, group)                           -> (codes, scales)
+    vs_q4_layout(codes, scales, d, group)              -> table (4-bit, laid out)
+    vs_q4_scores(x, table, nc, group)                  -> scores
     vs_candidate_norms(C, feature_major=False)         -> norms
     vs_tile_rows(cache_bytes, d, bytes_per_value)      -> int (host only)
 Metrics: VS_L2SQ_MIN, VS_L2SQ_MAX, VS_COS_MAX, VS_COS_MIN.
@@ -36,7 +46,7 @@ METRICS = {"l2sq_min": 0, "l2sq_max": 1, "cos_max": 2, "cos_min": 3}
 
 STATUS = {0: "VS_OK", 1: "VS_ERR_NULL", 2: "VS_ERR_SHAPE", 3: "VS_ERR_METRIC",
           4: "VS_ERR_WORKSPACE", 5: "VS_ERR_ALIGN", 6: "VS_ERR_INDEX",
-          7: "VS_ERR_UNSUPPORTED", 8: "VS_ERR_HIP"}
+          7: "VS_ERR_UNSUPPORTED", 8: "VS_ERR_HIP", 9: "VS_ERR_DTYPE"}
 
 EXPORTS = ["vs_bmu_search_workspace", "vs_bmu_search", "vs_bmu_search_noalloc",
            "vs_bmu_search_unfused",
@@ -50,6 +60,10 @@ EXPORTS = ["vs_bmu_search_workspace", "vs_bmu_search", "vs_bmu_search_noalloc",
            "vs_som_update_workspace", "vs_som_update", "vs_som_update_csr", "vs_som_qe",
            "vs_som_epoch_workspace", "vs_som_epoch", "vs_som_epoch_csr_workspace",
            "vs_som_epoch_csr", "vs_som_epoch_csr_f16", "vs_csr_blocked_to_f16",
+           "vs_group_rows_workspace", "vs_group_rows", "vs_row_lookup",
+           "vs_row_lookup_backward_workspace", "vs_row_lookup_backward", "vs_route_rows",
+           "vs_route_rows_backward", "vs_combine_rows", "vs_combine_rows_backward",
+           "vs_q4_bytes", "vs_q4_quantize", "vs_q4_layout", "vs_q4_scores",
            "vs_candidate_norms", "vs_tile_rows", "vs_timing_enable", "vs_timing_read",
            "vs_timing_kernel_name", "vs_status_str", "vs_last_hip_error", "vs_version"]
 
@@ -120,6 +134,22 @@ def lib() -> ctypes.CDLL:
     L.vs_csr_blocked_to_f16.argtypes = [P, I64, I32, P, P]
     L.vs_som_epoch_csr_f16.argtypes = [P, P, P, I64, I64, P, P, I32, I32, I32, F, I32, P, P, P,
                                        P, SZ, P]
+    L.vs_group_rows_workspace.argtypes = [I64, I64]
+    L.vs_group_rows_workspace.restype = SZ
+    L.vs_group_rows.argtypes = [P, I64, I64, P, P, P, P, SZ, P]
+    L.vs_row_lookup.argtypes = [P, I64, I32, I32, P, I64, F, P, P]
+    L.vs_row_lookup_backward_workspace.argtypes = [I64, I32]
+    L.vs_row_lookup_backward_workspace.restype = SZ
+    L.vs_row_lookup_backward.argtypes = [P, I64, I32, I32, P, P, P, I64, F, I32, P, P, SZ, P]
+    L.vs_route_rows.argtypes = [P, I64, I32, I32, P, P, I64, I32, P, P]
+    L.vs_route_rows_backward.argtypes = [P, I64, I32, I32, P, I32, P, P]
+    L.vs_combine_rows.argtypes = [P, I64, I32, I32, P, P, I32, P, P]
+    L.vs_combine_rows_backward.argtypes = [P, P, I64, I32, I32, P, P, P, I64, I32, P, P, P]
+    L.vs_q4_bytes.argtypes = [I64, I32, I32]
+    L.vs_q4_bytes.restype = SZ
+    L.vs_q4_quantize.argtypes = [P, I64, I32, I32, I32, I32, P, P, P]
+    L.vs_q4_layout.argtypes = [P, P, I64, I32, I32, P, P]
+    L.vs_q4_scores.argtypes = [P, I64, I32, I32, P, I64, I32, I32, P, P]
     L.vs_candidate_norms.argtypes = [P, I64, I32, I32, P, P]
     L.vs_tile_rows.argtypes = [I64, I32, I32]
     L.vs_tile_rows.restype = I64
@@ -140,6 +170,9 @@ def lib() -> ctypes.CDLL:
                  "vs_som_update", "vs_som_update_csr", "vs_som_qe",
                  "vs_som_epoch", "vs_som_epoch_csr", "vs_som_epoch_csr_f16",
                  "vs_csr_blocked_to_f16",
+                 "vs_group_rows", "vs_row_lookup", "vs_row_lookup_backward", "vs_route_rows",
+                 "vs_route_rows_backward", "vs_combine_rows", "vs_combine_rows_backward",
+                 "vs_q4_quantize", "vs_q4_layout", "vs_q4_scores",
                  "vs_candidate_norms", "vs_timing_enable", "vs_timing_read",
                  "vs_last_hip_error"):
         getattr(L, name).restype = ctypes.c_int
@@ -901,6 +934,282 @@ def vs_som_epoch_csr_f16(indptr, indices, values, CB, map_shape, d: int, sigma: 
                                     ws.numel() * ws.element_size(), _stream(dev))
     _check(rc, "vs_som_epoch_csr_f16")
     return bmu_out, score_out, qe_out
+
+
+# Element types of the table operators (vs_dtype of the C ABI).
+VS_F32, VS_F16, VS_BF16 = 0, 1, 2
+_dtypes = None
+
+
+def _dtype(t, name):
+    """The vs_dtype of a tensor's or argument's element type."""
+    global _dtypes
+    if _dtypes is None:
+        torch = _torch()
+        _dtypes = {torch.float32: VS_F32, torch.float16: VS_F16, torch.bfloat16: VS_BF16}
+    code = _dtypes.get(t)
+    if code is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t}")
+    return code
+
+
+def _rows_arg(t, name, device=None, dtype=None):
+    """A contiguous matrix of a table operator, on the call's device."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
+    _dtype(t.dtype, name)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other inputs on {device}")
+    return t
+
+
+def _same_dev(t, name, dtype, device):
+    _dev(t, name, dtype)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other inputs on {device}")
+    return t
+
+
+def vs_group_rows(ids, n_groups: int, order=None, offsets=None, slot=None, workspace=None,
+                  want_slot: bool = True):
+    """Entries grouped by unit: a stable sort of the int32 ids (any shape, taken
+    flat).  Returns (order [n], offsets [n_groups + 1], slot [n] or None);
+    entries with an id outside [0, n_groups) are dropped (see include/vs.h)."""
+    torch = _torch()
+    L = lib()
+    _dev(ids, "ids", torch.int32)
+    n, n_groups = ids.numel(), int(n_groups)
+    dev = ids.device
+    if not 1 <= n_groups <= 2147483646:
+        raise VsError(2, "vs_group_rows")
+    order = _out(order, "order", torch.int32, n, dev)
+    offsets = _out(offsets, "offsets", torch.int32, n_groups + 1, dev)
+    slot = _out(slot, "slot", torch.int32, n, dev, want_slot)
+    ws = _workspace(L.vs_group_rows_workspace(n, n_groups), dev, workspace)
+    with _on(dev):
+        rc = L.vs_group_rows(_ptr(ids), n, n_groups, _ptr(order), _ptr(offsets), _ptr(slot),
+                             _ptr(ws), ws.numel() * ws.element_size(), _stream(dev))
+    _check(rc, "vs_group_rows")
+    return order, offsets, slot
+
+
+def vs_row_lookup(T, ids, scale: float = 1.0, out=None):
+    """Rows of the table T by index: out[i] = scale * T[ids[i]], a row of zeros
+    for an id outside the table.  ids may have any shape (taken flat)."""
+    torch = _torch()
+    L = lib()
+    _rows_arg(T, "T")
+    dev = T.device
+    _same_dev(ids, "ids", torch.int32, dev)
+    g, d = T.shape
+    n = ids.numel()
+    out = _out(out, "out", T.dtype, (n, d), dev)
+    with _on(dev):
+        rc = L.vs_row_lookup(_ptr(T), g, d, _dtype(T.dtype, "T"), _ptr(ids), n, float(scale),
+                             _ptr(out), _stream(dev))
+    _check(rc, "vs_row_lookup")
+    return out
+
+
+def vs_row_lookup_backward(dY, ids, order, offsets, scale: float = 1.0, grad_dtype=None,
+                           out=None, workspace=None):
+    """The table's gradient of vs_row_lookup: out[g] = scale * the sum of the
+    rows of dY whose id is g, zeros for the others.  order and offsets come
+    from vs_group_rows(ids, n_groups); grad_dtype is dY's type (default) or
+    torch.float32."""
+    torch = _torch()
+    L = lib()
+    _rows_arg(dY, "dY")
+    dev = dY.device
+    for t, name in ((ids, "ids"), (order, "order"), (offsets, "offsets")):
+        _same_dev(t, name, torch.int32, dev)
+    n, d = dY.shape
+    g = offsets.numel() - 1
+    if ids.numel() != n or order.numel() < n:
+        raise ValueError("ids and order must hold one entry per row of dY")
+    grad_dtype = dY.dtype if grad_dtype is None else grad_dtype
+    out = _out(out, "out", grad_dtype, (max(g, 0), d), dev)
+    ws = _workspace(L.vs_row_lookup_backward_workspace(n, d), dev, workspace)
+    with _on(dev):
+        rc = L.vs_row_lookup_backward(_ptr(dY), n, d, _dtype(dY.dtype, "dY"), _ptr(ids),
+                                      _ptr(order), _ptr(offsets), g, float(scale),
+                                      _dtype(grad_dtype, "grad_dtype"), _ptr(out), _ptr(ws),
+                                      ws.numel() * ws.element_size(), _stream(dev))
+    _check(rc, "vs_row_lookup_backward")
+    return out
+
+
+def _slots(slot, n, k, dev):
+    torch = _torch()
+    _same_dev(slot, "slot", torch.int32, dev)
+    if slot.numel() != n * k:
+        raise ValueError(f"slot holds {slot.numel()} entries, {n} rows of {k} need {n * k}")
+
+
+def vs_route_rows(X, slot, offsets, k: int, out=None):
+    """Rows sent to their units: out[slot[i * k + j]] = X[i] (n k rows in unit
+    order), zeros in the rows of no unit.  slot and offsets come from
+    vs_group_rows of the n x k ids."""
+    torch = _torch()
+    L = lib()
+    _rows_arg(X, "X")
+    dev = X.device
+    n, d = X.shape
+    k = int(k)
+    _slots(slot, n, k, dev)
+    _same_dev(offsets, "offsets", torch.int32, dev)
+    out = _out(out, "out", X.dtype, (n * k, d), dev)
+    with _on(dev):
+        rc = L.vs_route_rows(_ptr(X), n, d, _dtype(X.dtype, "X"), _ptr(slot), _ptr(offsets),
+                             offsets.numel() - 1, k, _ptr(out), _stream(dev))
+    _check(rc, "vs_route_rows")
+    return out
+
+
+def vs_route_rows_backward(dXs, slot, k: int, out=None):
+    """Gradient of vs_route_rows: out[i] = sum of dXs over row i's entries."""
+    L = lib()
+    _rows_arg(dXs, "dXs")
+    dev = dXs.device
+    m, d = dXs.shape
+    k = int(k)
+    if k < 1 or m % k:
+        raise ValueError(f"dXs must hold k = {k} rows per row")
+    n = m // k
+    _slots(slot, n, k, dev)
+    out = _out(out, "out", dXs.dtype, (n, d), dev)
+    with _on(dev):
+        rc = L.vs_route_rows_backward(_ptr(dXs), n, d, _dtype(dXs.dtype, "dXs"), _ptr(slot), k,
+                                      _ptr(out), _stream(dev))
+    _check(rc, "vs_route_rows_backward")
+    return out
+
+
+def vs_combine_rows(Ys, slot, weights, out=None):
+    """Rows brought back: out[i] = sum_j weights[i, j] Ys[slot[i * k + j]] over
+    the kept entries (Ys n k rows in unit order, weights n x k float32)."""
+    torch = _torch()
+    L = lib()
+    _rows_arg(Ys, "Ys")
+    dev = Ys.device
+    _rows_arg(weights, "weights", dev, torch.float32)
+    n, k = weights.shape
+    d = Ys.shape[1]
+    if Ys.shape[0] != n * k:
+        raise ValueError("Ys must hold one row per entry of weights")
+    _slots(slot, n, k, dev)
+    out = _out(out, "out", Ys.dtype, (n, d), dev)
+    with _on(dev):
+        rc = L.vs_combine_rows(_ptr(Ys), n, d, _dtype(Ys.dtype, "Ys"), _ptr(slot), _ptr(weights),
+                               k, _ptr(out), _stream(dev))
+    _check(rc, "vs_combine_rows")
+    return out
+
+
+def vs_combine_rows_backward(dY, Ys, slot, weights, offsets, out=None, dweights=None):
+    """Gradients of vs_combine_rows: (dYs, dweights), dYs[slot[e]] = weights[e]
+    dY[i] (zeros in the rows of no unit) and dweights[e] = dY[i] . Ys[slot[e]]
+    (0 for a dropped entry)."""
+    torch = _torch()
+    L = lib()
+    _rows_arg(dY, "dY")
+    dev = dY.device
+    _rows_arg(Ys, "Ys", dev, dY.dtype)
+    _rows_arg(weights, "weights", dev, torch.float32)
+    n, k = weights.shape
+    d = dY.shape[1]
+    if dY.shape[0] != n or tuple(Ys.shape) != (n * k, d):
+        raise ValueError("dY must be n x d and Ys (n * k) x d for weights n x k")
+    _slots(slot, n, k, dev)
+    _same_dev(offsets, "offsets", torch.int32, dev)
+    out = _out(out, "out", dY.dtype, (n * k, d), dev)
+    dweights = _out(dweights, "dweights", torch.float32, (n, k), dev)
+    with _on(dev):
+        rc = L.vs_combine_rows_backward(_ptr(dY), _ptr(Ys), n, d, _dtype(dY.dtype, "dY"),
+                                        _ptr(slot), _ptr(weights), _ptr(offsets),
+                                        offsets.numel() - 1, k, _ptr(out), _ptr(dweights),
+                                        _stream(dev))
+    _check(rc, "vs_combine_rows_backward")
+    return out, dweights
+
+
+def _q4_group(group):
+    group = int(group)
+    if group not in (32, 64, 128):
+        raise ValueError(f"group must be 32, 64 or 128, got {group}")
+    return group
+
+
+def vs_q4_quantize(T, group: int = 32, scale_dtype=None, codes=None, scales=None):
+    """4-bit codes and group scales of the table T (nc x d): (codes uint8
+    [nc, ceil(d / 2)], scales [nc, ceil(d / group)] of torch.float16 (default)
+    or torch.bfloat16); T[i, k] ~ scales[i, k // group] * (code - 8)."""
+    torch = _torch()
+    L = lib()
+    _rows_arg(T, "T")
+    dev = T.device
+    nc, d = T.shape
+    group = _q4_group(group)
+    scale_dtype = torch.float16 if scale_dtype is None else scale_dtype
+    codes = _out(codes, "codes", torch.uint8, (nc, (d + 1) // 2), dev)
+    scales = _out(scales, "scales", scale_dtype, (nc, (d + group - 1) // group), dev)
+    with _on(dev):
+        rc = L.vs_q4_quantize(_ptr(T), nc, d, _dtype(T.dtype, "T"), group,
+                              _dtype(scale_dtype, "scale_dtype"), _ptr(codes), _ptr(scales),
+                              _stream(dev))
+    _check(rc, "vs_q4_quantize")
+    return codes, scales
+
+
+def vs_q4_layout(codes, scales, d: int, group: int = 32, out=None):
+    """The laid-out table vs_q4_scores reads, from plain codes and scales (of
+    vs_q4_quantize, or a stored model's): a flat uint8 tensor."""
+    torch = _torch()
+    L = lib()
+    _dev(codes, "codes", torch.uint8, 2)
+    dev = codes.device
+    if not isinstance(scales, torch.Tensor) or scales.dtype not in (torch.float16,
+                                                                    torch.bfloat16):
+        raise TypeError("scales must be float16 or bfloat16")
+    _rows_arg(scales, "scales", dev)
+    nc, d, group = codes.shape[0], int(d), _q4_group(group)
+    if codes.shape[1] != (d + 1) // 2 or tuple(scales.shape) != (nc, (d + group - 1) // group):
+        raise ValueError(f"codes and scales disagree with {nc} rows of {d} in groups of {group}")
+    out = _out(out, "out", torch.uint8, L.vs_q4_bytes(nc, d, group), dev)
+    with _on(dev):
+        rc = L.vs_q4_layout(_ptr(codes), _ptr(scales), nc, d, group, _ptr(out), _stream(dev))
+    _check(rc, "vs_q4_layout")
+    return out
+
+
+def vs_q4_scores(x, table, nc: int, group: int = 32, scale_dtype=None, out=None):
+    """Scores [nq, nc] (float32) of the queries x (nq x d) over a table of nc
+    rows laid out by vs_q4_layout with this group and scale type (default
+    torch.float16)."""
+    torch = _torch()
+    L = lib()
+    _rows_arg(x, "x")
+    dev = x.device
+    _same_dev(table, "table", torch.uint8, dev)
+    nq, d = x.shape
+    nc, group = int(nc), _q4_group(group)
+    scale_dtype = torch.float16 if scale_dtype is None else scale_dtype
+    need = L.vs_q4_bytes(nc, d, group)
+    if table.numel() != need:
+        raise ValueError(f"table holds {table.numel()} bytes, {nc} rows of {d} take {need}")
+    out = _out(out, "out", torch.float32, (nq, nc), dev)
+    with _on(dev):
+        rc = L.vs_q4_scores(_ptr(x), nq, d, _dtype(x.dtype, "x"), _ptr(table), nc, group,
+                            _dtype(scale_dtype, "scale_dtype"), _ptr(out), _stream(dev))
+    _check(rc, "vs_q4_scores")
+    return out
 
 
 def vs_candidate_norms(C, feature_major: bool = False, out=None):

@@ -14,6 +14,7 @@
 
 #include "vs.h"
 #include "vs_internal.h"
+#include "vs_types.h"
 
 #define VS_API extern "C" __attribute__((visibility("default")))
 
@@ -999,6 +1000,204 @@ VS_API int vs_som_epoch_csr_f16(const int32_t *indptr, const int32_t *indices,
                              sigma, radius, ws + ws1, workspace_bytes - ws1, stream);
 }
 
+// ---- entries grouped by unit, rows by index and by unit ------------------------
+
+constexpr int64_t kMaxGroups = 2147483646;  // offsets hold n_groups + 1 values
+constexpr int32_t kMaxPerRow = 1024;
+
+static bool bad_dtype(int32_t t) { return t < vs::kF32 || t > vs::kBF16; }
+static bool al_type(const void *p, int32_t t) {
+    return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(vs::dtype_bytes(t) - 1)) == 0;
+}
+static bool bad_group_shape(int64_t n, int64_t n_groups) {
+    return n < 0 || n > kMaxIndex || n_groups < 1 || n_groups > kMaxGroups;
+}
+
+VS_API size_t vs_group_rows_workspace(int64_t n, int64_t n_groups) {
+    if (bad_group_shape(n, n_groups)) return 0;
+    return vs::group_workspace(n, n_groups);
+}
+
+VS_API int vs_group_rows(const int32_t *ids, int64_t n, int64_t n_groups, int32_t *order,
+                         int32_t *offsets, int32_t *slot, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+    if (bad_group_shape(n, n_groups)) return VS_ERR_SHAPE;
+    if ((n > 0 && (!ids || !order)) || !offsets || !workspace) return VS_ERR_NULL;
+    if (!al4(ids) || !al4(order) || !al4(offsets) || !al4(slot) || !al256(workspace))
+        return VS_ERR_ALIGN;
+    if (workspace_bytes < vs::group_workspace(n, n_groups)) return VS_ERR_WORKSPACE;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    VS_TRY_HIP(vs::launch_group(ids, n, n_groups, order, offsets, slot, workspace,
+                                reinterpret_cast<hipStream_t>(stream)));
+    return VS_OK;
+}
+
+VS_API int vs_row_lookup(const void *T, int64_t n_groups, int32_t d, int32_t dtype,
+                         const int32_t *ids, int64_t n, float scale, void *Y, void *stream) {
+    if (bad_dtype(dtype)) return VS_ERR_DTYPE;
+    if (bad_group_shape(n, n_groups) || d < 1 || d > kMaxDim) return VS_ERR_SHAPE;
+    if (n == 0) return VS_OK;
+    if (!T || !ids || !Y) return VS_ERR_NULL;
+    if (!al_type(T, dtype) || !al4(ids) || !al_type(Y, dtype)) return VS_ERR_ALIGN;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    VS_TRY_HIP(vs::launch_row_lookup(T, n_groups, d, dtype, ids, n, scale, Y,
+                                     reinterpret_cast<hipStream_t>(stream), n_cu));
+    return VS_OK;
+}
+
+VS_API size_t vs_row_lookup_backward_workspace(int64_t n, int32_t d) {
+    if (n < 0 || n > kMaxIndex || d < 1 || d > kMaxDim) return 0;
+    return vs::row_lookup_bwd_workspace(n, d);
+}
+
+VS_API int vs_row_lookup_backward(const void *dY, int64_t n, int32_t d, int32_t dtype,
+                                  const int32_t *ids, const int32_t *order,
+                                  const int32_t *offsets, int64_t n_groups, float scale,
+                                  int32_t grad_dtype, void *dT, void *workspace,
+                                  size_t workspace_bytes, void *stream) {
+    if (bad_dtype(dtype) || bad_dtype(grad_dtype) ||
+        (grad_dtype != dtype && grad_dtype != vs::kF32))
+        return VS_ERR_DTYPE;
+    if (bad_group_shape(n, n_groups) || d < 1 || d > kMaxDim) return VS_ERR_SHAPE;
+    if ((n > 0 && (!dY || !ids || !order)) || !offsets || !dT || !workspace) return VS_ERR_NULL;
+    if (!al_type(dY, dtype) || !al4(ids) || !al4(order) || !al4(offsets) ||
+        !al_type(dT, grad_dtype) || !al256(workspace))
+        return VS_ERR_ALIGN;
+    if (workspace_bytes < vs::row_lookup_bwd_workspace(n, d)) return VS_ERR_WORKSPACE;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    VS_TRY_HIP(vs::launch_row_lookup_bwd(dY, n, d, dtype, ids, order, offsets, n_groups, scale,
+                                         grad_dtype, dT, workspace,
+                                         reinterpret_cast<hipStream_t>(stream), n_cu));
+    return VS_OK;
+}
+
+// checks shared by the four calls on rows in unit order; n_groups is 1 where
+// the call takes none
+static int route_check(int64_t n, int32_t d, int32_t dtype, int64_t n_groups, int32_t k) {
+    if (bad_dtype(dtype)) return VS_ERR_DTYPE;
+    if (bad_group_shape(n, n_groups) || d < 1 || d > kMaxDim || k < 1 || k > kMaxPerRow ||
+        n * k > kMaxIndex)
+        return VS_ERR_SHAPE;
+    return VS_OK;
+}
+
+VS_API int vs_route_rows(const void *X, int64_t n, int32_t d, int32_t dtype, const int32_t *slot,
+                         const int32_t *offsets, int64_t n_groups, int32_t k, void *Xs,
+                         void *stream) {
+    if (const int s = route_check(n, d, dtype, n_groups, k)) return s;
+    if (n == 0) return VS_OK;
+    if (!X || !slot || !offsets || !Xs) return VS_ERR_NULL;
+    if (!al_type(X, dtype) || !al4(slot) || !al4(offsets) || !al_type(Xs, dtype))
+        return VS_ERR_ALIGN;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    VS_TRY_HIP(vs::launch_route_rows(X, n, d, dtype, slot, offsets + n_groups, k, Xs,
+                                     reinterpret_cast<hipStream_t>(stream), n_cu));
+    return VS_OK;
+}
+
+VS_API int vs_route_rows_backward(const void *dXs, int64_t n, int32_t d, int32_t dtype,
+                                  const int32_t *slot, int32_t k, void *dX, void *stream) {
+    if (const int s = route_check(n, d, dtype, 1, k)) return s;
+    if (n == 0) return VS_OK;
+    if (!dXs || !slot || !dX) return VS_ERR_NULL;
+    if (!al_type(dXs, dtype) || !al4(slot) || !al_type(dX, dtype)) return VS_ERR_ALIGN;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    VS_TRY_HIP(vs::launch_combine_rows(dXs, n, d, dtype, slot, nullptr, k, dX,
+                                       reinterpret_cast<hipStream_t>(stream), n_cu));
+    return VS_OK;
+}
+
+VS_API int vs_combine_rows(const void *Ys, int64_t n, int32_t d, int32_t dtype,
+                           const int32_t *slot, const float *weights, int32_t k, void *Y,
+                           void *stream) {
+    if (const int s = route_check(n, d, dtype, 1, k)) return s;
+    if (n == 0) return VS_OK;
+    if (!Ys || !slot || !weights || !Y) return VS_ERR_NULL;
+    if (!al_type(Ys, dtype) || !al4(slot) || !al4(weights) || !al_type(Y, dtype))
+        return VS_ERR_ALIGN;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    VS_TRY_HIP(vs::launch_combine_rows(Ys, n, d, dtype, slot, weights, k, Y,
+                                       reinterpret_cast<hipStream_t>(stream), n_cu));
+    return VS_OK;
+}
+
+VS_API int vs_combine_rows_backward(const void *dY, const void *Ys, int64_t n, int32_t d,
+                                    int32_t dtype, const int32_t *slot, const float *weights,
+                                    const int32_t *offsets, int64_t n_groups, int32_t k,
+                                    void *dYs, float *dweights, void *stream) {
+    if (const int s = route_check(n, d, dtype, n_groups, k)) return s;
+    if (n == 0) return VS_OK;
+    if (!dY || !Ys || !slot || !weights || !offsets || !dYs || !dweights) return VS_ERR_NULL;
+    if (!al_type(dY, dtype) || !al_type(Ys, dtype) || !al4(slot) || !al4(weights) ||
+        !al4(offsets) || !al_type(dYs, dtype) || !al4(dweights))
+        return VS_ERR_ALIGN;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    VS_TRY_HIP(vs::launch_combine_rows_bwd(dY, Ys, n, d, dtype, slot, weights, offsets + n_groups,
+                                           k, dYs, dweights,
+                                           reinterpret_cast<hipStream_t>(stream), n_cu));
+    return VS_OK;
+}
+
+// ---- tables in 4-bit codes ------------------------------------------------------
+
+static bool bad_q4_shape(int64_t nc, int32_t d, int32_t group) {
+    return nc < 1 || nc > kMaxIndex || d < 1 || d > kMaxDim ||
+           (group != 32 && group != 64 && group != 128);
+}
+static bool bad_scale_dtype(int32_t t) { return t != vs::kF16 && t != vs::kBF16; }
+inline bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+VS_API size_t vs_q4_bytes(int64_t nc, int32_t d, int32_t group) {
+    if (bad_q4_shape(nc, d, group)) return 0;
+    return vs::q4_bytes(nc, d, group);
+}
+
+VS_API int vs_q4_quantize(const void *T, int64_t nc, int32_t d, int32_t dtype, int32_t group,
+                          int32_t scale_dtype, uint8_t *codes, void *scales, void *stream) {
+    if (bad_dtype(dtype) || bad_scale_dtype(scale_dtype)) return VS_ERR_DTYPE;
+    if (bad_q4_shape(nc, d, group)) return VS_ERR_SHAPE;
+    if (!T || !codes || !scales) return VS_ERR_NULL;
+    if (!al_type(T, dtype) || !al_type(scales, scale_dtype)) return VS_ERR_ALIGN;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    VS_TRY_HIP(vs::launch_q4_quantize(T, nc, d, dtype, group, scale_dtype, codes, scales,
+                                      reinterpret_cast<hipStream_t>(stream), n_cu));
+    return VS_OK;
+}
+
+VS_API int vs_q4_layout(const uint8_t *codes, const void *scales, int64_t nc, int32_t d,
+                        int32_t group, void *out, void *stream) {
+    if (bad_q4_shape(nc, d, group)) return VS_ERR_SHAPE;
+    if (!codes || !scales || !out) return VS_ERR_NULL;
+    if ((reinterpret_cast<uintptr_t>(scales) & 1) != 0 || !al16(out)) return VS_ERR_ALIGN;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    VS_TRY_HIP(vs::launch_q4_layout(codes, scales, nc, d, group, out,
+                                    reinterpret_cast<hipStream_t>(stream), n_cu));
+    return VS_OK;
+}
+
+VS_API int vs_q4_scores(const void *x, int64_t nq, int32_t d, int32_t dtype, const void *table,
+                        int64_t nc, int32_t group, int32_t scale_dtype, float *y, void *stream) {
+    if (bad_dtype(dtype) || bad_scale_dtype(scale_dtype)) return VS_ERR_DTYPE;
+    if (nq < 0 || nq > kMaxIndex || bad_q4_shape(nc, d, group)) return VS_ERR_SHAPE;
+    if (nq == 0) return VS_OK;
+    if (!x || !table || !y) return VS_ERR_NULL;
+    if (!al_type(x, dtype) || !al16(table) || !al4(y)) return VS_ERR_ALIGN;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    VS_TRY_HIP(vs::launch_q4_scores(x, nq, d, dtype, table, nc, group, scale_dtype, y,
+                                    reinterpret_cast<hipStream_t>(stream)));
+    return VS_OK;
+}
+
 VS_API int64_t vs_tile_rows(int64_t cache_bytes, int32_t d, int32_t bytes_per_value) {
     if (cache_bytes <= 0 || d < 1 || bytes_per_value < 1) return 0;
     // floor(cache * 0.85 / (d * b)) in exact integer arithmetic: 0.85 = 17/20
@@ -1019,6 +1218,7 @@ VS_API const char *vs_status_str(int status) {
     case VS_ERR_INDEX: return "index out of range";
     case VS_ERR_UNSUPPORTED: return "no supported (gfx950) GPU";
     case VS_ERR_HIP: return "HIP error";
+    case VS_ERR_DTYPE: return "unknown or unsuitable element type";
     default: return "unknown status";
     }
 }

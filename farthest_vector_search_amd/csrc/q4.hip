@@ -1,0 +1,349 @@
+// q4.hip -- a candidate table in 4-bit codes and the scores of queries over it.
+//
+// Row i of the table stands for v[i, k] = s[i, k / group] (c[i, k] - 8), codes
+// c in 0 .. 15, one 16-bit scale per group of 32, 64 or 128 columns.  Scores
+// are the dot products y[q, i] = sum_k x[q, k] v[i, k], one group at a time:
+//   y = sum_g s_g (sum_{k in g} (16 + c_k) x_k - 24 sum_{k in g} x_k).
+// 16 + c is a 16-bit float made by putting the four code bits behind its
+// leading one, so a pair of codes costs one shift and one and-or; the matrix
+// instruction multiplies it exactly, and a second one with the constant -24
+// supplies the other sum.  Both start from zero in every group, in fp32.
+//
+// The matrix instruction is v_mfma_f32_16x16x32: 16 table rows x 16 columns of
+// queries.  f16 queries use its f16 form.  bf16 queries use the bf16 form;
+// f32 queries too, as three bf16 columns that add up to the query exactly
+// (8 + 8 + 8 bits), five queries to a tile of 16 columns.
+//
+// Layout of the table: blocks of 16 rows x 128 columns, 1 KiB of codes each,
+// in the order of the lanes: lane l (row l % 16, part l / 16) holds 16 bytes,
+// and its 32-bit word t holds columns 32 t + 8 (l / 16) .. + 7 of the block,
+// what the lane feeds to the t-th instruction.  Columns 2 j and 2 j + 1 of
+// the eight sit at bits 4 j and 16 + 4 j.  The scales follow behind all the
+// codes: per block four runs (rows 4 r .. 4 r + 3) of [group][row].
+#include <type_traits>
+
+#include "vs_internal.h"
+#include "vs_types.h"
+
+namespace vs {
+
+namespace {
+
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+
+constexpr int kBlockRows = 16, kBlockCols = 128;
+
+inline int64_t row_blocks(int64_t nc) { return (nc + kBlockRows - 1) / kBlockRows; }
+inline int64_t col_blocks(int64_t d) { return (d + kBlockCols - 1) / kBlockCols; }
+
+// ---- quantize: codes and scales of a plain table ---------------------------
+//
+// One lane per two columns (a byte of codes); the lanes of a group share its
+// largest magnitude.  s = max / 7 rounded to the scale type and held inside
+// its finite range; c = rint(v / s) held in -8 .. 7, ties to even, plus 8.
+template <typename T, typename S>
+__global__ __launch_bounds__(256) void k_q4_quantize(const T *__restrict__ table, int64_t nc,
+                                                     int32_t d, int group,
+                                                     uint8_t *__restrict__ codes,
+                                                     S *__restrict__ scales) {
+    const int lanes = group / 2;
+    const int64_t groups = (d + group - 1) / group;
+    const int64_t bytes = ((int64_t)d + 1) / 2;
+    const int64_t total = nc * groups;
+    const int sub = threadIdx.x & (lanes - 1);
+    const int per = 256 / lanes;
+    const float top = sizeof(S) == 2 && std::is_same<S, _Float16>::value ? 65504.0f : 3.3895314e38f;
+    for (int64_t e = (int64_t)blockIdx.x * per + threadIdx.x / lanes; e < total;
+         e += (int64_t)gridDim.x * per) {
+        const int64_t row = e / groups, g = e - row * groups;
+        const int64_t k = g * group + 2 * sub;
+        const T *src = table + row * d;
+        const float v0 = k < d ? widen(src[k]) : 0.0f;
+        const float v1 = k + 1 < d ? widen(src[k + 1]) : 0.0f;
+        float m = fmaxf(fabsf(v0), fabsf(v1));
+        for (int s = 1; s < lanes; s <<= 1) m = fmaxf(m, __shfl_xor(m, s));
+        const S sc = narrow<S>(fminf(m / 7.0f, top));
+        const float s = widen(sc);
+        int c0 = 8, c1 = 8;
+        if (s > 0.0f) {
+            c0 = 8 + (int)fminf(fmaxf(rintf(v0 / s), -8.0f), 7.0f);
+            c1 = 8 + (int)fminf(fmaxf(rintf(v1 / s), -8.0f), 7.0f);
+        }
+        if (k < d) codes[row * bytes + k / 2] = (uint8_t)(c0 | c1 << 4);
+        if (sub == 0) scales[row * groups + g] = sc;
+    }
+}
+
+// ---- layout: plain codes and scales into blocks ------------------------------
+
+__global__ __launch_bounds__(256) void k_q4_layout(const uint8_t *__restrict__ codes,
+                                                   const uint16_t *__restrict__ scales, int64_t nc,
+                                                   int32_t d, int group, int64_t nrb, int64_t ncb,
+                                                   uint32_t *__restrict__ out) {
+    const int64_t words = nrb * ncb * 256;
+    const int64_t bytes = ((int64_t)d + 1) / 2;
+    const int per_block = kBlockCols / group;  // groups per block
+    const int64_t groups = (d + group - 1) / group;
+    const int64_t nscale = nrb * ncb * per_block * kBlockRows;
+    uint16_t *sc = reinterpret_cast<uint16_t *>(out + words);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words + nscale;
+         i += (int64_t)gridDim.x * 256) {
+        if (i < words) {
+            const int64_t blk = i >> 8;
+            const int lane = (int)(i >> 2) & 63, t = (int)i & 3;
+            const int64_t rb = blk / ncb, cb = blk - rb * ncb;
+            const int64_t row = rb * kBlockRows + (lane & 15);
+            const int64_t k0 = cb * kBlockCols + 32 * t + 8 * (lane >> 4);
+            uint32_t w = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                uint32_t c = 8;  // stands for 0
+                if (row < nc && k0 + e < d)
+                    c = (codes[row * bytes + (k0 + e) / 2] >> (4 * (e & 1))) & 15;
+                w |= c << (4 * (e >> 1) + 16 * (e & 1));
+            }
+            out[i] = w;
+        } else {
+            const int64_t j = i - words;
+            const int64_t blk = j / (per_block * kBlockRows);
+            const int in = (int)(j - blk * (per_block * kBlockRows));
+            const int run = in / (4 * per_block), g = in / 4 % per_block, r = in % 4;
+            const int64_t rb = blk / ncb, cb = blk - rb * ncb;
+            const int64_t row = rb * kBlockRows + 4 * run + r, gg = cb * per_block + g;
+            sc[j] = row < nc && gg < groups ? scales[row * groups + gg] : (uint16_t)0;
+        }
+    }
+}
+
+// ---- scores -------------------------------------------------------------------
+
+// How queries of type X enter the matrix instruction.
+template <typename X>
+struct Form {  // f32 and bf16: bf16 columns
+    using A = bf16x8;
+    static constexpr int pieces = std::is_same<X, float>::value ? 3 : 1;
+    // 16 + c: 0x4180 | c << 3; -24 is 0xc1c0
+    static constexpr int place = 3;
+    static constexpr uint32_t lead = 0x41804180u, mask = 0x00780078u, minus24 = 0xc1c0c1c0u;
+    static __device__ __forceinline__ f32x4 mul(A a, A b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+};
+template <>
+struct Form<_Float16> {
+    using A = f16x8;
+    static constexpr int pieces = 1;
+    // 16 + c: 0x4c00 | c << 6; -24 is 0xce00
+    static constexpr int place = 6;
+    static constexpr uint32_t lead = 0x4c004c00u, mask = 0x03c003c0u, minus24 = 0xce00ce00u;
+    static __device__ __forceinline__ f32x4 mul(A a, A b, f32x4 c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+};
+
+union Frag {
+    uint32_t u[4];
+    bf16x8 b;
+    f16x8 h;
+};
+template <typename A>
+__device__ __forceinline__ A frag_as(const Frag &f) {
+    if constexpr (std::is_same<A, f16x8>::value) return f.h;
+    else return f.b;
+}
+
+// The eight codes of a word as 16 + c.
+template <typename F>
+__device__ __forceinline__ Frag expand(uint32_t w) {
+    Frag f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int up = F::place - 4 * j;
+        f.u[j] = ((up >= 0 ? w << up : w >> -up) & F::mask) | F::lead;
+    }
+    return f;
+}
+
+// Piece p of an f32 value: x = piece 0 + piece 1 + piece 2, each the leading
+// 8 bits of what is left.  A value that is not finite is its own piece 0.
+__device__ __forceinline__ uint32_t bf16_piece(float x, int p) {
+    const uint32_t u = __float_as_uint(x);
+    if ((u & 0x7f800000u) == 0x7f800000u) {
+        if (p > 0) return 0;
+        return (u >> 16) | ((u & 0x007fffffu) ? 0x40u : 0u);  // a NaN stays one
+    }
+    float r = x;
+    for (int i = 0; i < p; ++i) r -= __uint_as_float(__float_as_uint(r) & 0xffff0000u);
+    return __float_as_uint(r) >> 16;
+}
+
+// Columns k .. k + 7 of query q as one lane's operand (zeros past the query).
+template <typename X>
+__device__ __forceinline__ Frag query_frag(const X *__restrict__ x, int64_t nq, int32_t d,
+                                           int64_t q, int piece, int64_t k) {
+    Frag f;
+    const X *row = x + q * d;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        uint32_t h = 0;
+        if (q < nq && k + e < d) {
+            if constexpr (std::is_same<X, float>::value) {
+                h = bf16_piece(row[k + e], piece);
+            } else {
+                h = reinterpret_cast<const uint16_t *>(row)[k + e];
+            }
+        }
+        if (e & 1) f.u[e >> 1] |= h << 16;
+        else f.u[e >> 1] = h;
+    }
+    return f;
+}
+
+template <typename X, typename S, int GROUP>
+__global__ __launch_bounds__(256) void k_q4_scores(const X *__restrict__ x, int64_t nq, int64_t nc,
+                                                   int32_t d, int64_t nrb, int64_t ncb,
+                                                   const uint4 *__restrict__ codes,
+                                                   const S *__restrict__ scales,
+                                                   float *__restrict__ y) {
+    using F = Form<X>;
+    using A = typename F::A;
+    constexpr int QT = 16 / F::pieces;     // queries per tile of columns
+    constexpr int PER = kBlockCols / GROUP;  // groups per block
+    __shared__ float red[4][16][17];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int col = lane & 15, part = lane >> 4;
+    const int64_t tiles = (nq + QT - 1) / QT;
+    const int piece = col / QT;
+    Frag m24;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m24.u[j] = F::minus24;
+
+    for (int64_t ct = blockIdx.y; ct < tiles; ct += gridDim.y)
+        for (int64_t rb = blockIdx.x; rb < nrb; rb += gridDim.x) {
+            const int64_t q = col < QT * F::pieces ? ct * QT + col % QT : nq;
+            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int64_t cb = w; cb < ncb; cb += waves) {
+                const int64_t blk = rb * ncb + cb;
+                const uint4 a4 = codes[blk * 64 + lane];
+                const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w};
+                const S *sp = scales + (blk * 4 + part) * (4 * PER);
+#pragma unroll
+                for (int g = 0; g < PER; ++g) {
+                    f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int s = 0; s < GROUP / 32; ++s) {
+                        const int t = g * (GROUP / 32) + s;
+                        const Frag b = query_frag(x, nq, d, q, piece,
+                                                  cb * kBlockCols + 32 * t + 8 * part);
+                        c = F::mul(frag_as<A>(m24), frag_as<A>(b), c);
+                        c = F::mul(frag_as<A>(expand<F>(a[t])), frag_as<A>(b), c);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[r] = __builtin_fmaf(widen(sp[4 * g + r]), c[r], acc[r]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) red[w][col][4 * part + r] = acc[r];
+            __syncthreads();
+            for (int o = threadIdx.x; o < QT * 16; o += blockDim.x) {
+                const int r = o & 15, qq = o >> 4;
+                float sum = 0.0f;
+                for (int p = 0; p < F::pieces; ++p)
+                    for (int v = 0; v < waves; ++v) sum += red[v][qq + p * QT][r];
+                const int64_t row = rb * kBlockRows + r, query = ct * QT + qq;
+                if (row < nc && query < nq) y[query * nc + row] = sum;
+            }
+            __syncthreads();
+        }
+}
+
+template <typename X, typename S>
+hipError_t scores_group(const X *x, int64_t nq, int32_t d, const void *table, int64_t nc,
+                        int group, float *y, hipStream_t st) {
+    const int64_t nrb = row_blocks(nc), ncb = col_blocks(d);
+    const uint4 *codes = static_cast<const uint4 *>(table);
+    const S *scales = reinterpret_cast<const S *>(codes + nrb * ncb * 64);
+    const int64_t tiles = (nq * Form<X>::pieces + 15) / 16;
+    const dim3 grid((unsigned)(nrb < (1 << 20) ? nrb : 1 << 20), (unsigned)(tiles < 64 ? tiles : 64));
+    const dim3 block(64 * (unsigned)(ncb < 4 ? ncb : 4));
+    timing_before(st, "k_q4_scores");
+    switch (group) {
+    case 32:
+        hipLaunchKernelGGL((k_q4_scores<X, S, 32>), grid, block, 0, st, x, nq, nc, d, nrb, ncb,
+                           codes, scales, y);
+        break;
+    case 64:
+        hipLaunchKernelGGL((k_q4_scores<X, S, 64>), grid, block, 0, st, x, nq, nc, d, nrb, ncb,
+                           codes, scales, y);
+        break;
+    default:
+        hipLaunchKernelGGL((k_q4_scores<X, S, 128>), grid, block, 0, st, x, nq, nc, d, nrb, ncb,
+                           codes, scales, y);
+    }
+    timing_after(st);
+    return hipGetLastError();
+}
+
+template <typename X>
+hipError_t scores_scale(const void *x, int64_t nq, int32_t d, const void *table, int64_t nc,
+                        int group, int scale_dtype, float *y, hipStream_t st) {
+    if (scale_dtype == kF16)
+        return scores_group<X, _Float16>((const X *)x, nq, d, table, nc, group, y, st);
+    return scores_group<X, __bf16>((const X *)x, nq, d, table, nc, group, y, st);
+}
+
+template <typename T>
+hipError_t quantize_scale(const void *table, int64_t nc, int32_t d, int group, int scale_dtype,
+                          uint8_t *codes, void *scales, unsigned grid, hipStream_t st) {
+    if (scale_dtype == kF16)
+        hipLaunchKernelGGL((k_q4_quantize<T, _Float16>), dim3(grid), dim3(256), 0, st,
+                           (const T *)table, nc, d, group, codes, (_Float16 *)scales);
+    else
+        hipLaunchKernelGGL((k_q4_quantize<T, __bf16>), dim3(grid), dim3(256), 0, st,
+                           (const T *)table, nc, d, group, codes, (__bf16 *)scales);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t q4_bytes(int64_t nc, int32_t d, int group) {
+    const size_t blocks = (size_t)row_blocks(nc) * (size_t)col_blocks(d);
+    return blocks * (1024 + (size_t)(kBlockCols / group) * kBlockRows * 2);
+}
+
+hipError_t launch_q4_quantize(const void *table, int64_t nc, int32_t d, int dtype, int group,
+                              int scale_dtype, uint8_t *codes, void *scales, hipStream_t st,
+                              int n_cu) {
+    const int64_t want = (nc * ((d + group - 1) / group) * (group / 2) + 255) / 256;
+    const int64_t most = (int64_t)n_cu * 64;
+    const unsigned grid = (unsigned)(want < most ? want : most);
+    switch (dtype) {
+    case kF32: return quantize_scale<float>(table, nc, d, group, scale_dtype, codes, scales, grid, st);
+    case kF16: return quantize_scale<_Float16>(table, nc, d, group, scale_dtype, codes, scales, grid, st);
+    default: return quantize_scale<__bf16>(table, nc, d, group, scale_dtype, codes, scales, grid, st);
+    }
+}
+
+hipError_t launch_q4_layout(const uint8_t *codes, const void *scales, int64_t nc, int32_t d,
+                            int group, void *out, hipStream_t st, int n_cu) {
+    const int64_t nrb = row_blocks(nc), ncb = col_blocks(d);
+    const int64_t most = (int64_t)n_cu * 64;
+    const int64_t want = nrb * ncb + 1;
+    hipLaunchKernelGGL(k_q4_layout, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st,
+                       codes, (const uint16_t *)scales, nc, d, group, nrb, ncb, (uint32_t *)out);
+    return hipGetLastError();
+}
+
+hipError_t launch_q4_scores(const void *x, int64_t nq, int32_t d, int dtype, const void *table,
+                            int64_t nc, int group, int scale_dtype, float *y, hipStream_t st) {
+    switch (dtype) {
+    case kF32: return scores_scale<float>(x, nq, d, table, nc, group, scale_dtype, y, st);
+    case kF16: return scores_scale<_Float16>(x, nq, d, table, nc, group, scale_dtype, y, st);
+    default: return scores_scale<__bf16>(x, nq, d, table, nc, group, scale_dtype, y, st);
+    }
+}
+
+}  // namespace vs

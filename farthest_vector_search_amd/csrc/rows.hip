@@ -1,0 +1,310 @@
+// rows.hip -- rows of a table by index, rows sent to their units and brought
+// back with weights, and the gradients of both.
+//
+//   lookup            Y[i] = scale T[ids[i]]           (zeros: ids outside the table)
+//   lookup backward   dT[g] = scale sum dY[order[p]], p = offsets[g] .. offsets[g+1]-1
+//   route             Xs[slot[i k + j]] = X[i]
+//   combine           Y[i] = sum_j w[i k + j] Ys[slot[i k + j]]
+//   combine backward  dYs[slot[e]] = w[e] dY[e / k],  dw[e] = dY[e / k] . Ys[slot[e]]
+//   route backward    combine with every weight 1
+// All are bound by memory: a group of lanes takes a row, each lane one vector
+// of it at a time.  Sums are fp32 in a fixed order and rounded once.  Indices
+// come from device memory, so each is checked against its array before use.
+#include <type_traits>
+
+#include "vs_internal.h"
+#include "vs_types.h"
+
+namespace vs {
+
+namespace {
+
+// Lanes per row: the smallest power of two that covers a row's vectors, at
+// most a wave.  A workgroup of 256 threads takes 256 / lanes rows at a time.
+struct RowGrid {
+    int lanes, log2_lanes;
+    unsigned grid;
+};
+RowGrid row_grid(int64_t rows, int64_t vecs, int n_cu) {
+    RowGrid g{1, 0, 1};
+    while (g.lanes < 64 && g.lanes < vecs) g.lanes <<= 1, ++g.log2_lanes;
+    const int64_t want = (rows * g.lanes + 255) / 256;
+    const int64_t most = (int64_t)n_cu * 64;
+    g.grid = (unsigned)(want < 1 ? 1 : want < most ? want : most);
+    return g;
+}
+
+template <typename T, int N>
+__global__ __launch_bounds__(256) void k_row_lookup(const T *__restrict__ table, int64_t G,
+                                                    int32_t d, const int32_t *__restrict__ ids,
+                                                    int64_t n, float scale, T *__restrict__ Y,
+                                                    int lsh) {
+    using V = Vec<T, N>;
+    const int lane = threadIdx.x & ((1 << lsh) - 1);
+    const int64_t step = (int64_t)gridDim.x * (256 >> lsh);
+    const int vecs = d / N;
+    for (int64_t i = (int64_t)blockIdx.x * (256 >> lsh) + (threadIdx.x >> lsh); i < n; i += step) {
+        const int64_t id = ids[i];
+        const bool ok = id >= 0 && id < G;
+        const V *src = reinterpret_cast<const V *>(table + (ok ? id : 0) * d);
+        V *dst = reinterpret_cast<V *>(Y + i * d);
+        for (int c = lane; c < vecs; c += 1 << lsh) {
+            V v;
+            if (ok) v = src[c];
+#pragma unroll
+            for (int t = 0; t < N; ++t) v.v[t] = ok ? narrow<T>(scale * widen(v.v[t])) : T(0.0f);
+            dst[c] = v;
+        }
+    }
+}
+
+template <typename T, typename O, int N>
+__global__ __launch_bounds__(256) void k_row_lookup_bwd(
+    const T *__restrict__ dY, int64_t n, int32_t d, const int32_t *__restrict__ order,
+    const int32_t *__restrict__ offsets, int64_t G, float scale, O *__restrict__ dT, int lsh) {
+    const int lane = threadIdx.x & ((1 << lsh) - 1);
+    const int64_t step = (int64_t)gridDim.x * (256 >> lsh);
+    const int vecs = d / N;
+    for (int64_t g = (int64_t)blockIdx.x * (256 >> lsh) + (threadIdx.x >> lsh); g < G; g += step) {
+        int64_t lo = offsets[g], hi = offsets[g + 1];
+        lo = lo < 0 ? 0 : lo;
+        hi = hi > n ? n : hi;
+        for (int c = lane; c < vecs; c += 1 << lsh) {
+            float acc[N] = {};
+            for (int64_t p = lo; p < hi; ++p) {
+                const int64_t i = order[p];
+                if (i < 0 || i >= n) continue;
+                const Vec<T, N> v = reinterpret_cast<const Vec<T, N> *>(dY + i * d)[c];
+#pragma unroll
+                for (int t = 0; t < N; ++t) acc[t] += widen(v.v[t]);
+            }
+            Vec<O, N> o;
+#pragma unroll
+            for (int t = 0; t < N; ++t) o.v[t] = narrow<O>(scale * acc[t]);
+            reinterpret_cast<Vec<O, N> *>(dT + g * d)[c] = o;
+        }
+    }
+}
+
+// rows kept .. m-1 of a unit-ordered matrix (those of no unit) set to zero
+template <typename T, int N>
+__device__ __forceinline__ void zero_tail(T *__restrict__ Xs, int64_t kept, int64_t m, int32_t d,
+                                          int lane, int lsh, int64_t row, int64_t step) {
+    if (kept < 0) kept = 0;
+    for (int64_t p = kept + row; p < m; p += step)
+        for (int c = lane; c < d / N; c += 1 << lsh) {
+            Vec<T, N> z;
+#pragma unroll
+            for (int t = 0; t < N; ++t) z.v[t] = T(0.0f);
+            reinterpret_cast<Vec<T, N> *>(Xs + p * d)[c] = z;
+        }
+}
+
+template <typename T, int N>
+__global__ __launch_bounds__(256) void k_route_rows(const T *__restrict__ X, int64_t n, int32_t d,
+                                                    const int32_t *__restrict__ slot,
+                                                    const int32_t *__restrict__ kept, int32_t k,
+                                                    T *__restrict__ Xs, int lsh) {
+    using V = Vec<T, N>;
+    const int lane = threadIdx.x & ((1 << lsh) - 1);
+    const int64_t step = (int64_t)gridDim.x * (256 >> lsh);
+    const int64_t row = (int64_t)blockIdx.x * (256 >> lsh) + (threadIdx.x >> lsh);
+    const int64_t m = n * k;
+    const int vecs = d / N;
+    for (int64_t i = row; i < n; i += step) {
+        for (int c = lane; c < vecs; c += 1 << lsh) {
+            const V v = reinterpret_cast<const V *>(X + i * d)[c];
+            for (int j = 0; j < k; ++j) {
+                const int64_t p = slot[i * k + j];
+                if (p >= 0 && p < m) reinterpret_cast<V *>(Xs + p * d)[c] = v;
+            }
+        }
+    }
+    zero_tail<T, N>(Xs, *kept, m, d, lane, lsh, row, step);
+}
+
+template <typename T, int N>
+__global__ __launch_bounds__(256) void k_combine_rows(const T *__restrict__ Ys, int64_t n,
+                                                      int32_t d, const int32_t *__restrict__ slot,
+                                                      const float *__restrict__ weights, int32_t k,
+                                                      T *__restrict__ Y, int lsh) {
+    using V = Vec<T, N>;
+    const int lane = threadIdx.x & ((1 << lsh) - 1);
+    const int64_t step = (int64_t)gridDim.x * (256 >> lsh);
+    const int64_t m = n * k;
+    const int vecs = d / N;
+    for (int64_t i = (int64_t)blockIdx.x * (256 >> lsh) + (threadIdx.x >> lsh); i < n; i += step) {
+        for (int c = lane; c < vecs; c += 1 << lsh) {
+            float acc[N] = {};
+            for (int j = 0; j < k; ++j) {
+                const int64_t p = slot[i * k + j];
+                if (p < 0 || p >= m) continue;
+                const float w = weights ? weights[i * k + j] : 1.0f;
+                const V v = reinterpret_cast<const V *>(Ys + p * d)[c];
+#pragma unroll
+                for (int t = 0; t < N; ++t) acc[t] = __builtin_fmaf(w, widen(v.v[t]), acc[t]);
+            }
+            V o;
+#pragma unroll
+            for (int t = 0; t < N; ++t) o.v[t] = narrow<T>(acc[t]);
+            reinterpret_cast<V *>(Y + i * d)[c] = o;
+        }
+    }
+}
+
+template <typename T, int N>
+__global__ __launch_bounds__(256) void k_combine_rows_bwd(
+    const T *__restrict__ dY, const T *__restrict__ Ys, int64_t n, int32_t d,
+    const int32_t *__restrict__ slot, const float *__restrict__ weights,
+    const int32_t *__restrict__ kept, int32_t k, T *__restrict__ dYs, float *__restrict__ dw,
+    int lsh) {
+    using V = Vec<T, N>;
+    const int lane = threadIdx.x & ((1 << lsh) - 1);
+    const int64_t step = (int64_t)gridDim.x * (256 >> lsh);
+    const int64_t row = (int64_t)blockIdx.x * (256 >> lsh) + (threadIdx.x >> lsh);
+    const int64_t m = n * k;
+    const int vecs = d / N;
+    for (int64_t i = row; i < n; i += step) {
+        for (int j = 0; j < k; ++j) {
+            const int64_t p = slot[i * k + j];
+            float dot = 0.0f;
+            if (p >= 0 && p < m) {
+                const float w = weights[i * k + j];
+                for (int c = lane; c < vecs; c += 1 << lsh) {
+                    const V a = reinterpret_cast<const V *>(dY + i * d)[c];
+                    const V b = reinterpret_cast<const V *>(Ys + p * d)[c];
+                    V o;
+#pragma unroll
+                    for (int t = 0; t < N; ++t) {
+                        dot = __builtin_fmaf(widen(a.v[t]), widen(b.v[t]), dot);
+                        o.v[t] = narrow<T>(w * widen(a.v[t]));
+                    }
+                    reinterpret_cast<V *>(dYs + p * d)[c] = o;
+                }
+            }
+            for (int s = 1; s < 1 << lsh; s <<= 1) dot += __shfl_xor(dot, s);
+            if (lane == 0) dw[i * k + j] = dot;
+        }
+    }
+    zero_tail<T, N>(dYs, *kept, m, d, lane, lsh, row, step);
+}
+
+// f(element type, elements per access) for a row type; N covers 16 bytes and
+// the smaller powers of two
+template <typename T, typename F>
+hipError_t with_vec(int n, F f) {
+    switch (n) {
+    case 8:
+        if constexpr (sizeof(T) == 2) return f(T(), std::integral_constant<int, 8>());
+        return hipErrorInvalidValue;
+    case 4: return f(T(), std::integral_constant<int, 4>());
+    case 2: return f(T(), std::integral_constant<int, 2>());
+    default: return f(T(), std::integral_constant<int, 1>());
+    }
+}
+template <typename F>
+hipError_t with_type(int dtype, int n, F f) {
+    switch (dtype) {
+    case kF32: return with_vec<float>(n, f);
+    case kF16: return with_vec<_Float16>(n, f);
+    default: return with_vec<__bf16>(n, f);
+    }
+}
+
+inline uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
+
+}  // namespace
+
+hipError_t launch_row_lookup(const void *table, int64_t G, int32_t d, int dtype,
+                             const int32_t *ids, int64_t n, float scale, void *Y, hipStream_t st,
+                             int n_cu) {
+    const int nv = vec_elems(d, dtype_bytes(dtype), addr(table) | addr(Y));
+    const RowGrid g = row_grid(n, d / nv, n_cu);
+    return with_type(dtype, nv, [&](auto t, auto nc) {
+        using T = decltype(t);
+        timing_before(st, "k_row_lookup");
+        hipLaunchKernelGGL((k_row_lookup<T, decltype(nc)::value>), dim3(g.grid), dim3(256), 0, st,
+                           (const T *)table, G, d, ids, n, scale, (T *)Y, g.log2_lanes);
+        timing_after(st);
+        return hipGetLastError();
+    });
+}
+
+size_t row_lookup_bwd_workspace(int64_t n, int32_t d) {
+    (void)n, (void)d;
+    return 256;
+}
+
+hipError_t launch_row_lookup_bwd(const void *dY, int64_t n, int32_t d, int dtype,
+                                 const int32_t *ids, const int32_t *order, const int32_t *offsets,
+                                 int64_t G, float scale, int grad_dtype, void *dT, void *ws,
+                                 hipStream_t st, int n_cu) {
+    (void)ids, (void)ws;
+    // one vector length for both sides: the shorter of what each allows
+    int nv = vec_elems(d, dtype_bytes(dtype), addr(dY));
+    const int no = vec_elems(d, dtype_bytes(grad_dtype), addr(dT));
+    if (no < nv) nv = no;
+    const RowGrid g = row_grid(G, d / nv, n_cu);
+    return with_type(dtype, nv, [&](auto t, auto nc) {
+        using T = decltype(t);
+        constexpr int N = decltype(nc)::value;
+        timing_before(st, "k_row_lookup_bwd");
+        if (grad_dtype == dtype)
+            hipLaunchKernelGGL((k_row_lookup_bwd<T, T, N>), dim3(g.grid), dim3(256), 0, st,
+                               (const T *)dY, n, d, order, offsets, G, scale, (T *)dT,
+                               g.log2_lanes);
+        else
+            hipLaunchKernelGGL((k_row_lookup_bwd<T, float, N>), dim3(g.grid), dim3(256), 0, st,
+                               (const T *)dY, n, d, order, offsets, G, scale, (float *)dT,
+                               g.log2_lanes);
+        timing_after(st);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_route_rows(const void *X, int64_t n, int32_t d, int dtype, const int32_t *slot,
+                             const int32_t *kept, int32_t k, void *Xs, hipStream_t st, int n_cu) {
+    const int nv = vec_elems(d, dtype_bytes(dtype), addr(X) | addr(Xs));
+    const RowGrid g = row_grid(n, d / nv, n_cu);
+    return with_type(dtype, nv, [&](auto t, auto nc) {
+        using T = decltype(t);
+        timing_before(st, "k_route_rows");
+        hipLaunchKernelGGL((k_route_rows<T, decltype(nc)::value>), dim3(g.grid), dim3(256), 0, st,
+                           (const T *)X, n, d, slot, kept, k, (T *)Xs, g.log2_lanes);
+        timing_after(st);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_combine_rows(const void *Ys, int64_t n, int32_t d, int dtype,
+                               const int32_t *slot, const float *weights, int32_t k, void *Y,
+                               hipStream_t st, int n_cu) {
+    const int nv = vec_elems(d, dtype_bytes(dtype), addr(Ys) | addr(Y));
+    const RowGrid g = row_grid(n, d / nv, n_cu);
+    return with_type(dtype, nv, [&](auto t, auto nc) {
+        using T = decltype(t);
+        timing_before(st, "k_combine_rows");
+        hipLaunchKernelGGL((k_combine_rows<T, decltype(nc)::value>), dim3(g.grid), dim3(256), 0,
+                           st, (const T *)Ys, n, d, slot, weights, k, (T *)Y, g.log2_lanes);
+        timing_after(st);
+        return hipGetLastError();
+    });
+}
+
+hipError_t launch_combine_rows_bwd(const void *dY, const void *Ys, int64_t n, int32_t d, int dtype,
+                                   const int32_t *slot, const float *weights, const int32_t *kept,
+                                   int32_t k, void *dYs, float *dw, hipStream_t st, int n_cu) {
+    const int nv = vec_elems(d, dtype_bytes(dtype), addr(dY) | addr(Ys) | addr(dYs));
+    const RowGrid g = row_grid(n, d / nv, n_cu);
+    return with_type(dtype, nv, [&](auto t, auto nc) {
+        using T = decltype(t);
+        timing_before(st, "k_combine_rows_bwd");
+        hipLaunchKernelGGL((k_combine_rows_bwd<T, decltype(nc)::value>), dim3(g.grid), dim3(256),
+                           0, st, (const T *)dY, (const T *)Ys, n, d, slot, weights, kept, k,
+                           (T *)dYs, dw, g.log2_lanes);
+        timing_after(st);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace vs

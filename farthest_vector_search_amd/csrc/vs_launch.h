@@ -121,6 +121,39 @@ struct SomArgs {
 hipError_t launch_som_update(const SomArgs &a, hipStream_t st, int n_cu);
 hipError_t launch_som_qe(const float *score, int64_t n, double *out, hipStream_t st);
 
+// Entries grouped by unit (group.hip): order, offsets (G + 1) and, where not
+// null, slot.  ws holds group_workspace bytes.
+size_t group_workspace(int64_t n, int64_t G);
+hipError_t launch_group(const int32_t *ids, int64_t n, int64_t G, int32_t *order,
+                        int32_t *offsets, int32_t *slot, void *ws, hipStream_t st);
+// Rows by index, rows by unit and their gradients (rows.hip); dtype: vs_dtype.
+// kept points at the number of kept entries (the last of the offsets).
+hipError_t launch_row_lookup(const void *table, int64_t G, int32_t d, int dtype,
+                             const int32_t *ids, int64_t n, float scale, void *Y, hipStream_t st,
+                             int n_cu);
+size_t row_lookup_bwd_workspace(int64_t n, int32_t d);
+hipError_t launch_row_lookup_bwd(const void *dY, int64_t n, int32_t d, int dtype,
+                                 const int32_t *ids, const int32_t *order, const int32_t *offsets,
+                                 int64_t G, float scale, int grad_dtype, void *dT, void *ws,
+                                 hipStream_t st, int n_cu);
+hipError_t launch_route_rows(const void *X, int64_t n, int32_t d, int dtype, const int32_t *slot,
+                             const int32_t *kept, int32_t k, void *Xs, hipStream_t st, int n_cu);
+hipError_t launch_combine_rows(const void *Ys, int64_t n, int32_t d, int dtype,
+                               const int32_t *slot, const float *weights, int32_t k, void *Y,
+                               hipStream_t st, int n_cu);
+hipError_t launch_combine_rows_bwd(const void *dY, const void *Ys, int64_t n, int32_t d, int dtype,
+                                   const int32_t *slot, const float *weights, const int32_t *kept,
+                                   int32_t k, void *dYs, float *dw, hipStream_t st, int n_cu);
+// Tables in 4-bit codes (q4.hip)
+size_t q4_bytes(int64_t nc, int32_t d, int group);
+hipError_t launch_q4_quantize(const void *table, int64_t nc, int32_t d, int dtype, int group,
+                              int scale_dtype, uint8_t *codes, void *scales, hipStream_t st,
+                              int n_cu);
+hipError_t launch_q4_layout(const uint8_t *codes, const void *scales, int64_t nc, int32_t d,
+                            int group, void *out, hipStream_t st, int n_cu);
+hipError_t launch_q4_scores(const void *x, int64_t nq, int32_t d, int dtype, const void *table,
+                            int64_t nc, int group, int scale_dtype, float *y, hipStream_t st);
+
 // Timing hook (api.hip).
 void timing_before(hipStream_t st, const char *name);
 void timing_after(hipStream_t st);

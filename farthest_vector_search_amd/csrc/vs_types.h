@@ -1,0 +1,36 @@
+// vs_types.h -- element types and short vectors of the table operators
+// (group.hip, rows.hip, q4.hip).
+//
+// Arithmetic is fp32 throughout: values are widened on load (exactly) and
+// rounded once, to nearest even, when they are stored.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace vs {
+
+enum DType : int { kF32 = 0, kF16 = 1, kBF16 = 2 };
+
+inline int dtype_bytes(int t) { return t == kF32 ? 4 : 2; }
+
+template <typename T>
+__device__ __forceinline__ float widen(T x) { return (float)x; }
+template <typename T>
+__device__ __forceinline__ T narrow(float x) { return (T)x; }
+
+template <typename T, int N>
+struct alignas(sizeof(T) * N) Vec {
+    T v[N];
+};
+
+// Elements per vector access: 16 bytes where every row starts on a 16-byte
+// boundary (the row size and the matrices' addresses allow it), else the
+// largest power of two that does.  `addr` is the or of the addresses.
+inline int vec_elems(int64_t d, int esize, uintptr_t addr) {
+    const uint64_t bits = (uint64_t)d * (uint64_t)esize | (uint64_t)addr | 16u;
+    const int bytes = (int)(bits & (~bits + 1));
+    return bytes / esize;
+}
+
+}  // namespace vs

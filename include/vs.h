@@ -69,7 +69,9 @@ typedef enum {
                                workspace not 256-byte aligned               */
     VS_ERR_INDEX = 6,       /* an index argument is out of range             */
     VS_ERR_UNSUPPORTED = 7, /* no GPU of a supported architecture            */
-    VS_ERR_HIP = 8          /* a HIP call failed; see vs_last_hip_error()    */
+    VS_ERR_HIP = 8,         /* a HIP call failed; see vs_last_hip_error()    */
+    VS_ERR_DTYPE = 9        /* unknown element type, or one the call does
+                               not take                                     */
 } vs_status;
 
 typedef enum {
@@ -78,6 +80,13 @@ typedef enum {
     VS_COS_MAX = 2,  /* most similar: rows unit-norm, score = dot          */
     VS_COS_MIN = 3   /* most different: rows unit-norm, score = dot [DIV]  */
 } vs_metric;
+
+/* Element types of the table operators (vs_group_rows and below). */
+typedef enum {
+    VS_F32 = 0,
+    VS_F16 = 1, /* IEEE binary16 */
+    VS_BF16 = 2
+} vs_dtype;
 
 /*
  * Dense search [BMU].
@@ -429,6 +438,114 @@ int vs_som_epoch_csr_f16(const int32_t *indptr, const int32_t *indices, const fl
                          int32_t map_cols, int32_t d, float sigma, int32_t radius,
                          int32_t *bmu_out, float *score_out, double *qe_out, void *workspace,
                          size_t workspace_bytes, void *stream);
+
+/*
+ * Entries grouped by unit: a stable sort of indices, e.g. of the winners a
+ * search returned.
+ *   ids        int32[n]: the unit of each entry.  An id outside [0, n_groups)
+ *              (the -1 of a search without a candidate) drops the entry.
+ *   order      int32[n]: the entries sorted by unit, entries of one unit in
+ *              their own order; -1 behind the last kept entry.
+ *   offsets    int32[n_groups + 1]: unit g's entries are order[offsets[g]] ..
+ *              order[offsets[g + 1] - 1]; offsets[n_groups] = entries kept.
+ *   slot       int32[n] or NULL: each entry's place in order, -1 if dropped.
+ * n in [0, 2^31-1] (0 writes the offsets only), n_groups in [1, 2^31-2].
+ * The outputs must not overlap ids.
+ */
+size_t vs_group_rows_workspace(int64_t n, int64_t n_groups);
+int vs_group_rows(const int32_t *ids, int64_t n, int64_t n_groups, int32_t *order,
+                  int32_t *offsets, int32_t *slot, void *workspace, size_t workspace_bytes,
+                  void *stream);
+
+/*
+ * Rows of a table by index, and the table's gradient (next to
+ * vs_diversity_accumulate, which adds picked rows in place, and to the SOM
+ * batch update, which sums inputs per neuron with float atomics).
+ *   vs_row_lookup           Y[i] = scale T[ids[i]], i < n; a row of zeros for
+ *                           an id outside [0, n_groups).  T is n_groups x d,
+ *                           Y n x d, both of `dtype` (a vs_dtype).
+ *   vs_row_lookup_backward  dT[g] = scale sum of the rows dY[i] with ids[i] =
+ *                           g, summed in fp32 in a fixed order and rounded
+ *                           once; units without entries get zeros, so every
+ *                           row of dT is written.  dY is n x d of `dtype`,
+ *                           dT n_groups x d of `grad_dtype` (`dtype` or
+ *                           VS_F32, else VS_ERR_DTYPE).  order and offsets as
+ *                           vs_group_rows makes them from the same ids.
+ * n in [0, 2^31-1], n_groups in [1, 2^31-2], d in [1, 2^20].  Addresses are
+ * aligned to their element; rows on 16-byte boundaries are fastest.  An
+ * index read from order or offsets that does not fit the arrays is skipped;
+ * nothing outside the arrays is read.  Inputs and outputs must not overlap.
+ */
+int vs_row_lookup(const void *T, int64_t n_groups, int32_t d, int32_t dtype, const int32_t *ids,
+                  int64_t n, float scale, void *Y, void *stream);
+size_t vs_row_lookup_backward_workspace(int64_t n, int32_t d);
+int vs_row_lookup_backward(const void *dY, int64_t n, int32_t d, int32_t dtype,
+                           const int32_t *ids, const int32_t *order, const int32_t *offsets,
+                           int64_t n_groups, float scale, int32_t grad_dtype, void *dT,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rows sent to their units and brought back.  Row i has k entries e = i k + j
+ * (its units, best first, say); vs_group_rows of the n k entries' ids gives
+ * slot and offsets, and unit g's rows are then rows offsets[g] ..
+ * offsets[g + 1] - 1 of a matrix of m = n k rows in unit order.
+ *   vs_route_rows             Xs[slot[e]] = X[i] for every kept entry e of row
+ *                             i; rows offsets[n_groups] .. m - 1 of Xs, which
+ *                             belong to no unit, are set to zero.
+ *   vs_route_rows_backward    dX[i] = sum over i's kept entries of dXs[slot[e]].
+ *   vs_combine_rows           Y[i] = sum over i's kept entries of weights[e]
+ *                             Ys[slot[e]] (zeros if none is kept).
+ *   vs_combine_rows_backward  dYs[slot[e]] = weights[e] dY[i] (rows of no unit
+ *                             set to zero) and dweights[e] = dY[i] .
+ *                             Ys[slot[e]], 0 for a dropped entry.
+ * X, Y, dX, dY are n x d, Xs, Ys, dXs, dYs m x d, all of `dtype`; weights and
+ * dweights float32[m].  What belongs to a dropped entry is never read.  Sums
+ * are fp32, over j in order, and rounded once.  n k <= 2^31-1, k in [1, 1024],
+ * n_groups in [1, 2^31-2], d in [1, 2^20]; n == 0 is a no-op.  A slot outside
+ * [-1, m) is taken as dropped.  Inputs and outputs must not overlap.
+ */
+int vs_route_rows(const void *X, int64_t n, int32_t d, int32_t dtype, const int32_t *slot,
+                  const int32_t *offsets, int64_t n_groups, int32_t k, void *Xs, void *stream);
+int vs_route_rows_backward(const void *dXs, int64_t n, int32_t d, int32_t dtype,
+                           const int32_t *slot, int32_t k, void *dX, void *stream);
+int vs_combine_rows(const void *Ys, int64_t n, int32_t d, int32_t dtype, const int32_t *slot,
+                    const float *weights, int32_t k, void *Y, void *stream);
+int vs_combine_rows_backward(const void *dY, const void *Ys, int64_t n, int32_t d, int32_t dtype,
+                             const int32_t *slot, const float *weights, const int32_t *offsets,
+                             int64_t n_groups, int32_t k, void *dYs, float *dweights,
+                             void *stream);
+
+/*
+ * A candidate table in 4-bit codes with one scale per group of columns, and
+ * the scores (dot products) of a few queries over it.
+ *   plain form   codes uint8[nc x ceil(d / 2)]: columns 2 b (low half) and
+ *                2 b + 1 of a row in its byte b; scales [nc x ceil(d / group)]
+ *                of scale_dtype (VS_F16 or VS_BF16).  The table's value is
+ *                T[i][k] = scales[i][k / group] (code[i][k] - 8), codes 0 .. 15.
+ *   vs_q4_quantize  codes and scales of a table T (nc x d, `dtype`): s = the
+ *                group's largest magnitude / 7, rounded to the scale type and
+ *                held inside its finite range; code = 8 + T / s rounded to the
+ *                nearest whole number, ties to even, held in -8 .. 7 (8 where
+ *                s is 0, and in the unused half of an odd row's last byte).
+ *   vs_q4_layout the plain form in the order the scores read it (16 rows x
+ *                128 columns to a block, then the scales): out is caller-owned,
+ *                vs_q4_bytes(nc, d, group) bytes, 16-byte aligned.
+ *   vs_q4_scores y[q][i] = x[q] . T[i], float32[nq x nc], from the laid-out
+ *                table; x is nq x d of `dtype`.  Products are exact and sums
+ *                fp32, a group at a time.  Queries are assumed finite, with
+ *                magnitudes below 2^115; a query that is not affects its own
+ *                scores only.  Made for few queries (the table is read once
+ *                for every 16; for every 5 of VS_F32).
+ * group is 32, 64 or 128; nc in [1, 2^31-1], d in [1, 2^20], nq in [0, 2^31-1]
+ * (0: no-op).  vs_q4_bytes returns 0 for invalid sizes.
+ */
+size_t vs_q4_bytes(int64_t nc, int32_t d, int32_t group);
+int vs_q4_quantize(const void *T, int64_t nc, int32_t d, int32_t dtype, int32_t group,
+                   int32_t scale_dtype, uint8_t *codes, void *scales, void *stream);
+int vs_q4_layout(const uint8_t *codes, const void *scales, int64_t nc, int32_t d, int32_t group,
+                 void *out, void *stream);
+int vs_q4_scores(const void *x, int64_t nq, int32_t d, int32_t dtype, const void *table,
+                 int64_t nc, int32_t group, int32_t scale_dtype, float *y, void *stream);
 
 /*
  * Squared L2 norms of candidates, float32, fixed summation order (the same
