@@ -58,31 +58,171 @@ __global__ __launch_bounds__(256) void k_row_lookup(const T *__restrict__ table,
     }
 }
 
+// ---- lookup backward -------------------------------------------------------
+//
+// The sorted order cuts into one run of rows per unit, summed by the lanes of
+// one unit.  Units differ widely in length (padding, common tokens), so one
+// with more than kRun rows is cut at multiples of kRun places: each piece's
+// sum goes to the workspace in fp32 and a second kernel adds a unit's pieces,
+// always in the same order.  A long unit covers the first or the last place
+// of every stretch of kRun places it touches, so a stretch holds at most two
+// pieces: part 0 of the unit at its first place, part 1 of the one at its
+// last if that unit starts inside the stretch.
+constexpr int kRun = 64;
+constexpr int kAhead = 8;        // rows in flight per lane
+constexpr int kJoinWaves = 16;
+
+struct Span {
+    int64_t lo, hi;
+};
+__device__ __forceinline__ Span unit_span(const int32_t *__restrict__ offsets, int64_t g,
+                                          int64_t n) {
+    Span s{offsets[g], offsets[g + 1]};
+    s.lo = s.lo < 0 ? 0 : s.lo;
+    s.hi = s.hi > n ? n : s.hi;
+    return s;
+}
+
+// unit of the entry at place p, or -1
+__device__ __forceinline__ int64_t unit_at(const int32_t *__restrict__ ids,
+                                           const int32_t *__restrict__ order, int64_t p, int64_t n,
+                                           int64_t G) {
+    const int64_t i = order[p];
+    if (i < 0 || i >= n) return -1;
+    const int64_t g = ids[i];
+    return g < G ? g : -1;
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void sum_rows(const T *__restrict__ dY, int64_t n, int32_t d,
+                                         const int32_t *__restrict__ order, Span s, int c,
+                                         float (&acc)[N]) {
+    using V = Vec<T, N>;
+    int64_t p = s.lo;
+    for (; p + kAhead <= s.hi; p += kAhead) {
+        V v[kAhead];
+        bool ok[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+            const int64_t i = order[p + a];
+            ok[a] = i >= 0 && i < n;
+            v[a] = reinterpret_cast<const V *>(dY + (ok[a] ? i : 0) * d)[c];
+        }
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+            for (int t = 0; t < N; ++t) acc[t] += ok[a] ? widen(v[a].v[t]) : 0.0f;
+    }
+    for (; p < s.hi; ++p) {
+        const int64_t i = order[p];
+        if (i < 0 || i >= n) continue;
+        const V v = reinterpret_cast<const V *>(dY + i * d)[c];
+#pragma unroll
+        for (int t = 0; t < N; ++t) acc[t] += widen(v.v[t]);
+    }
+}
+
+template <typename O, int N>
+__device__ __forceinline__ void store_row(O *__restrict__ dT, int64_t g, int32_t d, int c,
+                                          float scale, const float (&acc)[N]) {
+    Vec<O, N> o;
+#pragma unroll
+    for (int t = 0; t < N; ++t) o.v[t] = narrow<O>(scale * acc[t]);
+    reinterpret_cast<Vec<O, N> *>(dT + g * d)[c] = o;
+}
+
+// Workgroups 0 .. piece_blocks - 1 sum the pieces of long units, the others
+// the short units; blockIdx.y is the block of columns.
 template <typename T, typename O, int N>
 __global__ __launch_bounds__(256) void k_row_lookup_bwd(
-    const T *__restrict__ dY, int64_t n, int32_t d, const int32_t *__restrict__ order,
-    const int32_t *__restrict__ offsets, int64_t G, float scale, O *__restrict__ dT, int lsh) {
+    const T *__restrict__ dY, int64_t n, int32_t d, const int32_t *__restrict__ ids,
+    const int32_t *__restrict__ order, const int32_t *__restrict__ offsets, int64_t G, float scale,
+    O *__restrict__ dT, float *__restrict__ part, unsigned piece_blocks, int lsh) {
     const int lane = threadIdx.x & ((1 << lsh) - 1);
-    const int64_t step = (int64_t)gridDim.x * (256 >> lsh);
-    const int vecs = d / N;
-    for (int64_t g = (int64_t)blockIdx.x * (256 >> lsh) + (threadIdx.x >> lsh); g < G; g += step) {
-        int64_t lo = offsets[g], hi = offsets[g + 1];
-        lo = lo < 0 ? 0 : lo;
-        hi = hi > n ? n : hi;
-        for (int c = lane; c < vecs; c += 1 << lsh) {
-            float acc[N] = {};
-            for (int64_t p = lo; p < hi; ++p) {
-                const int64_t i = order[p];
-                if (i < 0 || i >= n) continue;
-                const Vec<T, N> v = reinterpret_cast<const Vec<T, N> *>(dY + i * d)[c];
+    const int per = 256 >> lsh;
+    const int c = ((int)blockIdx.y << lsh) + lane;
+    if (c >= d / N) return;
+    if (blockIdx.x < piece_blocks) {
+        int64_t kept = offsets[G];
+        kept = kept > n ? n : kept;
+        const int64_t step = (int64_t)piece_blocks * per;
+        for (int64_t s = (int64_t)blockIdx.x * per + (threadIdx.x >> lsh); s * kRun < kept;
+             s += step) {
+            const int64_t p0 = s * kRun, p1 = p0 + kRun < kept ? p0 + kRun : kept;
+            const int64_t g0 = unit_at(ids, order, p0, n, G);
+            const int64_t g1 = unit_at(ids, order, p1 - 1, n, G);
+            for (int b = 0; b < 2; ++b) {
+                const int64_t g = b ? g1 : g0;
+                if (g < 0 || (b && g1 == g0)) continue;
+                Span u = unit_span(offsets, g, n);
+                if (u.hi - u.lo <= kRun) continue;
+                u.lo = u.lo > p0 ? u.lo : p0;
+                u.hi = u.hi < p1 ? u.hi : p1;
+                float acc[N] = {};
+                sum_rows<T, N>(dY, n, d, order, u, c, acc);
+                Vec<float, N> o;
 #pragma unroll
-                for (int t = 0; t < N; ++t) acc[t] += widen(v.v[t]);
+                for (int t = 0; t < N; ++t) o.v[t] = acc[t];
+                reinterpret_cast<Vec<float, N> *>(part + (2 * s + b) * d)[c] = o;
             }
-            Vec<O, N> o;
-#pragma unroll
-            for (int t = 0; t < N; ++t) o.v[t] = narrow<O>(scale * acc[t]);
-            reinterpret_cast<Vec<O, N> *>(dT + g * d)[c] = o;
         }
+        return;
+    }
+    const int64_t step = (int64_t)(gridDim.x - piece_blocks) * per;
+    for (int64_t g = (int64_t)(blockIdx.x - piece_blocks) * per + (threadIdx.x >> lsh); g < G;
+         g += step) {
+        const Span u = unit_span(offsets, g, n);
+        if (u.hi - u.lo > kRun) continue;
+        float acc[N] = {};
+        sum_rows<T, N>(dY, n, d, order, u, c, acc);
+        store_row<O, N>(dT, g, d, c, scale, acc);
+    }
+}
+
+// One workgroup per stretch in which a long unit starts: its waves take the
+// unit's pieces in turn, and the waves' sums are added in their order.
+template <typename O, int N>
+__global__ __launch_bounds__(kJoinWaves * 64) void k_row_lookup_join(
+    int64_t n, int32_t d, const int32_t *__restrict__ ids, const int32_t *__restrict__ order,
+    const int32_t *__restrict__ offsets, int64_t G, float scale, const float *__restrict__ part,
+    O *__restrict__ dT) {
+    using V = Vec<float, N>;
+    __shared__ V sums[kJoinWaves][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+    const int c = (int)blockIdx.y * 64 + lane;
+    const bool in = c < d / N;
+    int64_t kept = offsets[G];
+    kept = kept > n ? n : kept;
+    for (int64_t s = blockIdx.x; s * kRun < kept; s += gridDim.x) {
+        const int64_t p0 = s * kRun, p1 = p0 + kRun < kept ? p0 + kRun : kept;
+        const int64_t g = unit_at(ids, order, p1 - 1, n, G);
+        if (g < 0) continue;  // uniform over the workgroup, as are the next two
+        const Span u = unit_span(offsets, g, n);
+        if (u.hi - u.lo <= kRun || u.lo < p0 || u.lo >= p1) continue;
+        const int64_t last = (u.hi - 1) / kRun;
+        V sum;
+#pragma unroll
+        for (int t = 0; t < N; ++t) sum.v[t] = 0.0f;
+        if (in)
+#pragma unroll 4
+            for (int64_t q = s + w; q <= last; q += kJoinWaves) {
+                const int64_t slot = 2 * q + (q == s && u.lo > p0 ? 1 : 0);
+                const V v = reinterpret_cast<const V *>(part + slot * d)[c];
+#pragma unroll
+                for (int t = 0; t < N; ++t) sum.v[t] += v.v[t];
+            }
+        sums[w][lane] = sum;
+        __syncthreads();
+        if (w == 0 && in) {
+            float acc[N];
+#pragma unroll
+            for (int t = 0; t < N; ++t) {
+                acc[t] = sums[0][lane].v[t];
+                for (int v = 1; v < kJoinWaves; ++v) acc[t] += sums[v][lane].v[t];
+            }
+            store_row<O, N>(dT, g, d, c, scale, acc);
+        }
+        __syncthreads();
     }
 }
 
@@ -230,35 +370,56 @@ hipError_t launch_row_lookup(const void *table, int64_t G, int32_t d, int dtype,
     });
 }
 
+// Two fp32 rows per stretch of kRun places.
 size_t row_lookup_bwd_workspace(int64_t n, int32_t d) {
-    (void)n, (void)d;
-    return 256;
+    const size_t stretches = (size_t)((n + kRun - 1) / kRun);
+    return 256 + stretches * 2 * (size_t)d * 4;
+}
+
+template <typename T, typename O, int N>
+static hipError_t lookup_bwd(const void *dY, int64_t n, int32_t d, const int32_t *ids,
+                             const int32_t *order, const int32_t *offsets, int64_t G, float scale,
+                             void *dT, float *part, hipStream_t st, int n_cu) {
+    const int vecs = d / N;
+    int lsh = 0;
+    while (lsh < 6 && (1 << lsh) < vecs) ++lsh;
+    const int per = 256 >> lsh;
+    const unsigned cols = (unsigned)((vecs + (1 << lsh) - 1) >> lsh);
+    const int64_t stretches = (n + kRun - 1) / kRun, most = (int64_t)n_cu * 32;
+    const int64_t pb = (stretches + per - 1) / per, ub = (G + per - 1) / per;
+    const unsigned pieces = (unsigned)(pb < most ? pb : most);
+    const unsigned units = (unsigned)(ub < most ? ub : most);
+    timing_before(st, "k_row_lookup_bwd");
+    hipLaunchKernelGGL((k_row_lookup_bwd<T, O, N>), dim3(pieces + units, cols), dim3(256), 0, st,
+                       (const T *)dY, n, d, ids, order, offsets, G, scale, (O *)dT, part, pieces,
+                       lsh);
+    timing_after(st);
+    if (n > kRun) {  // else no unit is long
+        const unsigned jc = (unsigned)((vecs + 63) / 64);
+        hipLaunchKernelGGL((k_row_lookup_join<O, N>),
+                           dim3((unsigned)(stretches < most ? stretches : most), jc),
+                           dim3(kJoinWaves * 64), 0, st, n, d, ids, order, offsets, G, scale, part,
+                           (O *)dT);
+    }
+    return hipGetLastError();
 }
 
 hipError_t launch_row_lookup_bwd(const void *dY, int64_t n, int32_t d, int dtype,
                                  const int32_t *ids, const int32_t *order, const int32_t *offsets,
                                  int64_t G, float scale, int grad_dtype, void *dT, void *ws,
                                  hipStream_t st, int n_cu) {
-    (void)ids, (void)ws;
     // one vector length for both sides: the shorter of what each allows
     int nv = vec_elems(d, dtype_bytes(dtype), addr(dY));
     const int no = vec_elems(d, dtype_bytes(grad_dtype), addr(dT));
     if (no < nv) nv = no;
-    const RowGrid g = row_grid(G, d / nv, n_cu);
     return with_type(dtype, nv, [&](auto t, auto nc) {
         using T = decltype(t);
         constexpr int N = decltype(nc)::value;
-        timing_before(st, "k_row_lookup_bwd");
         if (grad_dtype == dtype)
-            hipLaunchKernelGGL((k_row_lookup_bwd<T, T, N>), dim3(g.grid), dim3(256), 0, st,
-                               (const T *)dY, n, d, order, offsets, G, scale, (T *)dT,
-                               g.log2_lanes);
-        else
-            hipLaunchKernelGGL((k_row_lookup_bwd<T, float, N>), dim3(g.grid), dim3(256), 0, st,
-                               (const T *)dY, n, d, order, offsets, G, scale, (float *)dT,
-                               g.log2_lanes);
-        timing_after(st);
-        return hipGetLastError();
+            return lookup_bwd<T, T, N>(dY, n, d, ids, order, offsets, G, scale, dT, (float *)ws,
+                                       st, n_cu);
+        return lookup_bwd<T, float, N>(dY, n, d, ids, order, offsets, G, scale, dT, (float *)ws,
+                                       st, n_cu);
     });
 }
 
