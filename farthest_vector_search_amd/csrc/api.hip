@@ -1194,7 +1194,7 @@ VS_API int vs_q4_scores(const void *x, int64_t nq, int32_t d, int32_t dtype, con
     int n_cu = 0;
     if (const int s = device_ready(&n_cu)) return s;
     VS_TRY_HIP(vs::launch_q4_scores(x, nq, d, dtype, table, nc, group, scale_dtype, y,
-                                    reinterpret_cast<hipStream_t>(stream)));
+                                    reinterpret_cast<hipStream_t>(stream), n_cu));
     return VS_OK;
 }
 

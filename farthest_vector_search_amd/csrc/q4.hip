@@ -179,39 +179,214 @@ __device__ __forceinline__ uint32_t bf16_piece(float x, int p) {
     return __float_as_uint(r) >> 16;
 }
 
-// Columns k .. k + 7 of query q as one lane's operand (zeros past the query).
+// Columns k .. k + 7 of query q as one lane's operand, zeros past the query
+// and for q >= nq.  wide: queries start on 16-byte boundaries and d % 8 == 0.
 template <typename X>
 __device__ __forceinline__ Frag query_frag(const X *__restrict__ x, int64_t nq, int32_t d,
-                                           int64_t q, int piece, int64_t k) {
+                                           int64_t q, int piece, int64_t k, bool wide) {
     Frag f;
-    const X *row = x + q * d;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f.u[j] = 0;
+    if (q >= nq || k >= d) return f;
+    Vec<X, 8> v;
+    const X *row = x + q * d + k;
+    if (wide) {
+        using W = Vec<X, 16 / sizeof(X)>;
+        W *to = reinterpret_cast<W *>(&v);
+#pragma unroll
+        for (int j = 0; j < (int)(8 / (16 / sizeof(X))); ++j)
+            to[j] = reinterpret_cast<const W *>(row)[j];
+    } else {
+        const int last = (int)(d - 1 - k);  // >= 0
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v.v[e] = row[e < last ? e : last];
+#pragma unroll
+        for (int e = 1; e < 8; ++e)
+            if (e > last) v.v[e] = X(0.0f);
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        uint32_t h = 0;
-        if (q < nq && k + e < d) {
-            if constexpr (std::is_same<X, float>::value) {
-                h = bf16_piece(row[k + e], piece);
-            } else {
-                h = reinterpret_cast<const uint16_t *>(row)[k + e];
-            }
+        uint32_t h;
+        if constexpr (std::is_same<X, float>::value) {
+            h = bf16_piece(v.v[e], piece);
+        } else {
+            uint16_t raw;
+            __builtin_memcpy(&raw, &v.v[e], 2);
+            h = raw;
         }
-        if (e & 1) f.u[e >> 1] |= h << 16;
-        else f.u[e >> 1] = h;
+        f.u[e >> 1] |= h << (16 * (e & 1));
     }
     return f;
 }
 
+// One block's codes and scales as a lane holds them.
+template <typename S, int PER>
+struct Block {
+    uint4 a;
+    Vec<S, 4 * PER> s;
+    __device__ __forceinline__ void load(const uint4 *__restrict__ codes,
+                                         const S *__restrict__ scales, int64_t blk, int lane) {
+        a = codes[blk * 64 + lane];
+        s = reinterpret_cast<const Vec<S, 4 * PER> *>(scales)[blk * 4 + (lane >> 4)];
+    }
+};
+
+// Many rows: a workgroup of 16 waves takes a run of row blocks, whose blocks
+// lie one behind the other, and cuts that stream into 16 equal segments, so
+// waves differ by less than a row block whatever the table's shape.  The
+// queries are staged once, in operand order, in LDS; each wave then streams
+// its segment with kBlocksAhead blocks in flight and no barrier.  A row block
+// cut by a segment's border is finished by the wave that began it, from the
+// parts (heads) the next waves leave in LDS, added in their order.
+constexpr int kStreamWaves = 16;
+constexpr int kBlocksAhead = 4;
+
+template <typename X, typename S, int GROUP, int NT>
+__global__ __launch_bounds__(kStreamWaves * 64) void k_q4_scores_stream(
+    const X *__restrict__ x, int64_t nq, int64_t nc, int32_t d, int64_t nrb, int32_t ncb,
+    const uint4 *__restrict__ codes, const S *__restrict__ scales, float *__restrict__ y,
+    int32_t rows_per, int wide) {
+    using F = Form<X>;
+    using A = typename F::A;
+    constexpr int QT = 16 / F::pieces;
+    constexpr int PER = kBlockCols / GROUP;
+    extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
+    Frag *frags = reinterpret_cast<Frag *>(lds);  // [4 ncb][NT][64]
+    f32x4 *heads = reinterpret_cast<f32x4 *>(frags + (size_t)ncb * 4 * NT * 64);  // [wave][NT][64]
+
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int col = lane & 15, part = lane >> 4;
+    const int64_t r0 = (int64_t)blockIdx.x * rows_per;
+    const int64_t r1 = r0 + rows_per < nrb ? r0 + rows_per : nrb;
+    const int32_t total = (int32_t)(r1 - r0) * ncb;
+    const int32_t seg = (total + kStreamWaves - 1) / kStreamWaves;
+    const int32_t b0 = seg * w < total ? seg * w : total;
+    const int32_t b1 = b0 + seg < total ? b0 + seg : total;
+    const int64_t base = r0 * ncb;
+    const int64_t q0 = (int64_t)blockIdx.y * NT * QT;
+
+    Block<S, PER> buf[kBlocksAhead];
+    if (b0 < b1)
+#pragma unroll
+        for (int u = 0; u < kBlocksAhead; ++u)
+            buf[u].load(codes, scales, base + (b0 + u < b1 ? b0 + u : b1 - 1), lane);
+
+    for (int i = threadIdx.x; i < ncb * 4 * NT * 64; i += kStreamWaves * 64) {
+        const int l = i & 63, ct = (i >> 6) % NT, t = (i >> 6) / NT;
+        const int c = l & 15;
+        const int64_t q = c < QT * F::pieces ? q0 + ct * QT + c % QT : nq;
+        frags[i] = query_frag(x, nq, d, q, c / QT, 32 * (int64_t)t + 8 * (l >> 4), wide != 0);
+    }
+    __syncthreads();
+
+    Frag m24;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m24.u[j] = F::minus24;
+    f32x4 acc[NT];
+#pragma unroll
+    for (int ct = 0; ct < NT; ++ct) acc[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // scores of 16 rows: a query's pieces added smallest first
+    auto store = [&](int64_t rb) {
+#pragma unroll
+        for (int ct = 0; ct < NT; ++ct) {
+            f32x4 v = acc[ct];
+            if constexpr (F::pieces == 3) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float mid = __shfl(acc[ct][r], lane + QT), lo = __shfl(acc[ct][r], lane + 2 * QT);
+                    v[r] += mid + lo;
+                }
+            }
+            const int64_t q = q0 + ct * QT + col, row = rb * kBlockRows + 4 * part;
+            if (col < QT && q < nq) {
+                float *to = y + q * nc + row;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (row + r < nc) to[r] = v[r];
+            }
+        }
+    };
+    auto clear = [&]() {
+#pragma unroll
+        for (int ct = 0; ct < NT; ++ct) acc[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    auto leave_head = [&]() {
+#pragma unroll
+        for (int ct = 0; ct < NT; ++ct) heads[(w * NT + ct) * 64 + lane] = acc[ct];
+    };
+
+    int32_t rb = b0 / ncb, cb = b0 - rb * ncb;  // row block inside the run
+    bool head = cb != 0;
+    for (int32_t b = b0; b < b1; b += kBlocksAhead) {
+#pragma unroll
+        for (int u = 0; u < kBlocksAhead; ++u) {
+            if (b + u >= b1) break;
+            const Block<S, PER> now = buf[u];
+            const int32_t next = b + u + kBlocksAhead;
+            buf[u].load(codes, scales, base + (next < b1 ? next : b1 - 1), lane);
+            const uint32_t a[4] = {now.a.x, now.a.y, now.a.z, now.a.w};
+            const Frag *fr = frags + (size_t)cb * 4 * NT * 64 + lane;
+#pragma unroll
+            for (int g = 0; g < PER; ++g) {
+                f32x4 c[NT];
+#pragma unroll
+                for (int ct = 0; ct < NT; ++ct) c[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int s = 0; s < GROUP / 32; ++s) {
+                    const int t = g * (GROUP / 32) + s;
+                    const Frag e = expand<F>(a[t]);
+#pragma unroll
+                    for (int ct = 0; ct < NT; ++ct) {
+                        const Frag q = fr[(t * NT + ct) * 64];
+                        c[ct] = F::mul(frag_as<A>(m24), frag_as<A>(q), c[ct]);
+                        c[ct] = F::mul(frag_as<A>(e), frag_as<A>(q), c[ct]);
+                    }
+                }
+#pragma unroll
+                for (int ct = 0; ct < NT; ++ct)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[ct][r] = __builtin_fmaf(widen(now.s.v[4 * g + r]), c[ct][r], acc[ct][r]);
+            }
+            if (++cb == ncb) {
+                if (head) leave_head();
+                else store(r0 + rb);
+                head = false;
+                clear();
+                cb = 0;
+                ++rb;
+            }
+        }
+    }
+    const bool open = b0 < b1 && cb != 0;  // the segment ends inside a row block
+    if (open && head) leave_head();
+    __syncthreads();
+    if (open && !head) {
+        const int32_t end = (rb + 1) * ncb;
+        for (int v = w + 1; v < kStreamWaves && seg * v < end; ++v)
+#pragma unroll
+            for (int ct = 0; ct < NT; ++ct) acc[ct] += heads[(v * NT + ct) * 64 + lane];
+        store(r0 + rb);
+    }
+}
+
+// Wide queries whose operands do not fit in LDS: a workgroup per row block and
+// tile of columns, its waves taking the row block's blocks in turn and the
+// queries straight from memory.
+constexpr int kWideWaves = 16;
+
 template <typename X, typename S, int GROUP>
-__global__ __launch_bounds__(256) void k_q4_scores(const X *__restrict__ x, int64_t nq, int64_t nc,
-                                                   int32_t d, int64_t nrb, int64_t ncb,
-                                                   const uint4 *__restrict__ codes,
-                                                   const S *__restrict__ scales,
-                                                   float *__restrict__ y) {
+__global__ __launch_bounds__(kWideWaves * 64) void k_q4_scores_wide(
+    const X *__restrict__ x, int64_t nq, int64_t nc, int32_t d, int64_t nrb, int64_t ncb,
+    const uint4 *__restrict__ codes, const S *__restrict__ scales, float *__restrict__ y,
+    int wide) {
     using F = Form<X>;
     using A = typename F::A;
     constexpr int QT = 16 / F::pieces;     // queries per tile of columns
     constexpr int PER = kBlockCols / GROUP;  // groups per block
-    __shared__ float red[4][16][17];
+    __shared__ float red[kWideWaves][16][17];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, waves = blockDim.x >> 6;
     const int col = lane & 15, part = lane >> 4;
     const int64_t tiles = (nq + QT - 1) / QT;
@@ -226,9 +401,9 @@ __global__ __launch_bounds__(256) void k_q4_scores(const X *__restrict__ x, int6
             f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
             for (int64_t cb = w; cb < ncb; cb += waves) {
                 const int64_t blk = rb * ncb + cb;
-                const uint4 a4 = codes[blk * 64 + lane];
-                const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w};
-                const S *sp = scales + (blk * 4 + part) * (4 * PER);
+                Block<S, PER> now;
+                now.load(codes, scales, blk, lane);
+                const uint32_t a[4] = {now.a.x, now.a.y, now.a.z, now.a.w};
 #pragma unroll
                 for (int g = 0; g < PER; ++g) {
                     f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -236,13 +411,14 @@ __global__ __launch_bounds__(256) void k_q4_scores(const X *__restrict__ x, int6
                     for (int s = 0; s < GROUP / 32; ++s) {
                         const int t = g * (GROUP / 32) + s;
                         const Frag b = query_frag(x, nq, d, q, piece,
-                                                  cb * kBlockCols + 32 * t + 8 * part);
+                                                  cb * kBlockCols + 32 * t + 8 * part,
+                                                  wide != 0);
                         c = F::mul(frag_as<A>(m24), frag_as<A>(b), c);
                         c = F::mul(frag_as<A>(expand<F>(a[t])), frag_as<A>(b), c);
                     }
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        acc[r] = __builtin_fmaf(widen(sp[4 * g + r]), c[r], acc[r]);
+                        acc[r] = __builtin_fmaf(widen(now.s.v[4 * g + r]), c[r], acc[r]);
                 }
             }
 #pragma unroll
@@ -251,7 +427,7 @@ __global__ __launch_bounds__(256) void k_q4_scores(const X *__restrict__ x, int6
             for (int o = threadIdx.x; o < QT * 16; o += blockDim.x) {
                 const int r = o & 15, qq = o >> 4;
                 float sum = 0.0f;
-                for (int p = 0; p < F::pieces; ++p)
+                for (int p = F::pieces - 1; p >= 0; --p)
                     for (int v = 0; v < waves; ++v) sum += red[v][qq + p * QT][r];
                 const int64_t row = rb * kBlockRows + r, query = ct * QT + qq;
                 if (row < nc && query < nq) y[query * nc + row] = sum;
@@ -260,39 +436,77 @@ __global__ __launch_bounds__(256) void k_q4_scores(const X *__restrict__ x, int6
         }
 }
 
-template <typename X, typename S>
-hipError_t scores_group(const X *x, int64_t nq, int32_t d, const void *table, int64_t nc,
-                        int group, float *y, hipStream_t st) {
+constexpr size_t kLds = 160 * 1024;
+
+// LDS of the streaming kernel with nt tiles of columns
+size_t stream_lds(int64_t ncb, int nt) {
+    return ((size_t)ncb * 4 + kStreamWaves) * (size_t)nt * 1024;
+}
+
+template <typename X, typename S, int GROUP, int NT>
+void launch_stream(const X *x, int64_t nq, int32_t d, const uint4 *codes, const S *scales,
+                   int64_t nc, float *y, int wide, hipStream_t st, int n_cu) {
+    const int64_t nrb = row_blocks(nc), ncb = col_blocks(d);
+    constexpr int QT = 16 / Form<X>::pieces;
+    // a run of row blocks per CU, of fewer than 2^30 blocks
+    int64_t per = (nrb + n_cu - 1) / n_cu;
+    const int64_t most = (int64_t(1) << 30) / ncb;
+    if (per > most) per = most;
+    const int64_t cols = (nq + (int64_t)NT * QT - 1) / ((int64_t)NT * QT);
+    for (int64_t c = 0; c < cols; c += 65535) {  // the grid's limit in y
+        const int64_t cn = cols - c < 65535 ? cols - c : 65535, q = c * NT * QT;
+        hipLaunchKernelGGL((k_q4_scores_stream<X, S, GROUP, NT>),
+                           dim3((unsigned)((nrb + per - 1) / per), (unsigned)cn),
+                           dim3(kStreamWaves * 64), stream_lds(ncb, NT), st, x + q * d, nq - q, nc,
+                           d, nrb, (int32_t)ncb, codes, scales, y + q * nc, (int32_t)per, wide);
+    }
+}
+
+template <typename X, typename S, int GROUP>
+hipError_t scores_group(const X *x, int64_t nq, int32_t d, const void *table, int64_t nc, float *y,
+                        hipStream_t st, int n_cu) {
     const int64_t nrb = row_blocks(nc), ncb = col_blocks(d);
     const uint4 *codes = static_cast<const uint4 *>(table);
     const S *scales = reinterpret_cast<const S *>(codes + nrb * ncb * 64);
-    const int64_t tiles = (nq * Form<X>::pieces + 15) / 16;
-    const dim3 grid((unsigned)(nrb < (1 << 20) ? nrb : 1 << 20), (unsigned)(tiles < 64 ? tiles : 64));
-    const dim3 block(64 * (unsigned)(ncb < 4 ? ncb : 4));
+    const int wide = d % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0;
+    constexpr int QT = 16 / Form<X>::pieces;
+    const int64_t tiles = (nq + QT - 1) / QT;
     timing_before(st, "k_q4_scores");
-    switch (group) {
-    case 32:
-        hipLaunchKernelGGL((k_q4_scores<X, S, 32>), grid, block, 0, st, x, nq, nc, d, nrb, ncb,
-                           codes, scales, y);
-        break;
-    case 64:
-        hipLaunchKernelGGL((k_q4_scores<X, S, 64>), grid, block, 0, st, x, nq, nc, d, nrb, ncb,
-                           codes, scales, y);
-        break;
-    default:
-        hipLaunchKernelGGL((k_q4_scores<X, S, 128>), grid, block, 0, st, x, nq, nc, d, nrb, ncb,
-                           codes, scales, y);
+    // the table is read once per launch row of column tiles: as many tiles as
+    // the queries need and LDS holds
+    if (tiles > 2 && stream_lds(ncb, 4) <= kLds)
+        launch_stream<X, S, GROUP, 4>(x, nq, d, codes, scales, nc, y, wide, st, n_cu);
+    else if (tiles > 1 && stream_lds(ncb, 2) <= kLds)
+        launch_stream<X, S, GROUP, 2>(x, nq, d, codes, scales, nc, y, wide, st, n_cu);
+    else if (stream_lds(ncb, 1) <= kLds)
+        launch_stream<X, S, GROUP, 1>(x, nq, d, codes, scales, nc, y, wide, st, n_cu);
+    else {
+        const dim3 grid((unsigned)(nrb < (1 << 20) ? nrb : 1 << 20),
+                        (unsigned)(tiles < 64 ? tiles : 64));
+        const dim3 block(64 * (unsigned)(ncb < kWideWaves ? ncb : kWideWaves));
+        hipLaunchKernelGGL((k_q4_scores_wide<X, S, GROUP>), grid, block, 0, st, x, nq, nc, d, nrb,
+                           ncb, codes, scales, y, wide);
     }
     timing_after(st);
     return hipGetLastError();
 }
 
+template <typename X, typename S>
+hipError_t scores_type(const X *x, int64_t nq, int32_t d, const void *table, int64_t nc, int group,
+                       float *y, hipStream_t st, int n_cu) {
+    switch (group) {
+    case 32: return scores_group<X, S, 32>(x, nq, d, table, nc, y, st, n_cu);
+    case 64: return scores_group<X, S, 64>(x, nq, d, table, nc, y, st, n_cu);
+    default: return scores_group<X, S, 128>(x, nq, d, table, nc, y, st, n_cu);
+    }
+}
+
 template <typename X>
 hipError_t scores_scale(const void *x, int64_t nq, int32_t d, const void *table, int64_t nc,
-                        int group, int scale_dtype, float *y, hipStream_t st) {
+                        int group, int scale_dtype, float *y, hipStream_t st, int n_cu) {
     if (scale_dtype == kF16)
-        return scores_group<X, _Float16>((const X *)x, nq, d, table, nc, group, y, st);
-    return scores_group<X, __bf16>((const X *)x, nq, d, table, nc, group, y, st);
+        return scores_type<X, _Float16>((const X *)x, nq, d, table, nc, group, y, st, n_cu);
+    return scores_type<X, __bf16>((const X *)x, nq, d, table, nc, group, y, st, n_cu);
 }
 
 template <typename T>
@@ -338,11 +552,12 @@ hipError_t launch_q4_layout(const uint8_t *codes, const void *scales, int64_t nc
 }
 
 hipError_t launch_q4_scores(const void *x, int64_t nq, int32_t d, int dtype, const void *table,
-                            int64_t nc, int group, int scale_dtype, float *y, hipStream_t st) {
+                            int64_t nc, int group, int scale_dtype, float *y, hipStream_t st,
+                            int n_cu) {
     switch (dtype) {
-    case kF32: return scores_scale<float>(x, nq, d, table, nc, group, scale_dtype, y, st);
-    case kF16: return scores_scale<_Float16>(x, nq, d, table, nc, group, scale_dtype, y, st);
-    default: return scores_scale<__bf16>(x, nq, d, table, nc, group, scale_dtype, y, st);
+    case kF32: return scores_scale<float>(x, nq, d, table, nc, group, scale_dtype, y, st, n_cu);
+    case kF16: return scores_scale<_Float16>(x, nq, d, table, nc, group, scale_dtype, y, st, n_cu);
+    default: return scores_scale<__bf16>(x, nq, d, table, nc, group, scale_dtype, y, st, n_cu);
     }
 }
 

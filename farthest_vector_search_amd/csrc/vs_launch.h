@@ -152,7 +152,8 @@ hipError_t launch_q4_quantize(const void *table, int64_t nc, int32_t d, int dtyp
 hipError_t launch_q4_layout(const uint8_t *codes, const void *scales, int64_t nc, int32_t d,
                             int group, void *out, hipStream_t st, int n_cu);
 hipError_t launch_q4_scores(const void *x, int64_t nq, int32_t d, int dtype, const void *table,
-                            int64_t nc, int group, int scale_dtype, float *y, hipStream_t st);
+                            int64_t nc, int group, int scale_dtype, float *y, hipStream_t st,
+                            int n_cu);
 
 // Timing hook (api.hip).
 void timing_before(hipStream_t st, const char *name);

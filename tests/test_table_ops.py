@@ -397,7 +397,8 @@ SCORE_CASES = [
     (1, 1, 1, 32), (1, 17, 33, 32), (3, 100, 128, 64), (5, 333, 767, 64), (16, 64, 256, 128),
     (6, 31, 300, 32), (17, 50, 130, 128), (33, 1000, 96, 32), (2, 40, 4096, 128),
     (1, 5000, 256, 32), (16, 48, 1111, 32), (1, 20, 9000, 64), (48, 16, 20000, 128),
-    (11, 129, 4100, 64), (1, 3, 70000, 32),
+    (11, 129, 4100, 64), (1, 3, 70000, 32), (7, 20011, 200, 32), (16, 30000, 640, 64),
+    (40, 9000, 250, 128), (2, 70000, 96, 64), (1, 300, 4096, 32),
 ]
 
 
