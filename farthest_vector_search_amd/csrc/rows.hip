@@ -70,7 +70,7 @@ __global__ __launch_bounds__(256) void k_row_lookup(const T *__restrict__ table,
 // last if that unit starts inside the stretch.
 constexpr int kRun = 64;
 constexpr int kAhead = 8;        // rows in flight per lane
-constexpr int kJoinWaves = 16;
+constexpr int kJoinWaves = 4;
 
 struct Span {
     int64_t lo, hi;
@@ -93,33 +93,44 @@ __device__ __forceinline__ int64_t unit_at(const int32_t *__restrict__ ids,
     return g < G ? g : -1;
 }
 
+// C rows at places p .. p + C - 1, all loads issued before the first use (an
+// index that does not fit loads row 0 and adds nothing)
+template <typename T, int N, int C>
+__device__ __forceinline__ void add_rows(const T *__restrict__ dY, int64_t n, int32_t d,
+                                         const int32_t *__restrict__ order, int64_t p, int c,
+                                         float (&acc)[N]) {
+    using V = Vec<T, N>;
+    V v[C];
+    bool ok[C];
+#pragma unroll
+    for (int a = 0; a < C; ++a) {
+        const int64_t i = order[p + a];
+        ok[a] = i >= 0 && i < n;
+        v[a] = reinterpret_cast<const V *>(dY + (ok[a] ? i : 0) * d)[c];
+    }
+#pragma unroll
+    for (int a = 0; a < C; ++a)
+#pragma unroll
+        for (int t = 0; t < N; ++t) acc[t] += ok[a] ? widen(v[a].v[t]) : 0.0f;
+}
+
 template <typename T, int N>
 __device__ __forceinline__ void sum_rows(const T *__restrict__ dY, int64_t n, int32_t d,
                                          const int32_t *__restrict__ order, Span s, int c,
                                          float (&acc)[N]) {
-    using V = Vec<T, N>;
     int64_t p = s.lo;
-    for (; p + kAhead <= s.hi; p += kAhead) {
-        V v[kAhead];
-        bool ok[kAhead];
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-            const int64_t i = order[p + a];
-            ok[a] = i >= 0 && i < n;
-            v[a] = reinterpret_cast<const V *>(dY + (ok[a] ? i : 0) * d)[c];
-        }
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a)
-#pragma unroll
-            for (int t = 0; t < N; ++t) acc[t] += ok[a] ? widen(v[a].v[t]) : 0.0f;
+    for (; p + kAhead <= s.hi; p += kAhead) add_rows<T, N, kAhead>(dY, n, d, order, p, c, acc);
+    static_assert(kAhead == 8, "the rest is at most 4 + 2 + 1 rows");
+    const int64_t left = s.hi - p;  // negative for a span that holds nothing
+    if (left >= 4) {
+        add_rows<T, N, 4>(dY, n, d, order, p, c, acc);
+        p += 4;
     }
-    for (; p < s.hi; ++p) {
-        const int64_t i = order[p];
-        if (i < 0 || i >= n) continue;
-        const V v = reinterpret_cast<const V *>(dY + i * d)[c];
-#pragma unroll
-        for (int t = 0; t < N; ++t) acc[t] += widen(v.v[t]);
+    if (p + 2 <= s.hi) {
+        add_rows<T, N, 2>(dY, n, d, order, p, c, acc);
+        p += 2;
     }
+    if (p < s.hi) add_rows<T, N, 1>(dY, n, d, order, p, c, acc);
 }
 
 template <typename O, int N>
@@ -204,7 +215,7 @@ __global__ __launch_bounds__(kJoinWaves * 64) void k_row_lookup_join(
 #pragma unroll
         for (int t = 0; t < N; ++t) sum.v[t] = 0.0f;
         if (in)
-#pragma unroll 4
+#pragma unroll 8
             for (int64_t q = s + w; q <= last; q += kJoinWaves) {
                 const int64_t slot = 2 * q + (q == s && u.lo > p0 ? 1 : 0);
                 const V v = reinterpret_cast<const V *>(part + slot * d)[c];
@@ -263,7 +274,27 @@ __global__ __launch_bounds__(256) void k_route_rows(const T *__restrict__ X, int
     zero_tail<T, N>(Xs, *kept, m, d, lane, lsh, row, step);
 }
 
-template <typename T, int N>
+// A chunk of a row's entries: places (-1: dropped) and weights, loaded at once.
+template <int KC>
+struct Entries {
+    int64_t p[KC];
+    float w[KC];
+    __device__ __forceinline__ void load(const int32_t *__restrict__ slot,
+                                         const float *__restrict__ weights, int64_t e0, int left,
+                                         int64_t m) {
+#pragma unroll
+        for (int j = 0; j < KC; ++j) {
+            const int64_t q = j < left ? slot[e0 + j] : -1;
+            p[j] = q >= 0 && q < m ? q : -1;
+            w[j] = weights && j < left ? weights[e0 + j] : 1.0f;
+        }
+    }
+    // the row to load: row 0, whose values are not used, for a dropped entry
+    __device__ __forceinline__ int64_t at(int j) const { return p[j] >= 0 ? p[j] : 0; }
+};
+
+// Two vectors of the row and KC of its entries are in flight per lane.
+template <typename T, int N, int KC>
 __global__ __launch_bounds__(256) void k_combine_rows(const T *__restrict__ Ys, int64_t n,
                                                       int32_t d, const int32_t *__restrict__ slot,
                                                       const float *__restrict__ weights, int32_t k,
@@ -272,27 +303,46 @@ __global__ __launch_bounds__(256) void k_combine_rows(const T *__restrict__ Ys, 
     const int lane = threadIdx.x & ((1 << lsh) - 1);
     const int64_t step = (int64_t)gridDim.x * (256 >> lsh);
     const int64_t m = n * k;
-    const int vecs = d / N;
+    const int vecs = d / N, width = 1 << lsh;
     for (int64_t i = (int64_t)blockIdx.x * (256 >> lsh) + (threadIdx.x >> lsh); i < n; i += step) {
-        for (int c = lane; c < vecs; c += 1 << lsh) {
-            float acc[N] = {};
-            for (int j = 0; j < k; ++j) {
-                const int64_t p = slot[i * k + j];
-                if (p < 0 || p >= m) continue;
-                const float w = weights ? weights[i * k + j] : 1.0f;
-                const V v = reinterpret_cast<const V *>(Ys + p * d)[c];
+        Entries<KC> en;
+        en.load(slot, weights, i * k, k, m);
+        for (int c = lane; c < vecs; c += 2 * width) {
+            const int c1 = c + width < vecs ? c + width : c;  // the last one alone: twice
+            float acc[2][N] = {};
+            for (int j0 = 0; j0 < k; j0 += KC) {
+                if (k > KC) en.load(slot, weights, i * k + j0, k - j0, m);
+                V v[2][KC];
 #pragma unroll
-                for (int t = 0; t < N; ++t) acc[t] = __builtin_fmaf(w, widen(v.v[t]), acc[t]);
+                for (int j = 0; j < KC; ++j) {
+                    const V *src = reinterpret_cast<const V *>(Ys + en.at(j) * d);
+                    v[0][j] = src[c];
+                    v[1][j] = src[c1];
+                }
+#pragma unroll
+                for (int j = 0; j < KC; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int t = 0; t < N; ++t) {
+                            const float s = __builtin_fmaf(en.w[j], widen(v[h][j].v[t]), acc[h][t]);
+                            acc[h][t] = en.p[j] >= 0 ? s : acc[h][t];
+                        }
             }
-            V o;
+            V o[2];
 #pragma unroll
-            for (int t = 0; t < N; ++t) o.v[t] = narrow<T>(acc[t]);
-            reinterpret_cast<V *>(Y + i * d)[c] = o;
+            for (int t = 0; t < N; ++t) {
+                o[0].v[t] = narrow<T>(acc[0][t]);
+                o[1].v[t] = narrow<T>(acc[1][t]);
+            }
+            V *dst = reinterpret_cast<V *>(Y + i * d);
+            dst[c] = o[0];
+            if (c1 != c) dst[c1] = o[1];
         }
     }
 }
 
-template <typename T, int N>
+template <typename T, int N, int KC>
 __global__ __launch_bounds__(256) void k_combine_rows_bwd(
     const T *__restrict__ dY, const T *__restrict__ Ys, int64_t n, int32_t d,
     const int32_t *__restrict__ slot, const float *__restrict__ weights,
@@ -305,25 +355,35 @@ __global__ __launch_bounds__(256) void k_combine_rows_bwd(
     const int64_t m = n * k;
     const int vecs = d / N;
     for (int64_t i = row; i < n; i += step) {
-        for (int j = 0; j < k; ++j) {
-            const int64_t p = slot[i * k + j];
-            float dot = 0.0f;
-            if (p >= 0 && p < m) {
-                const float w = weights[i * k + j];
-                for (int c = lane; c < vecs; c += 1 << lsh) {
-                    const V a = reinterpret_cast<const V *>(dY + i * d)[c];
-                    const V b = reinterpret_cast<const V *>(Ys + p * d)[c];
-                    V o;
+        for (int j0 = 0; j0 < k; j0 += KC) {
+            Entries<KC> en;
+            en.load(slot, weights, i * k + j0, k - j0, m);
+            float dot[KC] = {};
+            for (int c = lane; c < vecs; c += 1 << lsh) {
+                const V a = reinterpret_cast<const V *>(dY + i * d)[c];
+                V b[KC];
 #pragma unroll
-                    for (int t = 0; t < N; ++t) {
-                        dot = __builtin_fmaf(widen(a.v[t]), widen(b.v[t]), dot);
-                        o.v[t] = narrow<T>(w * widen(a.v[t]));
+                for (int j = 0; j < KC; ++j)
+                    b[j] = reinterpret_cast<const V *>(Ys + en.at(j) * d)[c];
+#pragma unroll
+                for (int j = 0; j < KC; ++j)
+                    if (en.p[j] >= 0) {
+                        V o;
+#pragma unroll
+                        for (int t = 0; t < N; ++t) {
+                            dot[j] = __builtin_fmaf(widen(a.v[t]), widen(b[j].v[t]), dot[j]);
+                            o.v[t] = narrow<T>(en.w[j] * widen(a.v[t]));
+                        }
+                        reinterpret_cast<V *>(dYs + en.p[j] * d)[c] = o;
                     }
-                    reinterpret_cast<V *>(dYs + p * d)[c] = o;
-                }
             }
-            for (int s = 1; s < 1 << lsh; s <<= 1) dot += __shfl_xor(dot, s);
-            if (lane == 0) dw[i * k + j] = dot;
+#pragma unroll
+            for (int j = 0; j < KC; ++j)
+                for (int s = 1; s < 1 << lsh; s <<= 1) dot[j] += __shfl_xor(dot[j], s);
+            if (lane == 0)
+#pragma unroll
+                for (int j = 0; j < KC; ++j)
+                    if (j0 + j < k) dw[i * k + j0 + j] = dot[j];
         }
     }
     zero_tail<T, N>(dYs, *kept, m, d, lane, lsh, row, step);
@@ -351,6 +411,14 @@ hipError_t with_type(int dtype, int n, F f) {
     }
 }
 
+// f(entries taken at a time) for rows of k entries
+template <typename F>
+hipError_t with_entries(int32_t k, F f) {
+    if (k == 1) return f(std::integral_constant<int, 1>());
+    if (k == 2) return f(std::integral_constant<int, 2>());
+    return f(std::integral_constant<int, 4>());
+}
+
 inline uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
 
 }  // namespace
@@ -376,13 +444,22 @@ size_t row_lookup_bwd_workspace(int64_t n, int32_t d) {
     return 256 + stretches * 2 * (size_t)d * 4;
 }
 
+static int idle_lanes(int vecs, int lsh) {
+    const int lanes = 1 << lsh;
+    return (vecs + lanes - 1) / lanes * lanes - vecs;
+}
+
 template <typename T, typename O, int N>
 static hipError_t lookup_bwd(const void *dY, int64_t n, int32_t d, const int32_t *ids,
                              const int32_t *order, const int32_t *offsets, int64_t G, float scale,
                              void *dT, float *part, hipStream_t st, int n_cu) {
     const int vecs = d / N;
+    // lanes per row: a wave, or half or a quarter of one where that leaves
+    // fewer lanes without a vector in the last block of columns
     int lsh = 0;
     while (lsh < 6 && (1 << lsh) < vecs) ++lsh;
+    for (int less = lsh - 1; vecs > 64 && less >= 4; --less)
+        if (idle_lanes(vecs, less) < idle_lanes(vecs, lsh)) lsh = less;
     const int per = 256 >> lsh;
     const unsigned cols = (unsigned)((vecs + (1 << lsh) - 1) >> lsh);
     const int64_t stretches = (n + kRun - 1) / kRun, most = (int64_t)n_cu * 32;
@@ -444,11 +521,15 @@ hipError_t launch_combine_rows(const void *Ys, int64_t n, int32_t d, int dtype,
     const RowGrid g = row_grid(n, d / nv, n_cu);
     return with_type(dtype, nv, [&](auto t, auto nc) {
         using T = decltype(t);
-        timing_before(st, "k_combine_rows");
-        hipLaunchKernelGGL((k_combine_rows<T, decltype(nc)::value>), dim3(g.grid), dim3(256), 0,
-                           st, (const T *)Ys, n, d, slot, weights, k, (T *)Y, g.log2_lanes);
-        timing_after(st);
-        return hipGetLastError();
+        constexpr int N = decltype(nc)::value;
+        return with_entries(k, [&](auto kc) {
+            timing_before(st, "k_combine_rows");
+            hipLaunchKernelGGL((k_combine_rows<T, N, decltype(kc)::value>), dim3(g.grid),
+                               dim3(256), 0, st, (const T *)Ys, n, d, slot, weights, k, (T *)Y,
+                               g.log2_lanes);
+            timing_after(st);
+            return hipGetLastError();
+        });
     });
 }
 
@@ -459,12 +540,15 @@ hipError_t launch_combine_rows_bwd(const void *dY, const void *Ys, int64_t n, in
     const RowGrid g = row_grid(n, d / nv, n_cu);
     return with_type(dtype, nv, [&](auto t, auto nc) {
         using T = decltype(t);
-        timing_before(st, "k_combine_rows_bwd");
-        hipLaunchKernelGGL((k_combine_rows_bwd<T, decltype(nc)::value>), dim3(g.grid), dim3(256),
-                           0, st, (const T *)dY, (const T *)Ys, n, d, slot, weights, kept, k,
-                           (T *)dYs, dw, g.log2_lanes);
-        timing_after(st);
-        return hipGetLastError();
+        constexpr int N = decltype(nc)::value;
+        return with_entries(k, [&](auto kc) {
+            timing_before(st, "k_combine_rows_bwd");
+            hipLaunchKernelGGL((k_combine_rows_bwd<T, N, decltype(kc)::value>), dim3(g.grid),
+                               dim3(256), 0, st, (const T *)dY, (const T *)Ys, n, d, slot,
+                               weights, kept, k, (T *)dYs, dw, g.log2_lanes);
+            timing_after(st);
+            return hipGetLastError();
+        });
     });
 }
 
