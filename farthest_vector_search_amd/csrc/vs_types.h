@@ -24,6 +24,37 @@ struct alignas(sizeof(T) * N) Vec {
     T v[N];
 };
 
+// Accesses that pass the caches by (each value is used once): what they move
+// would push out what others still need.
+template <int BYTES>
+struct RawBits;
+template <>
+struct RawBits<2> { typedef uint16_t type; };
+template <>
+struct RawBits<4> { typedef uint32_t type; };
+template <>
+struct RawBits<8> { typedef __attribute__((ext_vector_type(2))) uint32_t type; };
+template <>
+struct RawBits<16> { typedef __attribute__((ext_vector_type(4))) uint32_t type; };
+template <>
+struct RawBits<32> { typedef __attribute__((ext_vector_type(8))) uint32_t type; };
+
+template <typename V>
+__device__ __forceinline__ V load_once(const V *p) {
+    using R = typename RawBits<sizeof(V)>::type;
+    const R r = __builtin_nontemporal_load(reinterpret_cast<const R *>(p));
+    V v;
+    __builtin_memcpy(&v, &r, sizeof(V));
+    return v;
+}
+template <typename V>
+__device__ __forceinline__ void store_once(V *p, const V &v) {
+    using R = typename RawBits<sizeof(V)>::type;
+    R r;
+    __builtin_memcpy(&r, &v, sizeof(V));
+    __builtin_nontemporal_store(r, reinterpret_cast<R *>(p));
+}
+
 // Elements per vector access: 16 bytes where every row starts on a 16-byte
 // boundary (the row size and the matrices' addresses allow it), else the
 // largest power of two that does.  `addr` is the or of the addresses.
