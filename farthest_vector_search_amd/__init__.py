@@ -954,11 +954,10 @@ def _dtype(t, name):
 
 
 def _rows_arg(t, name, device=None, dtype=None):
-    """A contiguous matrix of a table operator, on the call's device."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    """The vs_dtype of a table operator's contiguous matrix on the call's device."""
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) torch tensor")
-    _dtype(t.dtype, name)
+    code = _dtype(t.dtype, name)
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 2:
@@ -967,7 +966,7 @@ def _rows_arg(t, name, device=None, dtype=None):
         raise ValueError(f"{name} must be contiguous")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other inputs on {device}")
-    return t
+    return code
 
 
 def _same_dev(t, name, dtype, device):
@@ -975,6 +974,27 @@ def _same_dev(t, name, dtype, device):
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other inputs on {device}")
     return t
+
+
+def _new(t, name, dtype, shape, like):
+    """_out on the device of `like`; the cheaper allocation for its own type."""
+    if t is not None:
+        return _out(t, name, dtype, shape, like.device)
+    if dtype == like.dtype:
+        return like.new_empty(shape)
+    return like.new_empty(shape, dtype=dtype)
+
+
+def _scratch(nbytes: int, like, workspace):
+    """(address, bytes) of the workspace, and the tensor that holds it; none
+    where the call needs none."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0, None
+        ws = like.new_empty(nbytes, dtype=_torch().uint8)
+    else:
+        ws = _workspace(nbytes, like.device, workspace)
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 def vs_group_rows(ids, n_groups: int, order=None, offsets=None, slot=None, workspace=None,
@@ -989,13 +1009,14 @@ def vs_group_rows(ids, n_groups: int, order=None, offsets=None, slot=None, works
     dev = ids.device
     if not 1 <= n_groups <= 2147483646:
         raise VsError(2, "vs_group_rows")
-    order = _out(order, "order", torch.int32, n, dev)
-    offsets = _out(offsets, "offsets", torch.int32, n_groups + 1, dev)
-    slot = _out(slot, "slot", torch.int32, n, dev, want_slot)
-    ws = _workspace(L.vs_group_rows_workspace(n, n_groups), dev, workspace)
+    order = _new(order, "order", torch.int32, (n,), ids)
+    offsets = _new(offsets, "offsets", torch.int32, (n_groups + 1,), ids)
+    if slot is not None or want_slot:
+        slot = _new(slot, "slot", torch.int32, (n,), ids)
+    ws, size, _held = _scratch(L.vs_group_rows_workspace(n, n_groups), ids, workspace)
     with _on(dev):
-        rc = L.vs_group_rows(_ptr(ids), n, n_groups, _ptr(order), _ptr(offsets), _ptr(slot),
-                             _ptr(ws), ws.numel() * ws.element_size(), _stream(dev))
+        rc = L.vs_group_rows(_ptr(ids), n, n_groups, _ptr(order), _ptr(offsets), _ptr(slot), ws,
+                             size, _stream(dev))
     _check(rc, "vs_group_rows")
     return order, offsets, slot
 
@@ -1005,15 +1026,15 @@ def vs_row_lookup(T, ids, scale: float = 1.0, out=None):
     for an id outside the table.  ids may have any shape (taken flat)."""
     torch = _torch()
     L = lib()
-    _rows_arg(T, "T")
+    code = _rows_arg(T, "T")
     dev = T.device
     _same_dev(ids, "ids", torch.int32, dev)
     g, d = T.shape
     n = ids.numel()
-    out = _out(out, "out", T.dtype, (n, d), dev)
+    out = _new(out, "out", T.dtype, (n, d), T)
     with _on(dev):
-        rc = L.vs_row_lookup(_ptr(T), g, d, _dtype(T.dtype, "T"), _ptr(ids), n, float(scale),
-                             _ptr(out), _stream(dev))
+        rc = L.vs_row_lookup(_ptr(T), g, d, code, _ptr(ids), n, float(scale), _ptr(out),
+                             _stream(dev))
     _check(rc, "vs_row_lookup")
     return out
 
@@ -1026,7 +1047,7 @@ def vs_row_lookup_backward(dY, ids, order, offsets, scale: float = 1.0, grad_dty
     torch.float32."""
     torch = _torch()
     L = lib()
-    _rows_arg(dY, "dY")
+    code = _rows_arg(dY, "dY")
     dev = dY.device
     for t, name in ((ids, "ids"), (order, "order"), (offsets, "offsets")):
         _same_dev(t, name, torch.int32, dev)
@@ -1035,13 +1056,13 @@ def vs_row_lookup_backward(dY, ids, order, offsets, scale: float = 1.0, grad_dty
     if ids.numel() != n or order.numel() < n:
         raise ValueError("ids and order must hold one entry per row of dY")
     grad_dtype = dY.dtype if grad_dtype is None else grad_dtype
-    out = _out(out, "out", grad_dtype, (max(g, 0), d), dev)
-    ws = _workspace(L.vs_row_lookup_backward_workspace(n, d), dev, workspace)
+    grad_code = _dtype(grad_dtype, "grad_dtype")
+    out = _new(out, "out", grad_dtype, (max(g, 0), d), dY)
+    ws, size, _held = _scratch(L.vs_row_lookup_backward_workspace(n, d), dY, workspace)
     with _on(dev):
-        rc = L.vs_row_lookup_backward(_ptr(dY), n, d, _dtype(dY.dtype, "dY"), _ptr(ids),
-                                      _ptr(order), _ptr(offsets), g, float(scale),
-                                      _dtype(grad_dtype, "grad_dtype"), _ptr(out), _ptr(ws),
-                                      ws.numel() * ws.element_size(), _stream(dev))
+        rc = L.vs_row_lookup_backward(_ptr(dY), n, d, code, _ptr(ids), _ptr(order),
+                                      _ptr(offsets), g, float(scale), grad_code, _ptr(out), ws,
+                                      size, _stream(dev))
     _check(rc, "vs_row_lookup_backward")
     return out
 
@@ -1059,15 +1080,15 @@ def vs_route_rows(X, slot, offsets, k: int, out=None):
     vs_group_rows of the n x k ids."""
     torch = _torch()
     L = lib()
-    _rows_arg(X, "X")
+    code = _rows_arg(X, "X")
     dev = X.device
     n, d = X.shape
     k = int(k)
     _slots(slot, n, k, dev)
     _same_dev(offsets, "offsets", torch.int32, dev)
-    out = _out(out, "out", X.dtype, (n * k, d), dev)
+    out = _new(out, "out", X.dtype, (n * k, d), X)
     with _on(dev):
-        rc = L.vs_route_rows(_ptr(X), n, d, _dtype(X.dtype, "X"), _ptr(slot), _ptr(offsets),
+        rc = L.vs_route_rows(_ptr(X), n, d, code, _ptr(slot), _ptr(offsets),
                              offsets.numel() - 1, k, _ptr(out), _stream(dev))
     _check(rc, "vs_route_rows")
     return out
@@ -1076,7 +1097,7 @@ def vs_route_rows(X, slot, offsets, k: int, out=None):
 def vs_route_rows_backward(dXs, slot, k: int, out=None):
     """Gradient of vs_route_rows: out[i] = sum of dXs over row i's entries."""
     L = lib()
-    _rows_arg(dXs, "dXs")
+    code = _rows_arg(dXs, "dXs")
     dev = dXs.device
     m, d = dXs.shape
     k = int(k)
@@ -1084,10 +1105,10 @@ def vs_route_rows_backward(dXs, slot, k: int, out=None):
         raise ValueError(f"dXs must hold k = {k} rows per row")
     n = m // k
     _slots(slot, n, k, dev)
-    out = _out(out, "out", dXs.dtype, (n, d), dev)
+    out = _new(out, "out", dXs.dtype, (n, d), dXs)
     with _on(dev):
-        rc = L.vs_route_rows_backward(_ptr(dXs), n, d, _dtype(dXs.dtype, "dXs"), _ptr(slot), k,
-                                      _ptr(out), _stream(dev))
+        rc = L.vs_route_rows_backward(_ptr(dXs), n, d, code, _ptr(slot), k, _ptr(out),
+                                      _stream(dev))
     _check(rc, "vs_route_rows_backward")
     return out
 
@@ -1097,7 +1118,7 @@ def vs_combine_rows(Ys, slot, weights, out=None):
     the kept entries (Ys n k rows in unit order, weights n x k float32)."""
     torch = _torch()
     L = lib()
-    _rows_arg(Ys, "Ys")
+    code = _rows_arg(Ys, "Ys")
     dev = Ys.device
     _rows_arg(weights, "weights", dev, torch.float32)
     n, k = weights.shape
@@ -1105,10 +1126,10 @@ def vs_combine_rows(Ys, slot, weights, out=None):
     if Ys.shape[0] != n * k:
         raise ValueError("Ys must hold one row per entry of weights")
     _slots(slot, n, k, dev)
-    out = _out(out, "out", Ys.dtype, (n, d), dev)
+    out = _new(out, "out", Ys.dtype, (n, d), Ys)
     with _on(dev):
-        rc = L.vs_combine_rows(_ptr(Ys), n, d, _dtype(Ys.dtype, "Ys"), _ptr(slot), _ptr(weights),
-                               k, _ptr(out), _stream(dev))
+        rc = L.vs_combine_rows(_ptr(Ys), n, d, code, _ptr(slot), _ptr(weights), k, _ptr(out),
+                               _stream(dev))
     _check(rc, "vs_combine_rows")
     return out
 
@@ -1119,7 +1140,7 @@ def vs_combine_rows_backward(dY, Ys, slot, weights, offsets, out=None, dweights=
     (0 for a dropped entry)."""
     torch = _torch()
     L = lib()
-    _rows_arg(dY, "dY")
+    code = _rows_arg(dY, "dY")
     dev = dY.device
     _rows_arg(Ys, "Ys", dev, dY.dtype)
     _rows_arg(weights, "weights", dev, torch.float32)
@@ -1129,13 +1150,12 @@ def vs_combine_rows_backward(dY, Ys, slot, weights, offsets, out=None, dweights=
         raise ValueError("dY must be n x d and Ys (n * k) x d for weights n x k")
     _slots(slot, n, k, dev)
     _same_dev(offsets, "offsets", torch.int32, dev)
-    out = _out(out, "out", dY.dtype, (n * k, d), dev)
-    dweights = _out(dweights, "dweights", torch.float32, (n, k), dev)
+    out = _new(out, "out", dY.dtype, (n * k, d), dY)
+    dweights = _new(dweights, "dweights", torch.float32, (n, k), weights)
     with _on(dev):
-        rc = L.vs_combine_rows_backward(_ptr(dY), _ptr(Ys), n, d, _dtype(dY.dtype, "dY"),
-                                        _ptr(slot), _ptr(weights), _ptr(offsets),
-                                        offsets.numel() - 1, k, _ptr(out), _ptr(dweights),
-                                        _stream(dev))
+        rc = L.vs_combine_rows_backward(_ptr(dY), _ptr(Ys), n, d, code, _ptr(slot),
+                                        _ptr(weights), _ptr(offsets), offsets.numel() - 1, k,
+                                        _ptr(out), _ptr(dweights), _stream(dev))
     _check(rc, "vs_combine_rows_backward")
     return out, dweights
 
@@ -1153,17 +1173,17 @@ def vs_q4_quantize(T, group: int = 32, scale_dtype=None, codes=None, scales=None
     or torch.bfloat16); T[i, k] ~ scales[i, k // group] * (code - 8)."""
     torch = _torch()
     L = lib()
-    _rows_arg(T, "T")
+    code = _rows_arg(T, "T")
     dev = T.device
     nc, d = T.shape
     group = _q4_group(group)
     scale_dtype = torch.float16 if scale_dtype is None else scale_dtype
-    codes = _out(codes, "codes", torch.uint8, (nc, (d + 1) // 2), dev)
-    scales = _out(scales, "scales", scale_dtype, (nc, (d + group - 1) // group), dev)
+    scale_code = _dtype(scale_dtype, "scale_dtype")
+    codes = _new(codes, "codes", torch.uint8, (nc, (d + 1) // 2), T)
+    scales = _new(scales, "scales", scale_dtype, (nc, (d + group - 1) // group), T)
     with _on(dev):
-        rc = L.vs_q4_quantize(_ptr(T), nc, d, _dtype(T.dtype, "T"), group,
-                              _dtype(scale_dtype, "scale_dtype"), _ptr(codes), _ptr(scales),
-                              _stream(dev))
+        rc = L.vs_q4_quantize(_ptr(T), nc, d, code, group, scale_code, _ptr(codes),
+                              _ptr(scales), _stream(dev))
     _check(rc, "vs_q4_quantize")
     return codes, scales
 
@@ -1182,7 +1202,7 @@ def vs_q4_layout(codes, scales, d: int, group: int = 32, out=None):
     nc, d, group = codes.shape[0], int(d), _q4_group(group)
     if codes.shape[1] != (d + 1) // 2 or tuple(scales.shape) != (nc, (d + group - 1) // group):
         raise ValueError(f"codes and scales disagree with {nc} rows of {d} in groups of {group}")
-    out = _out(out, "out", torch.uint8, L.vs_q4_bytes(nc, d, group), dev)
+    out = _new(out, "out", torch.uint8, (L.vs_q4_bytes(nc, d, group),), codes)
     with _on(dev):
         rc = L.vs_q4_layout(_ptr(codes), _ptr(scales), nc, d, group, _ptr(out), _stream(dev))
     _check(rc, "vs_q4_layout")
@@ -1195,7 +1215,7 @@ def vs_q4_scores(x, table, nc: int, group: int = 32, scale_dtype=None, out=None)
     torch.float16)."""
     torch = _torch()
     L = lib()
-    _rows_arg(x, "x")
+    code = _rows_arg(x, "x")
     dev = x.device
     _same_dev(table, "table", torch.uint8, dev)
     nq, d = x.shape
@@ -1204,10 +1224,11 @@ def vs_q4_scores(x, table, nc: int, group: int = 32, scale_dtype=None, out=None)
     need = L.vs_q4_bytes(nc, d, group)
     if table.numel() != need:
         raise ValueError(f"table holds {table.numel()} bytes, {nc} rows of {d} take {need}")
-    out = _out(out, "out", torch.float32, (nq, nc), dev)
+    scale_code = _dtype(scale_dtype, "scale_dtype")
+    out = _new(out, "out", torch.float32, (nq, nc), x)
     with _on(dev):
-        rc = L.vs_q4_scores(_ptr(x), nq, d, _dtype(x.dtype, "x"), _ptr(table), nc, group,
-                            _dtype(scale_dtype, "scale_dtype"), _ptr(out), _stream(dev))
+        rc = L.vs_q4_scores(_ptr(x), nq, d, code, _ptr(table), nc, group, scale_code, _ptr(out),
+                            _stream(dev))
     _check(rc, "vs_q4_scores")
     return out
 

@@ -1022,10 +1022,11 @@ VS_API int vs_group_rows(const int32_t *ids, int64_t n, int64_t n_groups, int32_
                          int32_t *offsets, int32_t *slot, void *workspace,
                          size_t workspace_bytes, void *stream) {
     if (bad_group_shape(n, n_groups)) return VS_ERR_SHAPE;
-    if ((n > 0 && (!ids || !order)) || !offsets || !workspace) return VS_ERR_NULL;
+    const size_t need = vs::group_workspace(n, n_groups);
+    if ((n > 0 && (!ids || !order)) || !offsets || (need > 0 && !workspace)) return VS_ERR_NULL;
     if (!al4(ids) || !al4(order) || !al4(offsets) || !al4(slot) || !al256(workspace))
         return VS_ERR_ALIGN;
-    if (workspace_bytes < vs::group_workspace(n, n_groups)) return VS_ERR_WORKSPACE;
+    if (workspace_bytes < need) return VS_ERR_WORKSPACE;
     int n_cu = 0;
     if (const int s = device_ready(&n_cu)) return s;
     VS_TRY_HIP(vs::launch_group(ids, n, n_groups, order, offsets, slot, workspace,
@@ -1061,11 +1062,13 @@ VS_API int vs_row_lookup_backward(const void *dY, int64_t n, int32_t d, int32_t 
         (grad_dtype != dtype && grad_dtype != vs::kF32))
         return VS_ERR_DTYPE;
     if (bad_group_shape(n, n_groups) || d < 1 || d > kMaxDim) return VS_ERR_SHAPE;
-    if ((n > 0 && (!dY || !ids || !order)) || !offsets || !dT || !workspace) return VS_ERR_NULL;
+    const size_t need = vs::row_lookup_bwd_workspace(n, d);
+    if ((n > 0 && (!dY || !ids || !order)) || !offsets || !dT || (need > 0 && !workspace))
+        return VS_ERR_NULL;
     if (!al_type(dY, dtype) || !al4(ids) || !al4(order) || !al4(offsets) ||
         !al_type(dT, grad_dtype) || !al256(workspace))
         return VS_ERR_ALIGN;
-    if (workspace_bytes < vs::row_lookup_bwd_workspace(n, d)) return VS_ERR_WORKSPACE;
+    if (workspace_bytes < need) return VS_ERR_WORKSPACE;
     int n_cu = 0;
     if (const int s = device_ready(&n_cu)) return s;
     VS_TRY_HIP(vs::launch_row_lookup_bwd(dY, n, d, dtype, ids, order, offsets, n_groups, scale,

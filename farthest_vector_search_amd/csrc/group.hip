@@ -334,7 +334,7 @@ inline size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // keys and entries twice, counts of the tiles, totals and starts of the digits
 size_t group_workspace(int64_t n, int64_t G) {
-    if (n <= kRankMost) return 256 + up256((size_t)n * 4);
+    if (n <= kRankMost) return G <= kRankUnits ? 0 : up256((size_t)n * 4);
     const size_t arr = up256((size_t)n * 4);
     const size_t tiles = (size_t)((n + kTile - 1) / kTile);
     return 4 * arr + up256(tiles * (4u << kMaxBits)) + (4u << kMaxBits) + up256((4u << kMaxBits) + 4);

@@ -142,28 +142,27 @@ __device__ __forceinline__ void store_row(O *__restrict__ dT, int64_t g, int32_t
     store_once(reinterpret_cast<Vec<O, N> *>(dT + g * d) + c, o);
 }
 
-// Workgroups 0 .. piece_blocks - 1 sum the pieces of long units, the others
-// the short units; blockIdx.y is the block of columns.  A row's lanes take U
-// units at once where units have few rows: the first kFirst rows of each are
-// loaded together, and all U results are stored at the end, since a wave's
-// later loads would wait for its stores (both count down in order).
-constexpr int kFirst = 2;
-
-template <typename T, typename O, int N, int U>
+// Workgroups 0 .. piece_blocks - 1 sum the pieces of long units, the others a
+// short unit per group of lanes.  Neighbouring groups take the blocks of
+// columns of one row, so that a row is read in one go.
+template <typename T, typename O, int N>
 __global__ __launch_bounds__(256) void k_row_lookup_bwd(
     const T *__restrict__ dY, int64_t n, int32_t d, const int32_t *__restrict__ ids,
     const int32_t *__restrict__ order, const int32_t *__restrict__ offsets, int64_t G, float scale,
-    O *__restrict__ dT, float *__restrict__ part, unsigned piece_blocks, int lsh) {
+    O *__restrict__ dT, float *__restrict__ part, unsigned piece_blocks, int lsh,
+    unsigned cols) {
     const int lane = threadIdx.x & ((1 << lsh) - 1);
     const int per = 256 >> lsh;
-    const int c = ((int)blockIdx.y << lsh) + lane;
-    if (c >= d / N) return;
+    const int vecs = d / N;
     if (blockIdx.x < piece_blocks) {
         int64_t kept = offsets[G];
         kept = kept > n ? n : kept;
         const int64_t step = (int64_t)piece_blocks * per;
-        for (int64_t s = (int64_t)blockIdx.x * per + (threadIdx.x >> lsh); s * kRun < kept;
-             s += step) {
+        for (int64_t item = (int64_t)blockIdx.x * per + (threadIdx.x >> lsh);; item += step) {
+            const int64_t s = item / cols;
+            if (s * kRun >= kept) break;
+            const int c = ((int)(item - s * cols) << lsh) + lane;
+            if (c >= vecs) continue;
             const int64_t p0 = s * kRun, p1 = p0 + kRun < kept ? p0 + kRun : kept;
             const int64_t g0 = unit_at(ids, order, p0, n, G);
             const int64_t g1 = unit_at(ids, order, p1 - 1, n, G);
@@ -184,48 +183,18 @@ __global__ __launch_bounds__(256) void k_row_lookup_bwd(
         }
         return;
     }
-    const int64_t step = (int64_t)(gridDim.x - piece_blocks) * per * U;
-    for (int64_t g = ((int64_t)(blockIdx.x - piece_blocks) * per + (threadIdx.x >> lsh)) * U; g < G;
-         g += step) {
-        Span s[U];
-        bool mine[U], some[U];  // neither long nor past the last unit; has rows
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            s[u] = unit_span(offsets, g + u < G ? g + u : G - 1, n);
-            mine[u] = g + u < G && s[u].hi - s[u].lo <= kRun;
-            if (!mine[u] || s[u].hi < s[u].lo) s[u].hi = s[u].lo;
-            some[u] = s[u].hi > s[u].lo;
-        }
-        float acc[U][N] = {};
-        if constexpr (U > 1) {
-            if (n > 0) {
-                Vec<T, N> v[U][kFirst];
-                bool ok[U][kFirst];
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-#pragma unroll
-                    for (int a = 0; a < kFirst; ++a) {
-                        const int64_t p = s[u].lo + a;
-                        const int64_t i = order[p < n ? p : n - 1];
-                        ok[u][a] = p < s[u].hi && i >= 0 && i < n;
-                        v[u][a] = reinterpret_cast<const Vec<T, N> *>(dY + (ok[u][a] ? i : 0) * d)[c];
-                    }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-#pragma unroll
-                    for (int a = 0; a < kFirst; ++a)
-#pragma unroll
-                        for (int t = 0; t < N; ++t)
-                            acc[u][t] += ok[u][a] ? widen(v[u][a].v[t]) : 0.0f;
-                    s[u].lo += kFirst;
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) sum_rows<T, N>(dY, n, d, order, s[u], c, acc[u]);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (mine[u]) store_row<O, N>(dT, g + u, d, c, some[u] ? scale : 0.0f, acc[u]);
+    const int64_t step = (int64_t)(gridDim.x - piece_blocks) * per;
+    for (int64_t item = (int64_t)(blockIdx.x - piece_blocks) * per + (threadIdx.x >> lsh);;
+         item += step) {
+        const int64_t g = item / cols;
+        if (g >= G) break;
+        const int c = ((int)(item - g * cols) << lsh) + lane;
+        if (c >= vecs) continue;
+        const Span u = unit_span(offsets, g, n);
+        if (u.hi - u.lo > kRun) continue;
+        float acc[N] = {};
+        sum_rows<T, N>(dY, n, d, order, u, c, acc);
+        store_row<O, N>(dT, g, d, c, u.hi > u.lo ? scale : 0.0f, acc);
     }
 }
 
@@ -477,10 +446,11 @@ hipError_t launch_row_lookup(const void *table, int64_t G, int32_t d, int dtype,
     });
 }
 
-// Two fp32 rows per stretch of kRun places.
+// Two fp32 rows per stretch of kRun places; none where no unit can be long.
 size_t row_lookup_bwd_workspace(int64_t n, int32_t d) {
+    if (n <= kRun) return 0;
     const size_t stretches = (size_t)((n + kRun - 1) / kRun);
-    return 256 + stretches * 2 * (size_t)d * 4;
+    return stretches * 2 * (size_t)d * 4;
 }
 
 static int idle_lanes(int vecs, int lsh) {
@@ -488,7 +458,7 @@ static int idle_lanes(int vecs, int lsh) {
     return (vecs + lanes - 1) / lanes * lanes - vecs;
 }
 
-template <typename T, typename O, int N, int U>
+template <typename T, typename O, int N>
 static hipError_t lookup_bwd(const void *dY, int64_t n, int32_t d, const int32_t *ids,
                              const int32_t *order, const int32_t *offsets, int64_t G, float scale,
                              void *dT, float *part, hipStream_t st, int n_cu) {
@@ -502,13 +472,14 @@ static hipError_t lookup_bwd(const void *dY, int64_t n, int32_t d, const int32_t
     const int per = 256 >> lsh;
     const unsigned cols = (unsigned)((vecs + (1 << lsh) - 1) >> lsh);
     const int64_t stretches = (n + kRun - 1) / kRun, most = (int64_t)n_cu * 32;
-    const int64_t pb = (stretches + per - 1) / per, ub = (G + per * U - 1) / (per * U);
+    const int64_t pb = (stretches * cols + per - 1) / per;
+    const int64_t ub = (G * cols + per - 1) / per;
     const unsigned pieces = (unsigned)(pb < most ? pb : most);
     const unsigned units = (unsigned)(ub < most ? ub : most);
     timing_before(st, "k_row_lookup_bwd");
-    hipLaunchKernelGGL((k_row_lookup_bwd<T, O, N, U>), dim3(pieces + units, cols), dim3(256), 0, st,
+    hipLaunchKernelGGL((k_row_lookup_bwd<T, O, N>), dim3(pieces + units), dim3(256), 0, st,
                        (const T *)dY, n, d, ids, order, offsets, G, scale, (O *)dT, part, pieces,
-                       lsh);
+                       lsh, cols);
     timing_after(st);
     if (n > kRun) {  // else no unit is long
         const unsigned jc = (unsigned)((vecs + 63) / 64);
@@ -518,16 +489,6 @@ static hipError_t lookup_bwd(const void *dY, int64_t n, int32_t d, const int32_t
                            (O *)dT);
     }
     return hipGetLastError();
-}
-
-// Four units at a time where they have less than two rows on average.
-template <typename T, typename O, int N>
-static hipError_t lookup_bwd_units(const void *dY, int64_t n, int32_t d, const int32_t *ids,
-                                   const int32_t *order, const int32_t *offsets, int64_t G,
-                                   float scale, void *dT, float *part, hipStream_t st, int n_cu) {
-    if (n <= 2 * G)
-        return lookup_bwd<T, O, N, 4>(dY, n, d, ids, order, offsets, G, scale, dT, part, st, n_cu);
-    return lookup_bwd<T, O, N, 1>(dY, n, d, ids, order, offsets, G, scale, dT, part, st, n_cu);
 }
 
 hipError_t launch_row_lookup_bwd(const void *dY, int64_t n, int32_t d, int dtype,
@@ -542,10 +503,10 @@ hipError_t launch_row_lookup_bwd(const void *dY, int64_t n, int32_t d, int dtype
         using T = decltype(t);
         constexpr int N = decltype(nc)::value;
         if (grad_dtype == dtype)
-            return lookup_bwd_units<T, T, N>(dY, n, d, ids, order, offsets, G, scale, dT,
-                                            (float *)ws, st, n_cu);
-        return lookup_bwd_units<T, float, N>(dY, n, d, ids, order, offsets, G, scale, dT,
-                                                (float *)ws, st, n_cu);
+            return lookup_bwd<T, T, N>(dY, n, d, ids, order, offsets, G, scale, dT, (float *)ws,
+                                       st, n_cu);
+        return lookup_bwd<T, float, N>(dY, n, d, ids, order, offsets, G, scale, dT, (float *)ws,
+                                       st, n_cu);
     });
 }
 

@@ -450,7 +450,9 @@ int vs_som_epoch_csr_f16(const int32_t *indptr, const int32_t *indices, const fl
  *              order[offsets[g + 1] - 1]; offsets[n_groups] = entries kept.
  *   slot       int32[n] or NULL: each entry's place in order, -1 if dropped.
  * n in [0, 2^31-1] (0 writes the offsets only), n_groups in [1, 2^31-2].
- * The outputs must not overlap ids.
+ * The outputs must not overlap ids.  workspace may be NULL where the size
+ * query returns 0 (few entries and units); the query also returns 0 for
+ * invalid sizes.
  */
 size_t vs_group_rows_workspace(int64_t n, int64_t n_groups);
 int vs_group_rows(const int32_t *ids, int64_t n, int64_t n_groups, int32_t *order,
@@ -475,6 +477,7 @@ int vs_group_rows(const int32_t *ids, int64_t n, int64_t n_groups, int32_t *orde
  * aligned to their element; rows on 16-byte boundaries are fastest.  An
  * index read from order or offsets that does not fit the arrays is skipped;
  * nothing outside the arrays is read.  Inputs and outputs must not overlap.
+ * workspace may be NULL where the size query returns 0 (few rows).
  */
 int vs_row_lookup(const void *T, int64_t n_groups, int32_t d, int32_t dtype, const int32_t *ids,
                   int64_t n, float scale, void *Y, void *stream);

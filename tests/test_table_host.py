@@ -36,8 +36,9 @@ def test_group_rows(L):
     assert call(n=2 ** 31) == SHAPE
     assert call(g=0) == SHAPE
     assert call(g=2 ** 31 - 1) == SHAPE
-    for name in ("ids", "order", "offsets", "ws"):
+    for name in ("ids", "order", "offsets"):
         assert call(**{name: 0}) == NULL
+    assert call(n=5000, ws=0) == NULL and call(n=50, g=5000, ws=0) == NULL
     for name in ("ids", "order", "offsets", "slot"):
         assert call(**{name: FAKE + 2}) == ALIGN
     assert call(ws=FAKE + 64) == ALIGN
@@ -46,7 +47,8 @@ def test_group_rows(L):
     assert call(n=1 << 20, g=1000, size=need - 1) == WORKSPACE
     assert L.vs_group_rows_workspace(-1, 4) == 0
     assert L.vs_group_rows_workspace(4, 0) == 0
-    assert L.vs_group_rows_workspace(0, 1) >= 1
+    assert L.vs_group_rows_workspace(10, 4) == 0  # counted in one launch
+    assert L.vs_group_rows_workspace(10, 100000) == 256
 
 
 def test_row_lookup(L):
@@ -73,8 +75,11 @@ def test_row_lookup_backward(L):
     assert call(dtype=0, gd=1) == DTYPE
     for bad in (dict(g=0), dict(d=0), dict(n=-1)):
         assert call(**bad) == SHAPE
-    for name in ("dY", "ids", "order", "offsets", "dT", "ws"):
+    for name in ("dY", "ids", "order", "offsets", "dT"):
         assert call(**{name: 0}) == NULL
+    assert call(n=65, ws=0) == NULL     # units of more than 64 rows may occur
+    assert L.vs_row_lookup_backward_workspace(64, 8) == 0
+    assert L.vs_row_lookup_backward_workspace(65, 8) == 4 * 8 * 4
     assert call(n=0, dY=0, ids=0, order=0, dT=0) == NULL  # the gradient is still written
     for name in ("ids", "order", "offsets"):
         assert call(**{name: FAKE + 2}) == ALIGN
