@@ -180,44 +180,49 @@ __device__ __forceinline__ uint32_t bf16_piece(float x, int p) {
 }
 
 // Columns k .. k + 7 of query q as one lane's operand, zeros past the query
-// and for q >= nq.  wide: queries start on 16-byte boundaries and d % 8 == 0.
+// and for q >= nq: raw() loads them, frag() makes the operand.  wide: queries
+// start on 16-byte boundaries and d % 8 == 0.
 template <typename X>
-__device__ __forceinline__ Frag query_frag(const X *__restrict__ x, int64_t nq, int32_t d,
-                                           int64_t q, int piece, int64_t k, bool wide) {
-    Frag f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f.u[j] = 0;
-    if (q >= nq || k >= d) return f;
+struct QueryPart {
     Vec<X, 8> v;
-    const X *row = x + q * d + k;
-    if (wide) {
-        using W = Vec<X, 16 / sizeof(X)>;
-        W *to = reinterpret_cast<W *>(&v);
+    int left;  // columns of the query from k on (<= 0: none)
+    __device__ __forceinline__ void raw(const X *__restrict__ x, int64_t nq, int32_t d, int64_t q,
+                                        int64_t k, bool wide) {
+        const int64_t rest = q < nq ? d - k : 0;
+        left = (int)(rest < 8 ? rest : 8);
+        // what is not there is read at the first query's start, and unused
+        const X *row = left > 0 ? x + q * d + k : x;
+        if (wide) {
+            using W = Vec<X, 16 / sizeof(X)>;
+            W *to = reinterpret_cast<W *>(&v);
 #pragma unroll
-        for (int j = 0; j < (int)(8 / (16 / sizeof(X))); ++j)
-            to[j] = reinterpret_cast<const W *>(row)[j];
-    } else {
-        const int last = (int)(d - 1 - k);  // >= 0
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v.v[e] = row[e < last ? e : last];
-#pragma unroll
-        for (int e = 1; e < 8; ++e)
-            if (e > last) v.v[e] = X(0.0f);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        uint32_t h;
-        if constexpr (std::is_same<X, float>::value) {
-            h = bf16_piece(v.v[e], piece);
+            for (int j = 0; j < (int)(8 / (16 / sizeof(X))); ++j)
+                to[j] = reinterpret_cast<const W *>(row)[j];
         } else {
-            uint16_t raw;
-            __builtin_memcpy(&raw, &v.v[e], 2);
-            h = raw;
+            const int last = left > 0 ? left - 1 : 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v.v[e] = row[e < last ? e : last];
         }
-        f.u[e >> 1] |= h << (16 * (e & 1));
     }
-    return f;
-}
+    __device__ __forceinline__ Frag frag(int piece) const {
+        Frag f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f.u[j] = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t h;
+            if constexpr (std::is_same<X, float>::value) {
+                h = bf16_piece(v.v[e], piece);
+            } else {
+                uint16_t bits;
+                __builtin_memcpy(&bits, &v.v[e], 2);
+                h = bits;
+            }
+            f.u[e >> 1] |= (e < left ? h : 0u) << (16 * (e & 1));
+        }
+        return f;
+    }
+};
 
 // One block's codes and scales as a lane holds them.
 template <typename S, int PER>
@@ -230,6 +235,15 @@ struct Block {
         s = reinterpret_cast<const Vec<S, 4 * PER> *>(scales)[blk * 4 + (lane >> 4)];
     }
 };
+
+// Where the staged operand of 8 query columns (chunk: their number / 8), tile
+// ct and column c lies: [step = chunk / 4][ct][part = chunk % 4][c], with c
+// turned by the chunk.  A wave's read of a step takes 1 KiB in a row; the
+// staging writes of one column, a chunk per lane, spread over all banks.
+template <int NT>
+__device__ __forceinline__ int frag_place(int chunk, int ct, int c) {
+    return (((chunk >> 2) * NT + ct) * 4 + (chunk & 3)) * 16 + (c ^ (chunk & 15));
+}
 
 // Many rows: a workgroup of 16 waves takes a run of row blocks, whose blocks
 // lie one behind the other, and cuts that stream into 16 equal segments, so
@@ -245,13 +259,13 @@ template <typename X, typename S, int GROUP, int NT>
 __global__ __launch_bounds__(kStreamWaves * 64) void k_q4_scores_stream(
     const X *__restrict__ x, int64_t nq, int64_t nc, int32_t d, int64_t nrb, int32_t ncb,
     const uint4 *__restrict__ codes, const S *__restrict__ scales, float *__restrict__ y,
-    int32_t rows_per, int wide) {
+    int32_t rows_per, int wide, int quads) {
     using F = Form<X>;
     using A = typename F::A;
     constexpr int QT = 16 / F::pieces;
     constexpr int PER = kBlockCols / GROUP;
     extern __shared__ __attribute__((aligned(16))) uint32_t lds[];
-    Frag *frags = reinterpret_cast<Frag *>(lds);  // [4 ncb][NT][64]
+    Frag *frags = reinterpret_cast<Frag *>(lds);  // 4 ncb NT 64, see frag_place
     f32x4 *heads = reinterpret_cast<f32x4 *>(frags + (size_t)ncb * 4 * NT * 64);  // [wave][NT][64]
 
     const int lane = threadIdx.x & 63;
@@ -272,12 +286,36 @@ __global__ __launch_bounds__(kStreamWaves * 64) void k_q4_scores_stream(
         for (int u = 0; u < kBlocksAhead; ++u)
             buf[u].load(codes, scales, base + (b0 + u < b1 ? b0 + u : b1 - 1), lane);
 
-    for (int i = threadIdx.x; i < ncb * 4 * NT * 64; i += kStreamWaves * 64) {
-        const int l = i & 63, ct = (i >> 6) % NT, t = (i >> 6) / NT;
-        const int c = l & 15;
-        const int64_t q = c < QT * F::pieces ? q0 + ct * QT + c % QT : nq;
-        frags[i] = query_frag(x, nq, d, q, c / QT, 32 * (int64_t)t + 8 * (l >> 4), wide != 0);
+    // neighbouring threads read neighbouring columns of one query (the same
+    // column of 16 queries could lie in one L2 channel), several parts in
+    // flight, and each part is widened into its pieces once
+    constexpr int kParts = std::is_same<X, float>::value ? 2 : 4;
+    const int chunks = ncb * (kBlockCols / 8), parts = chunks * NT * QT;
+    for (int i0 = threadIdx.x; i0 < parts; i0 += kParts * kStreamWaves * 64) {
+        QueryPart<X> qp[kParts];
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) {
+            const int i = i0 + h * kStreamWaves * 64, j = i / chunks;
+            qp[h].raw(x, nq, d, i < parts ? q0 + j : nq, 8 * (int64_t)(i - j * chunks), wide != 0);
+        }
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) {
+            const int i = i0 + h * kStreamWaves * 64, j = i / chunks, chunk = i - j * chunks;
+            if (i >= parts) break;
+            const int ct = j / QT;
+#pragma unroll
+            for (int p = 0; p < F::pieces; ++p)
+                frags[frag_place<NT>(chunk, ct, j - ct * QT + p * QT)] = qp[h].frag(p);
+        }
     }
+    if constexpr (F::pieces * QT < 16)  // the columns of no query
+        for (int i = threadIdx.x; i < chunks * NT; i += kStreamWaves * 64) {
+            const int ct = i / chunks;
+            Frag zero;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) zero.u[j] = 0;
+            for (int c = F::pieces * QT; c < 16; ++c) frags[frag_place<NT>(i - ct * chunks, ct, c)] = zero;
+        }
     __syncthreads();
 
     Frag m24;
@@ -302,9 +340,13 @@ __global__ __launch_bounds__(kStreamWaves * 64) void k_q4_scores_stream(
             const int64_t q = q0 + ct * QT + col, row = rb * kBlockRows + 4 * part;
             if (col < QT && q < nq) {
                 float *to = y + q * nc + row;
+                if (quads) {  // nc % 4 == 0: all four rows are there, or none
+                    if (row < nc) __builtin_nontemporal_store(v, reinterpret_cast<f32x4 *>(to));
+                } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    if (row + r < nc) to[r] = v[r];
+                    for (int r = 0; r < 4; ++r)
+                        if (row + r < nc) to[r] = v[r];
+                }
             }
         }
     };
@@ -327,7 +369,6 @@ __global__ __launch_bounds__(kStreamWaves * 64) void k_q4_scores_stream(
             const int32_t next = b + u + kBlocksAhead;
             buf[u].load(codes, scales, base + (next < b1 ? next : b1 - 1), lane);
             const uint32_t a[4] = {now.a.x, now.a.y, now.a.z, now.a.w};
-            const Frag *fr = frags + (size_t)cb * 4 * NT * 64 + lane;
 #pragma unroll
             for (int g = 0; g < PER; ++g) {
                 f32x4 c[NT];
@@ -339,7 +380,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void k_q4_scores_stream(
                     const Frag e = expand<F>(a[t]);
 #pragma unroll
                     for (int ct = 0; ct < NT; ++ct) {
-                        const Frag q = fr[(t * NT + ct) * 64];
+                        const Frag q = frags[frag_place<NT>(16 * cb + 4 * t + part, ct, col)];
                         c[ct] = F::mul(frag_as<A>(m24), frag_as<A>(q), c[ct]);
                         c[ct] = F::mul(frag_as<A>(e), frag_as<A>(q), c[ct]);
                     }
@@ -410,9 +451,9 @@ __global__ __launch_bounds__(kWideWaves * 64) void k_q4_scores_wide(
 #pragma unroll
                     for (int s = 0; s < GROUP / 32; ++s) {
                         const int t = g * (GROUP / 32) + s;
-                        const Frag b = query_frag(x, nq, d, q, piece,
-                                                  cb * kBlockCols + 32 * t + 8 * part,
-                                                  wide != 0);
+                        QueryPart<X> qp;
+                        qp.raw(x, nq, d, q, cb * kBlockCols + 32 * t + 8 * part, wide != 0);
+                        const Frag b = qp.frag(piece);
                         c = F::mul(frag_as<A>(m24), frag_as<A>(b), c);
                         c = F::mul(frag_as<A>(expand<F>(a[t])), frag_as<A>(b), c);
                     }
@@ -454,11 +495,13 @@ void launch_stream(const X *x, int64_t nq, int32_t d, const uint4 *codes, const 
     if (per > most) per = most;
     const int64_t cols = (nq + (int64_t)NT * QT - 1) / ((int64_t)NT * QT);
     for (int64_t c = 0; c < cols; c += 65535) {  // the grid's limit in y
+        const int quads = nc % 4 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0;
         const int64_t cn = cols - c < 65535 ? cols - c : 65535, q = c * NT * QT;
         hipLaunchKernelGGL((k_q4_scores_stream<X, S, GROUP, NT>),
                            dim3((unsigned)((nrb + per - 1) / per), (unsigned)cn),
                            dim3(kStreamWaves * 64), stream_lds(ncb, NT), st, x + q * d, nq - q, nc,
-                           d, nrb, (int32_t)ncb, codes, scales, y + q * nc, (int32_t)per, wide);
+                           d, nrb, (int32_t)ncb, codes, scales, y + q * nc, (int32_t)per, wide,
+                           quads);
     }
 }
 
