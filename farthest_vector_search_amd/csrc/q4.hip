@@ -14,12 +14,14 @@
 // f32 queries too, as three bf16 columns that add up to the query exactly
 // (8 + 8 + 8 bits), five queries to a tile of 16 columns.
 //
-// Layout of the table: blocks of 16 rows x 128 columns, 1 KiB of codes each,
-// in the order of the lanes: lane l (row l % 16, part l / 16) holds 16 bytes,
-// and its 32-bit word t holds columns 32 t + 8 (l / 16) .. + 7 of the block,
-// what the lane feeds to the t-th instruction.  Columns 2 j and 2 j + 1 of
-// the eight sit at bits 4 j and 16 + 4 j.  The scales follow behind all the
-// codes: per block four runs (rows 4 r .. 4 r + 3) of [group][row].
+// Layout of the table: blocks of 16 rows x 128 columns, a row block's one
+// behind the other.  A block is 1 KiB of codes in the order of the lanes: lane
+// l (row l % 16, part l / 16) holds 16 bytes, and its 32-bit word t holds
+// columns 32 t + 8 (l / 16) .. + 7 of the block, what the lane feeds to the
+// t-th instruction.  Columns 2 j and 2 j + 1 of the eight sit at bits 4 j and
+// 16 + 4 j.  Its scales follow in four runs (rows 4 r .. 4 r + 3) of
+// [group][row], in the same stretch of memory (an array of their own cost
+// 2 us of 47 at 65,536 x 4,096, group 128).
 #include <type_traits>
 
 #include "vs_internal.h"
@@ -78,41 +80,37 @@ __global__ __launch_bounds__(256) void k_q4_quantize(const T *__restrict__ table
 
 // ---- layout: plain codes and scales into blocks ------------------------------
 
+constexpr int block_bytes(int per) { return 1024 + kBlockRows * 2 * per; }  // per: groups a block
+
 __global__ __launch_bounds__(256) void k_q4_layout(const uint8_t *__restrict__ codes,
                                                    const uint16_t *__restrict__ scales, int64_t nc,
                                                    int32_t d, int group, int64_t nrb, int64_t ncb,
-                                                   uint32_t *__restrict__ out) {
-    const int64_t words = nrb * ncb * 256;
+                                                   uint8_t *__restrict__ out) {
     const int64_t bytes = ((int64_t)d + 1) / 2;
-    const int per_block = kBlockCols / group;  // groups per block
+    const int per = kBlockCols / group;
     const int64_t groups = (d + group - 1) / group;
-    const int64_t nscale = nrb * ncb * per_block * kBlockRows;
-    uint16_t *sc = reinterpret_cast<uint16_t *>(out + words);
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < words + nscale;
-         i += (int64_t)gridDim.x * 256) {
-        if (i < words) {
-            const int64_t blk = i >> 8;
-            const int lane = (int)(i >> 2) & 63, t = (int)i & 3;
-            const int64_t rb = blk / ncb, cb = blk - rb * ncb;
-            const int64_t row = rb * kBlockRows + (lane & 15);
-            const int64_t k0 = cb * kBlockCols + 32 * t + 8 * (lane >> 4);
-            uint32_t w = 0;
+    // a workgroup per block: 256 words of codes, 16 x per scales
+    for (int64_t blk = blockIdx.x; blk < nrb * ncb; blk += gridDim.x) {
+        const int64_t rb = blk / ncb, cb = blk - rb * ncb;
+        uint8_t *to = out + blk * block_bytes(per);
+        const int lane = (int)threadIdx.x >> 2, t = (int)threadIdx.x & 3;
+        const int64_t row = rb * kBlockRows + (lane & 15);
+        const int64_t k0 = cb * kBlockCols + 32 * t + 8 * (lane >> 4);
+        uint32_t w = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                uint32_t c = 8;  // stands for 0
-                if (row < nc && k0 + e < d)
-                    c = (codes[row * bytes + (k0 + e) / 2] >> (4 * (e & 1))) & 15;
-                w |= c << (4 * (e >> 1) + 16 * (e & 1));
-            }
-            out[i] = w;
-        } else {
-            const int64_t j = i - words;
-            const int64_t blk = j / (per_block * kBlockRows);
-            const int in = (int)(j - blk * (per_block * kBlockRows));
-            const int run = in / (4 * per_block), g = in / 4 % per_block, r = in % 4;
-            const int64_t rb = blk / ncb, cb = blk - rb * ncb;
-            const int64_t row = rb * kBlockRows + 4 * run + r, gg = cb * per_block + g;
-            sc[j] = row < nc && gg < groups ? scales[row * groups + gg] : (uint16_t)0;
+        for (int e = 0; e < 8; ++e) {
+            uint32_t c = 8;  // stands for 0
+            if (row < nc && k0 + e < d)
+                c = (codes[row * bytes + (k0 + e) / 2] >> (4 * (e & 1))) & 15;
+            w |= c << (4 * (e >> 1) + 16 * (e & 1));
+        }
+        reinterpret_cast<uint32_t *>(to)[threadIdx.x] = w;
+        if ((int)threadIdx.x < per * kBlockRows) {
+            const int in = threadIdx.x;
+            const int run = in / (4 * per), g = in / 4 % per, r = in % 4;
+            const int64_t srow = rb * kBlockRows + 4 * run + r, gg = cb * per + g;
+            reinterpret_cast<uint16_t *>(to + 1024)[in] =
+                srow < nc && gg < groups ? scales[srow * groups + gg] : (uint16_t)0;
         }
     }
 }
@@ -179,46 +177,46 @@ __device__ __forceinline__ uint32_t bf16_piece(float x, int p) {
     return __float_as_uint(r) >> 16;
 }
 
-// Columns k .. k + 7 of query q as one lane's operand, zeros past the query
-// and for q >= nq: raw() loads them, frag() makes the operand.  wide: queries
-// start on 16-byte boundaries and d % 8 == 0.
+// Columns k .. k + 7 of a query (its row; d columns) as one lane's operand,
+// zeros past the query: raw() loads them, frag() makes the operand.  wide:
+// queries start on 16-byte boundaries and d % 8 == 0, so all eight are there
+// or none.
 template <typename X>
 struct QueryPart {
     Vec<X, 8> v;
-    int left;  // columns of the query from k on (<= 0: none)
-    __device__ __forceinline__ void raw(const X *__restrict__ x, int64_t nq, int32_t d, int64_t q,
-                                        int64_t k, bool wide) {
-        const int64_t rest = q < nq ? d - k : 0;
-        left = (int)(rest < 8 ? rest : 8);
-        // what is not there is read at the first query's start, and unused
-        const X *row = left > 0 ? x + q * d + k : x;
+    int left;  // columns there, 8 at most (<= 0: none)
+    __device__ __forceinline__ void raw(const X *__restrict__ row, int32_t d, int32_t k,
+                                        bool wide) {
+        left = d - k < 8 ? d - k : 8;
+        const X *from = row + (left > 0 ? k : 0);  // without any, unused values
         if (wide) {
             using W = Vec<X, 16 / sizeof(X)>;
             W *to = reinterpret_cast<W *>(&v);
 #pragma unroll
             for (int j = 0; j < (int)(8 / (16 / sizeof(X))); ++j)
-                to[j] = reinterpret_cast<const W *>(row)[j];
+                to[j] = reinterpret_cast<const W *>(from)[j];
         } else {
             const int last = left > 0 ? left - 1 : 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v.v[e] = row[e < last ? e : last];
+            for (int e = 0; e < 8; ++e) v.v[e] = from[e < last ? e : last];
         }
     }
-    __device__ __forceinline__ Frag frag(int piece) const {
+    __device__ __forceinline__ Frag frag(int piece, bool wide) const {
         Frag f;
+        if constexpr (std::is_same<X, float>::value) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) f.u[j] = 0;
+            for (int j = 0; j < 4; ++j)
+                f.u[j] = bf16_piece(v.v[2 * j], piece) | bf16_piece(v.v[2 * j + 1], piece) << 16;
+        } else {
+            __builtin_memcpy(&f, &v, 16);
+        }
+        if (wide) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            uint32_t h;
-            if constexpr (std::is_same<X, float>::value) {
-                h = bf16_piece(v.v[e], piece);
-            } else {
-                uint16_t bits;
-                __builtin_memcpy(&bits, &v.v[e], 2);
-                h = bits;
-            }
-            f.u[e >> 1] |= (e < left ? h : 0u) << (16 * (e & 1));
+            for (int j = 0; j < 4; ++j) f.u[j] = left > 0 ? f.u[j] : 0;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e >= left) f.u[e >> 1] &= e & 1 ? 0x0000ffffu : 0xffff0000u;
         }
         return f;
     }
@@ -229,10 +227,11 @@ template <typename S, int PER>
 struct Block {
     uint4 a;
     Vec<S, 4 * PER> s;
-    __device__ __forceinline__ void load(const uint4 *__restrict__ codes,
-                                         const S *__restrict__ scales, int64_t blk, int lane) {
-        a = codes[blk * 64 + lane];
-        s = reinterpret_cast<const Vec<S, 4 * PER> *>(scales)[blk * 4 + (lane >> 4)];
+    __device__ __forceinline__ void load(const uint8_t *__restrict__ table, int64_t blk,
+                                         int lane) {
+        const uint8_t *from = table + blk * block_bytes(PER);
+        a = reinterpret_cast<const uint4 *>(from)[lane];
+        s = reinterpret_cast<const Vec<S, 4 * PER> *>(from + 1024)[lane >> 4];
     }
 };
 
@@ -253,12 +252,12 @@ __device__ __forceinline__ int frag_place(int chunk, int ct, int c) {
 // cut by a segment's border is finished by the wave that began it, from the
 // parts (heads) the next waves leave in LDS, added in their order.
 constexpr int kStreamWaves = 16;
-constexpr int kBlocksAhead = 4;
+constexpr int kBlocksAhead = 2;
 
 template <typename X, typename S, int GROUP, int NT>
 __global__ __launch_bounds__(kStreamWaves * 64) void k_q4_scores_stream(
     const X *__restrict__ x, int64_t nq, int64_t nc, int32_t d, int64_t nrb, int32_t ncb,
-    const uint4 *__restrict__ codes, const S *__restrict__ scales, float *__restrict__ y,
+    const uint8_t *__restrict__ table, float *__restrict__ y,
     int32_t rows_per, int wide, int quads) {
     using F = Form<X>;
     using A = typename F::A;
@@ -280,42 +279,60 @@ __global__ __launch_bounds__(kStreamWaves * 64) void k_q4_scores_stream(
     const int64_t base = r0 * ncb;
     const int64_t q0 = (int64_t)blockIdx.y * NT * QT;
 
+    // Staging, a query's 64 x 8 columns to a wave at a time: neighbouring lanes
+    // read neighbouring columns (the same column of 16 queries could lie in
+    // one L2 channel).  The first are asked for before the first blocks: loads
+    // return in order, so behind a block they would wait for it.  Columns of
+    // no query keep what LDS held: their sums go nowhere.
+    constexpr int kParts = std::is_same<X, float>::value ? 4 : 8;
+    const int chunks = ncb * (kBlockCols / 8), runs = (chunks + 63) >> 6;
+    const int queries = (int)(nq - q0 < NT * QT ? nq - q0 : NT * QT);
+    QueryPart<X> qp[kParts];
+    // (query, run of 64 parts) of this wave's next part; all uniform
+    const int step_q = kStreamWaves / runs, step_run = kStreamWaves - step_q * runs;
+    int ask_q = w / runs, ask_run = w - ask_q * runs, stage_q = ask_q, stage_run = ask_run;
+    auto go_on = [&](int &q, int &run) {
+        q += step_q;
+        run += step_run;
+        if (run >= runs) {
+            run -= runs;
+            ++q;
+        }
+    };
+    auto ask = [&]() {
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) {
+            if (ask_q >= queries) break;
+            qp[h].raw(x + (q0 + ask_q) * d, d, 8 * (64 * ask_run + lane), wide != 0);
+            go_on(ask_q, ask_run);
+        }
+    };
+    auto stage = [&]() {
+#pragma unroll
+        for (int h = 0; h < kParts; ++h) {
+            if (stage_q >= queries) break;
+            const int chunk = 64 * stage_run + lane;
+            if (chunk < chunks) {
+                const int ct = stage_q / QT;
+#pragma unroll
+                for (int p = 0; p < F::pieces; ++p)
+                    frags[frag_place<NT>(chunk, ct, stage_q - ct * QT + p * QT)] =
+                        qp[h].frag(p, wide != 0);
+            }
+            go_on(stage_q, stage_run);
+        }
+    };
+    ask();
     Block<S, PER> buf[kBlocksAhead];
     if (b0 < b1)
 #pragma unroll
         for (int u = 0; u < kBlocksAhead; ++u)
-            buf[u].load(codes, scales, base + (b0 + u < b1 ? b0 + u : b1 - 1), lane);
-
-    // neighbouring threads read neighbouring columns of one query (the same
-    // column of 16 queries could lie in one L2 channel), several parts in
-    // flight, and each part is widened into its pieces once
-    constexpr int kParts = std::is_same<X, float>::value ? 2 : 4;
-    const int chunks = ncb * (kBlockCols / 8), parts = chunks * NT * QT;
-    for (int i0 = threadIdx.x; i0 < parts; i0 += kParts * kStreamWaves * 64) {
-        QueryPart<X> qp[kParts];
-#pragma unroll
-        for (int h = 0; h < kParts; ++h) {
-            const int i = i0 + h * kStreamWaves * 64, j = i / chunks;
-            qp[h].raw(x, nq, d, i < parts ? q0 + j : nq, 8 * (int64_t)(i - j * chunks), wide != 0);
-        }
-#pragma unroll
-        for (int h = 0; h < kParts; ++h) {
-            const int i = i0 + h * kStreamWaves * 64, j = i / chunks, chunk = i - j * chunks;
-            if (i >= parts) break;
-            const int ct = j / QT;
-#pragma unroll
-            for (int p = 0; p < F::pieces; ++p)
-                frags[frag_place<NT>(chunk, ct, j - ct * QT + p * QT)] = qp[h].frag(p);
-        }
+            buf[u].load(table, base + (b0 + u < b1 ? b0 + u : b1 - 1), lane);
+    stage();
+    while (stage_q < queries) {
+        ask();
+        stage();
     }
-    if constexpr (F::pieces * QT < 16)  // the columns of no query
-        for (int i = threadIdx.x; i < chunks * NT; i += kStreamWaves * 64) {
-            const int ct = i / chunks;
-            Frag zero;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) zero.u[j] = 0;
-            for (int c = F::pieces * QT; c < 16; ++c) frags[frag_place<NT>(i - ct * chunks, ct, c)] = zero;
-        }
     __syncthreads();
 
     Frag m24;
@@ -361,44 +378,49 @@ __global__ __launch_bounds__(kStreamWaves * 64) void k_q4_scores_stream(
 
     int32_t rb = b0 / ncb, cb = b0 - rb * ncb;  // row block inside the run
     bool head = cb != 0;
+    auto work = [&](const Block<S, PER> &now) __attribute__((always_inline)) {
+        const uint32_t a[4] = {now.a.x, now.a.y, now.a.z, now.a.w};
+#pragma unroll
+        for (int g = 0; g < PER; ++g) {
+            f32x4 c[NT];
+#pragma unroll
+            for (int ct = 0; ct < NT; ++ct) c[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < GROUP / 32; ++s) {
+                const int t = g * (GROUP / 32) + s;
+                const Frag e = expand<F>(a[t]);
+#pragma unroll
+                for (int ct = 0; ct < NT; ++ct) {
+                    const Frag q = frags[frag_place<NT>(16 * cb + 4 * t + part, ct, col)];
+                    c[ct] = F::mul(frag_as<A>(m24), frag_as<A>(q), c[ct]);
+                    c[ct] = F::mul(frag_as<A>(e), frag_as<A>(q), c[ct]);
+                }
+            }
+#pragma unroll
+            for (int ct = 0; ct < NT; ++ct)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    acc[ct][r] = __builtin_fmaf(widen(now.s.v[4 * g + r]), c[ct][r], acc[ct][r]);
+        }
+        if (++cb == ncb) {
+            if (head) leave_head();
+            else store(r0 + rb);
+            head = false;
+            clear();
+            cb = 0;
+            ++rb;
+        }
+    };
+    // Every step asks for a block, past the end for the last one again: after a
+    // load that may not be there, each wait would be a wait for all.
     for (int32_t b = b0; b < b1; b += kBlocksAhead) {
 #pragma unroll
         for (int u = 0; u < kBlocksAhead; ++u) {
             if (b + u >= b1) break;
             const Block<S, PER> now = buf[u];
             const int32_t next = b + u + kBlocksAhead;
-            buf[u].load(codes, scales, base + (next < b1 ? next : b1 - 1), lane);
-            const uint32_t a[4] = {now.a.x, now.a.y, now.a.z, now.a.w};
-#pragma unroll
-            for (int g = 0; g < PER; ++g) {
-                f32x4 c[NT];
-#pragma unroll
-                for (int ct = 0; ct < NT; ++ct) c[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int s = 0; s < GROUP / 32; ++s) {
-                    const int t = g * (GROUP / 32) + s;
-                    const Frag e = expand<F>(a[t]);
-#pragma unroll
-                    for (int ct = 0; ct < NT; ++ct) {
-                        const Frag q = frags[frag_place<NT>(16 * cb + 4 * t + part, ct, col)];
-                        c[ct] = F::mul(frag_as<A>(m24), frag_as<A>(q), c[ct]);
-                        c[ct] = F::mul(frag_as<A>(e), frag_as<A>(q), c[ct]);
-                    }
-                }
-#pragma unroll
-                for (int ct = 0; ct < NT; ++ct)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[ct][r] = __builtin_fmaf(widen(now.s.v[4 * g + r]), c[ct][r], acc[ct][r]);
-            }
-            if (++cb == ncb) {
-                if (head) leave_head();
-                else store(r0 + rb);
-                head = false;
-                clear();
-                cb = 0;
-                ++rb;
-            }
+            buf[u].load(table, base + (next < b1 ? next : b1 - 1), lane);
+            work(now);
         }
     }
     const bool open = b0 < b1 && cb != 0;  // the segment ends inside a row block
@@ -421,7 +443,7 @@ constexpr int kWideWaves = 16;
 template <typename X, typename S, int GROUP>
 __global__ __launch_bounds__(kWideWaves * 64) void k_q4_scores_wide(
     const X *__restrict__ x, int64_t nq, int64_t nc, int32_t d, int64_t nrb, int64_t ncb,
-    const uint4 *__restrict__ codes, const S *__restrict__ scales, float *__restrict__ y,
+    const uint8_t *__restrict__ table, float *__restrict__ y,
     int wide) {
     using F = Form<X>;
     using A = typename F::A;
@@ -443,7 +465,7 @@ __global__ __launch_bounds__(kWideWaves * 64) void k_q4_scores_wide(
             for (int64_t cb = w; cb < ncb; cb += waves) {
                 const int64_t blk = rb * ncb + cb;
                 Block<S, PER> now;
-                now.load(codes, scales, blk, lane);
+                now.load(table, blk, lane);
                 const uint32_t a[4] = {now.a.x, now.a.y, now.a.z, now.a.w};
 #pragma unroll
                 for (int g = 0; g < PER; ++g) {
@@ -452,8 +474,9 @@ __global__ __launch_bounds__(kWideWaves * 64) void k_q4_scores_wide(
                     for (int s = 0; s < GROUP / 32; ++s) {
                         const int t = g * (GROUP / 32) + s;
                         QueryPart<X> qp;
-                        qp.raw(x, nq, d, q, cb * kBlockCols + 32 * t + 8 * part, wide != 0);
-                        const Frag b = qp.frag(piece);
+                        qp.raw(x + (q < nq ? q : 0) * d, q < nq ? d : 0,
+                               (int32_t)cb * kBlockCols + 32 * t + 8 * part, wide != 0);
+                        const Frag b = qp.frag(piece, wide != 0);
                         c = F::mul(frag_as<A>(m24), frag_as<A>(b), c);
                         c = F::mul(frag_as<A>(expand<F>(a[t])), frag_as<A>(b), c);
                     }
@@ -485,8 +508,8 @@ size_t stream_lds(int64_t ncb, int nt) {
 }
 
 template <typename X, typename S, int GROUP, int NT>
-void launch_stream(const X *x, int64_t nq, int32_t d, const uint4 *codes, const S *scales,
-                   int64_t nc, float *y, int wide, hipStream_t st, int n_cu) {
+void launch_stream(const X *x, int64_t nq, int32_t d, const uint8_t *table, int64_t nc,
+                   float *y, int wide, hipStream_t st, int n_cu) {
     const int64_t nrb = row_blocks(nc), ncb = col_blocks(d);
     constexpr int QT = 16 / Form<X>::pieces;
     // a run of row blocks per CU, of fewer than 2^30 blocks
@@ -500,17 +523,15 @@ void launch_stream(const X *x, int64_t nq, int32_t d, const uint4 *codes, const 
         hipLaunchKernelGGL((k_q4_scores_stream<X, S, GROUP, NT>),
                            dim3((unsigned)((nrb + per - 1) / per), (unsigned)cn),
                            dim3(kStreamWaves * 64), stream_lds(ncb, NT), st, x + q * d, nq - q, nc,
-                           d, nrb, (int32_t)ncb, codes, scales, y + q * nc, (int32_t)per, wide,
+                           d, nrb, (int32_t)ncb, table, y + q * nc, (int32_t)per, wide,
                            quads);
     }
 }
 
 template <typename X, typename S, int GROUP>
-hipError_t scores_group(const X *x, int64_t nq, int32_t d, const void *table, int64_t nc, float *y,
+hipError_t scores_group(const X *x, int64_t nq, int32_t d, const uint8_t *table, int64_t nc, float *y,
                         hipStream_t st, int n_cu) {
     const int64_t nrb = row_blocks(nc), ncb = col_blocks(d);
-    const uint4 *codes = static_cast<const uint4 *>(table);
-    const S *scales = reinterpret_cast<const S *>(codes + nrb * ncb * 64);
     const int wide = d % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0;
     constexpr int QT = 16 / Form<X>::pieces;
     const int64_t tiles = (nq + QT - 1) / QT;
@@ -518,24 +539,24 @@ hipError_t scores_group(const X *x, int64_t nq, int32_t d, const void *table, in
     // the table is read once per launch row of column tiles: as many tiles as
     // the queries need and LDS holds
     if (tiles > 2 && stream_lds(ncb, 4) <= kLds)
-        launch_stream<X, S, GROUP, 4>(x, nq, d, codes, scales, nc, y, wide, st, n_cu);
+        launch_stream<X, S, GROUP, 4>(x, nq, d, table, nc, y, wide, st, n_cu);
     else if (tiles > 1 && stream_lds(ncb, 2) <= kLds)
-        launch_stream<X, S, GROUP, 2>(x, nq, d, codes, scales, nc, y, wide, st, n_cu);
+        launch_stream<X, S, GROUP, 2>(x, nq, d, table, nc, y, wide, st, n_cu);
     else if (stream_lds(ncb, 1) <= kLds)
-        launch_stream<X, S, GROUP, 1>(x, nq, d, codes, scales, nc, y, wide, st, n_cu);
+        launch_stream<X, S, GROUP, 1>(x, nq, d, table, nc, y, wide, st, n_cu);
     else {
         const dim3 grid((unsigned)(nrb < (1 << 20) ? nrb : 1 << 20),
                         (unsigned)(tiles < 64 ? tiles : 64));
         const dim3 block(64 * (unsigned)(ncb < kWideWaves ? ncb : kWideWaves));
         hipLaunchKernelGGL((k_q4_scores_wide<X, S, GROUP>), grid, block, 0, st, x, nq, nc, d, nrb,
-                           ncb, codes, scales, y, wide);
+                           ncb, table, y, wide);
     }
     timing_after(st);
     return hipGetLastError();
 }
 
 template <typename X, typename S>
-hipError_t scores_type(const X *x, int64_t nq, int32_t d, const void *table, int64_t nc, int group,
+hipError_t scores_type(const X *x, int64_t nq, int32_t d, const uint8_t *table, int64_t nc, int group,
                        float *y, hipStream_t st, int n_cu) {
     switch (group) {
     case 32: return scores_group<X, S, 32>(x, nq, d, table, nc, y, st, n_cu);
@@ -548,8 +569,10 @@ template <typename X>
 hipError_t scores_scale(const void *x, int64_t nq, int32_t d, const void *table, int64_t nc,
                         int group, int scale_dtype, float *y, hipStream_t st, int n_cu) {
     if (scale_dtype == kF16)
-        return scores_type<X, _Float16>((const X *)x, nq, d, table, nc, group, y, st, n_cu);
-    return scores_type<X, __bf16>((const X *)x, nq, d, table, nc, group, y, st, n_cu);
+        return scores_type<X, _Float16>((const X *)x, nq, d, (const uint8_t *)table, nc, group, y,
+                                            st, n_cu);
+    return scores_type<X, __bf16>((const X *)x, nq, d, (const uint8_t *)table, nc, group, y,
+                                            st, n_cu);
 }
 
 template <typename T>
@@ -567,8 +590,8 @@ hipError_t quantize_scale(const void *table, int64_t nc, int32_t d, int group, i
 }  // namespace
 
 size_t q4_bytes(int64_t nc, int32_t d, int group) {
-    const size_t blocks = (size_t)row_blocks(nc) * (size_t)col_blocks(d);
-    return blocks * (1024 + (size_t)(kBlockCols / group) * kBlockRows * 2);
+    return (size_t)row_blocks(nc) * (size_t)col_blocks(d) *
+           (size_t)block_bytes(kBlockCols / group);
 }
 
 hipError_t launch_q4_quantize(const void *table, int64_t nc, int32_t d, int dtype, int group,
@@ -587,10 +610,9 @@ hipError_t launch_q4_quantize(const void *table, int64_t nc, int32_t d, int dtyp
 hipError_t launch_q4_layout(const uint8_t *codes, const void *scales, int64_t nc, int32_t d,
                             int group, void *out, hipStream_t st, int n_cu) {
     const int64_t nrb = row_blocks(nc), ncb = col_blocks(d);
-    const int64_t most = (int64_t)n_cu * 64;
-    const int64_t want = nrb * ncb + 1;
+    const int64_t most = (int64_t)n_cu * 64, want = nrb * ncb;
     hipLaunchKernelGGL(k_q4_layout, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st,
-                       codes, (const uint16_t *)scales, nc, d, group, nrb, ncb, (uint32_t *)out);
+                       codes, (const uint16_t *)scales, nc, d, group, nrb, ncb, (uint8_t *)out);
     return hipGetLastError();
 }
 

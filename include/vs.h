@@ -530,8 +530,8 @@ int vs_combine_rows_backward(const void *dY, const void *Ys, int64_t n, int32_t 
  *                held inside its finite range; code = 8 + T / s rounded to the
  *                nearest whole number, ties to even, held in -8 .. 7 (8 where
  *                s is 0, and in the unused half of an odd row's last byte).
- *   vs_q4_layout the plain form in the order the scores read it (16 rows x
- *                128 columns to a block, then the scales): out is caller-owned,
+ *   vs_q4_layout the plain form in the order the scores read it (blocks
+ *                of 16 rows x 128 columns, each with its scales): out is caller-owned,
  *                vs_q4_bytes(nc, d, group) bytes, 16-byte aligned.
  *   vs_q4_scores y[q][i] = x[q] . T[i], float32[nq x nc], from the laid-out
  *                table; x is nq x d of `dtype`.  Products are exact and sums
