@@ -70,7 +70,7 @@ __global__ __launch_bounds__(256) void k_row_lookup(const T *__restrict__ table,
 // last if that unit starts inside the stretch.
 constexpr int kRun = 64;
 constexpr int kAhead = 8;        // rows in flight per lane
-constexpr int kJoinWaves = 4;
+constexpr int kJoinWaves = 8;
 
 struct Span {
     int64_t lo, hi;
@@ -198,8 +198,9 @@ __global__ __launch_bounds__(256) void k_row_lookup_bwd(
     }
 }
 
-// One workgroup per stretch in which a long unit starts: its waves take the
-// unit's pieces in turn, and the waves' sums are added in their order.
+// A workgroup looks at kJoinWaves stretches, a wave each, for long units that
+// start there (most hold none); for each it found, its waves take the unit's
+// pieces in turn, and the waves' sums are added in their order.
 template <typename O, int N>
 __global__ __launch_bounds__(kJoinWaves * 64) void k_row_lookup_join(
     int64_t n, int32_t d, const int32_t *__restrict__ ids, const int32_t *__restrict__ order,
@@ -207,41 +208,57 @@ __global__ __launch_bounds__(kJoinWaves * 64) void k_row_lookup_join(
     O *__restrict__ dT) {
     using V = Vec<float, N>;
     __shared__ V sums[kJoinWaves][64];
+    __shared__ int32_t unit[kJoinWaves];  // -1: no long unit starts in the stretch
+    __shared__ Span span[kJoinWaves];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int c = (int)blockIdx.y * 64 + lane;
     const bool in = c < d / N;
     int64_t kept = offsets[G];
     kept = kept > n ? n : kept;
-    for (int64_t s = blockIdx.x; s * kRun < kept; s += gridDim.x) {
-        const int64_t p0 = s * kRun, p1 = p0 + kRun < kept ? p0 + kRun : kept;
-        const int64_t g = unit_at(ids, order, p1 - 1, n, G);
-        if (g < 0) continue;  // uniform over the workgroup, as are the next two
-        const Span u = unit_span(offsets, g, n);
-        if (u.hi - u.lo <= kRun || u.lo < p0 || u.lo >= p1) continue;
-        const int64_t last = (u.hi - 1) / kRun;
-        V sum;
-#pragma unroll
-        for (int t = 0; t < N; ++t) sum.v[t] = 0.0f;
-        if (in)
-#pragma unroll 8
-            for (int64_t q = s + w; q <= last; q += kJoinWaves) {
-                const int64_t slot = 2 * q + (q == s && u.lo > p0 ? 1 : 0);
-                const V v = reinterpret_cast<const V *>(part + slot * d)[c];
-#pragma unroll
-                for (int t = 0; t < N; ++t) sum.v[t] += v.v[t];
+    for (int64_t s0 = (int64_t)blockIdx.x * kJoinWaves; s0 * kRun < kept;
+         s0 += (int64_t)gridDim.x * kJoinWaves) {
+        if (lane == 0) {
+            const int64_t p0 = (s0 + w) * kRun, p1 = p0 + kRun < kept ? p0 + kRun : kept;
+            int64_t g = p0 < kept ? unit_at(ids, order, p1 - 1, n, G) : -1;
+            if (g >= 0) {
+                const Span u = unit_span(offsets, g, n);
+                if (u.hi - u.lo <= kRun || u.lo < p0 || u.lo >= p1) g = -1;
+                span[w] = u;
             }
-        sums[w][lane] = sum;
-        __syncthreads();
-        if (w == 0 && in) {
-            float acc[N];
-#pragma unroll
-            for (int t = 0; t < N; ++t) {
-                acc[t] = sums[0][lane].v[t];
-                for (int v = 1; v < kJoinWaves; ++v) acc[t] += sums[v][lane].v[t];
-            }
-            store_row<O, N>(dT, g, d, c, scale, acc);
+            unit[w] = (int32_t)g;
         }
         __syncthreads();
+        for (int f = 0; f < kJoinWaves; ++f) {
+            const int64_t g = unit[f];
+            if (g < 0) continue;  // uniform over the workgroup
+            const int64_t s = s0 + f;
+            const Span u = span[f];
+            const int64_t last = (u.hi - 1) / kRun;
+            V sum;
+#pragma unroll
+            for (int t = 0; t < N; ++t) sum.v[t] = 0.0f;
+            if (in)
+#pragma unroll 8
+                for (int64_t q = s + w; q <= last; q += kJoinWaves) {
+                    const int64_t slot = 2 * q + (q == s && u.lo > s * kRun ? 1 : 0);
+                    const V v = reinterpret_cast<const V *>(part + slot * d)[c];
+#pragma unroll
+                    for (int t = 0; t < N; ++t) sum.v[t] += v.v[t];
+                }
+            sums[w][lane] = sum;
+            __syncthreads();
+            if (w == 0 && in) {
+                float acc[N];
+#pragma unroll
+                for (int t = 0; t < N; ++t) {
+                    acc[t] = sums[0][lane].v[t];
+                    for (int v = 1; v < kJoinWaves; ++v) acc[t] += sums[v][lane].v[t];
+                }
+                store_row<O, N>(dT, g, d, c, scale, acc);
+            }
+            __syncthreads();
+        }
+        __syncthreads();  // `unit` is written again in the next turn
     }
 }
 
@@ -483,8 +500,9 @@ static hipError_t lookup_bwd(const void *dY, int64_t n, int32_t d, const int32_t
     timing_after(st);
     if (n > kRun) {  // else no unit is long
         const unsigned jc = (unsigned)((vecs + 63) / 64);
+        const int64_t looks = (stretches + kJoinWaves - 1) / kJoinWaves;
         hipLaunchKernelGGL((k_row_lookup_join<O, N>),
-                           dim3((unsigned)(stretches < most ? stretches : most), jc),
+                           dim3((unsigned)(looks < most ? looks : most), jc),
                            dim3(kJoinWaves * 64), 0, st, n, d, ids, order, offsets, G, scale, part,
                            (O *)dT);
     }
