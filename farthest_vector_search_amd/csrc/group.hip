@@ -106,10 +106,10 @@ __global__ __launch_bounds__(kRankWaves * 64) void k_group_rank(
 // itself; beyond, a scan over the tiles runs in between.
 constexpr int kTileWaves = 8;
 constexpr int kTileThreads = kTileWaves * 64;
-constexpr int kTileRounds = 4;
+constexpr int kTileRounds = 2;
 constexpr int kTile = kTileThreads * kTileRounds;  // entries per workgroup
 constexpr int kMaxBits = 10;
-constexpr int kFusedTiles = 64;
+constexpr int kFusedTiles = 128;
 
 __global__ __launch_bounds__(kTileThreads) void k_group_hist(const int32_t *__restrict__ ids,
                                                              const uint32_t *__restrict__ keys,

@@ -224,6 +224,70 @@ def test_row_lookup_backward(n, G, d, kind, t):
         assert torch.equal(got, again)
 
 
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("lens", [
+    [64, 65, 63, 128, 129, 1, 0, 200, 64, 0, 64], [65], [0, 0, 64, 0], [640, 640], [1, 191, 1],
+    [63, 66, 62, 67, 126, 130], [2, 3, 4, 5, 6, 7, 8, 9, 15, 16, 17]])
+def test_row_lookup_backward_unit_lengths(lens, t):
+    """Units about the length at which they are cut, at every alignment."""
+    r = rng(15, len(lens), sum(lens))
+    ids = r.permutation(np.repeat(np.arange(len(lens)), lens)).astype(np.int32)
+    n, G = len(ids), len(lens)
+    for d in (4, 320):
+        # whole numbers below 2^8 in all: sums are exact in fp32 (not always in f16, bf16)
+        dY64 = r.integers(-4, 5, (n, d)).astype(np.float64)
+        dY = torch.from_numpy(dY64).to(t).to(dev())
+        want = np.zeros((G, d))
+        np.add.at(want, ids, dY64)
+        order, offsets, _ = vs.vs_group_rows(i32(ids), G)
+        got = vs.vs_row_lookup_backward(dY, i32(ids), order, offsets, scale=0.5,
+                                        grad_dtype=torch.float32)
+        assert np.array_equal(host(got), 0.5 * want)
+
+
+def test_empty_calls():
+    e = torch.zeros(0, dtype=torch.int32, device=dev())
+    for G in (1, 70, 5000, 300000):
+        order, offsets, slot = vs.vs_group_rows(e, G)
+        assert order.numel() == 0 and slot.numel() == 0 and not offsets.any()
+        assert offsets.numel() == G + 1
+    T = torch.ones(3, 8, device=dev())
+    assert vs.vs_row_lookup(T, e).shape == (0, 8)
+    order, offsets, slot = vs.vs_group_rows(e, 3)
+    X, w = torch.zeros(0, 8, device=dev()), torch.zeros(0, 2, device=dev())
+    assert not vs.vs_row_lookup_backward(X, e, order, offsets, out=T.clone()).any()
+    assert vs.vs_route_rows(X, slot, offsets, 2).shape == (0, 8)
+    assert vs.vs_route_rows_backward(X, slot, 2).shape == (0, 8)
+    assert vs.vs_combine_rows(X, slot, w).shape == (0, 8)
+    dYs, dw = vs.vs_combine_rows_backward(X, X, slot, w, offsets)
+    assert dYs.shape == (0, 8) and dw.shape == (0, 2)
+    c, s = vs.vs_q4_quantize(T, 32)
+    assert vs.vs_q4_scores(X, vs.vs_q4_layout(c, s, 8, 32), 3, 32).shape == (0, 3)
+
+
+def test_route_and_combine_past_32_bit_offsets():
+    d = 2048
+    n = (1 << 31) // d + 65
+    g = torch.Generator(device=dev()).manual_seed(5)
+    X = torch.empty(n, d, dtype=torch.bfloat16, device=dev()).random_(-50, 51, generator=g)
+    ids = torch.zeros(n, dtype=torch.int32, device=dev())
+    ids[5] = 1  # the last place
+    ids[9] = -1
+    order, offsets, slot = vs.vs_group_rows(ids, 2)
+    Xs = vs.vs_route_rows(X, slot, offsets, 1)
+    p = slot.long()
+    assert int(p[5]) == n - 2 and int(p[9]) == -1
+    live = torch.tensor([0, 5, 10, n // 2, n - 2, n - 1], device=dev())
+    assert torch.equal(Xs[p[live]], X[live]) and not Xs[n - 1].any()
+    w = torch.full((n, 1), 2.0, device=dev())
+    Y = vs.vs_combine_rows(Xs, slot, w, out=torch.empty_like(X))
+    assert torch.equal(Y[live], 2 * X[live]) and not Y[9].any()
+    dYs, dw = vs.vs_combine_rows_backward(X, Xs, slot, w, offsets, out=Y)
+    assert torch.equal(dYs[p[live]], 2 * X[live]) and not dYs[n - 1].any()
+    # squares below 2500, 2,048 of them: sums below 2^23, exact
+    assert torch.equal(dw[live, 0], X[live].float().square().sum(1)) and float(dw[9]) == 0
+
+
 def test_row_lookup_backward_hides_dropped_rows():
     dY = torch.ones(6, 40, device=dev())
     dY[1] = float("nan")
@@ -459,6 +523,20 @@ def test_q4_scores_query_values(t):
     x = torch.zeros(1, d, dtype=t, device=dev())
     x[0, 7] = 1.2345678
     assert float(vs.vs_q4_scores(x, table, 1, group)) == float(x[0, 7])
+
+
+def test_q4_scores_past_32_bit_offsets():
+    nc, d = (1 << 20) + 50, 4200
+    g = torch.Generator(device=dev()).manual_seed(6)
+    codes = torch.empty(nc, d // 2, dtype=torch.uint8, device=dev()).random_(0, 256, generator=g)
+    scales = torch.ones(nc, 33, dtype=torch.float16, device=dev())
+    table = vs.vs_q4_layout(codes, scales, d, 128)
+    assert table.numel() > 1 << 31
+    x64 = rng(16).integers(-3, 4, (2, d)).astype(np.float64)
+    y = vs.vs_q4_scores(torch.from_numpy(x64).to(torch.bfloat16).to(dev()), table, nc, 128)
+    for rows_ in (slice(0, 40), slice(nc - 70, nc), slice(nc // 2, nc // 2 + 30)):
+        want = x64 @ (unpack(codes[rows_], d) - 8).T
+        assert np.array_equal(host(y[:, rows_]), want)
 
 
 # ------------------------------------------------- the operators in use --
