@@ -969,18 +969,26 @@ def _rows_arg(t, name, device=None, dtype=None):
     return code
 
 
-def _same_dev(t, name, dtype, device):
-    _dev(t, name, dtype)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the other inputs on {device}")
-    return t
+_int32 = None
+
+
+def _index_arg(t, name, device):
+    """A contiguous int32 tensor on the call's device; its address."""
+    global _int32
+    if _int32 is None:
+        _int32 = _torch().int32
+    if getattr(t, "dtype", None) is not _int32 or t.device != device or not t.is_contiguous():
+        _dev(t, name, _int32)  # says what is wrong
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the other inputs on {device}")
+    return t.data_ptr()
 
 
 def _new(t, name, dtype, shape, like):
     """_out on the device of `like`; the cheaper allocation for its own type."""
     if t is not None:
         return _out(t, name, dtype, shape, like.device)
-    if dtype == like.dtype:
+    if dtype is like.dtype:
         return like.new_empty(shape)
     return like.new_empty(shape, dtype=dtype)
 
@@ -995,6 +1003,28 @@ def _scratch(nbytes: int, like, workspace):
     else:
         ws = _workspace(nbytes, like.device, workspace)
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+_current = None
+
+
+def _run(name, device, *args):
+    """Call an entry point on the device's current stream, and check it."""
+    global _current
+    if _current is None:
+        torch = _torch()
+        _current = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+                    getattr(torch._C, "_cuda_getCurrentRawStream",
+                            lambda i: torch.cuda.current_stream(i).cuda_stream))
+    get_device, raw_stream = _current
+    i = device.index
+    if i == get_device():
+        rc = getattr(_lib, name)(*args, raw_stream(i))
+    else:
+        with _torch().cuda.device(device):
+            rc = getattr(_lib, name)(*args, raw_stream(i))
+    if rc:
+        raise VsError(rc, name)
 
 
 def vs_group_rows(ids, n_groups: int, order=None, offsets=None, slot=None, workspace=None,
@@ -1014,28 +1044,22 @@ def vs_group_rows(ids, n_groups: int, order=None, offsets=None, slot=None, works
     if slot is not None or want_slot:
         slot = _new(slot, "slot", torch.int32, (n,), ids)
     ws, size, _held = _scratch(L.vs_group_rows_workspace(n, n_groups), ids, workspace)
-    with _on(dev):
-        rc = L.vs_group_rows(_ptr(ids), n, n_groups, _ptr(order), _ptr(offsets), _ptr(slot), ws,
-                             size, _stream(dev))
-    _check(rc, "vs_group_rows")
+    _run("vs_group_rows", dev, ids.data_ptr(), n, n_groups, order.data_ptr(), offsets.data_ptr(),
+         _ptr(slot), ws, size)
     return order, offsets, slot
 
 
 def vs_row_lookup(T, ids, scale: float = 1.0, out=None):
     """Rows of the table T by index: out[i] = scale * T[ids[i]], a row of zeros
     for an id outside the table.  ids may have any shape (taken flat)."""
-    torch = _torch()
-    L = lib()
+    lib()
     code = _rows_arg(T, "T")
     dev = T.device
-    _same_dev(ids, "ids", torch.int32, dev)
+    at = _index_arg(ids, "ids", dev)
     g, d = T.shape
     n = ids.numel()
     out = _new(out, "out", T.dtype, (n, d), T)
-    with _on(dev):
-        rc = L.vs_row_lookup(_ptr(T), g, d, code, _ptr(ids), n, float(scale), _ptr(out),
-                             _stream(dev))
-    _check(rc, "vs_row_lookup")
+    _run("vs_row_lookup", dev, T.data_ptr(), g, d, code, at, n, float(scale), out.data_ptr())
     return out
 
 
@@ -1045,12 +1069,11 @@ def vs_row_lookup_backward(dY, ids, order, offsets, scale: float = 1.0, grad_dty
     rows of dY whose id is g, zeros for the others.  order and offsets come
     from vs_group_rows(ids, n_groups); grad_dtype is dY's type (default) or
     torch.float32."""
-    torch = _torch()
     L = lib()
     code = _rows_arg(dY, "dY")
     dev = dY.device
-    for t, name in ((ids, "ids"), (order, "order"), (offsets, "offsets")):
-        _same_dev(t, name, torch.int32, dev)
+    ids_at, order_at, offsets_at = (_index_arg(ids, "ids", dev), _index_arg(order, "order", dev),
+                                    _index_arg(offsets, "offsets", dev))
     n, d = dY.shape
     g = offsets.numel() - 1
     if ids.numel() != n or order.numel() < n:
@@ -1059,38 +1082,31 @@ def vs_row_lookup_backward(dY, ids, order, offsets, scale: float = 1.0, grad_dty
     grad_code = _dtype(grad_dtype, "grad_dtype")
     out = _new(out, "out", grad_dtype, (max(g, 0), d), dY)
     ws, size, _held = _scratch(L.vs_row_lookup_backward_workspace(n, d), dY, workspace)
-    with _on(dev):
-        rc = L.vs_row_lookup_backward(_ptr(dY), n, d, code, _ptr(ids), _ptr(order),
-                                      _ptr(offsets), g, float(scale), grad_code, _ptr(out), ws,
-                                      size, _stream(dev))
-    _check(rc, "vs_row_lookup_backward")
+    _run("vs_row_lookup_backward", dev, dY.data_ptr(), n, d, code, ids_at, order_at, offsets_at, g,
+         float(scale), grad_code, out.data_ptr(), ws, size)
     return out
 
 
 def _slots(slot, n, k, dev):
-    torch = _torch()
-    _same_dev(slot, "slot", torch.int32, dev)
+    at = _index_arg(slot, "slot", dev)
     if slot.numel() != n * k:
         raise ValueError(f"slot holds {slot.numel()} entries, {n} rows of {k} need {n * k}")
+    return at
 
 
 def vs_route_rows(X, slot, offsets, k: int, out=None):
     """Rows sent to their units: out[slot[i * k + j]] = X[i] (n k rows in unit
     order), zeros in the rows of no unit.  slot and offsets come from
     vs_group_rows of the n x k ids."""
-    torch = _torch()
-    L = lib()
+    lib()
     code = _rows_arg(X, "X")
     dev = X.device
     n, d = X.shape
     k = int(k)
-    _slots(slot, n, k, dev)
-    _same_dev(offsets, "offsets", torch.int32, dev)
+    slot_at, offsets_at = _slots(slot, n, k, dev), _index_arg(offsets, "offsets", dev)
     out = _new(out, "out", X.dtype, (n * k, d), X)
-    with _on(dev):
-        rc = L.vs_route_rows(_ptr(X), n, d, code, _ptr(slot), _ptr(offsets),
-                             offsets.numel() - 1, k, _ptr(out), _stream(dev))
-    _check(rc, "vs_route_rows")
+    _run("vs_route_rows", dev, X.data_ptr(), n, d, code, slot_at, offsets_at, offsets.numel() - 1, k,
+         out.data_ptr())
     return out
 
 
@@ -1104,12 +1120,9 @@ def vs_route_rows_backward(dXs, slot, k: int, out=None):
     if k < 1 or m % k:
         raise ValueError(f"dXs must hold k = {k} rows per row")
     n = m // k
-    _slots(slot, n, k, dev)
+    slot_at = _slots(slot, n, k, dev)
     out = _new(out, "out", dXs.dtype, (n, d), dXs)
-    with _on(dev):
-        rc = L.vs_route_rows_backward(_ptr(dXs), n, d, code, _ptr(slot), k, _ptr(out),
-                                      _stream(dev))
-    _check(rc, "vs_route_rows_backward")
+    _run("vs_route_rows_backward", dev, dXs.data_ptr(), n, d, code, slot_at, k, out.data_ptr())
     return out
 
 
@@ -1125,12 +1138,10 @@ def vs_combine_rows(Ys, slot, weights, out=None):
     d = Ys.shape[1]
     if Ys.shape[0] != n * k:
         raise ValueError("Ys must hold one row per entry of weights")
-    _slots(slot, n, k, dev)
+    slot_at = _slots(slot, n, k, dev)
     out = _new(out, "out", Ys.dtype, (n, d), Ys)
-    with _on(dev):
-        rc = L.vs_combine_rows(_ptr(Ys), n, d, code, _ptr(slot), _ptr(weights), k, _ptr(out),
-                               _stream(dev))
-    _check(rc, "vs_combine_rows")
+    _run("vs_combine_rows", dev, Ys.data_ptr(), n, d, code, slot_at, weights.data_ptr(), k,
+         out.data_ptr())
     return out
 
 
@@ -1148,15 +1159,12 @@ def vs_combine_rows_backward(dY, Ys, slot, weights, offsets, out=None, dweights=
     d = dY.shape[1]
     if dY.shape[0] != n or tuple(Ys.shape) != (n * k, d):
         raise ValueError("dY must be n x d and Ys (n * k) x d for weights n x k")
-    _slots(slot, n, k, dev)
-    _same_dev(offsets, "offsets", torch.int32, dev)
+    slot_at, offsets_at = _slots(slot, n, k, dev), _index_arg(offsets, "offsets", dev)
     out = _new(out, "out", dY.dtype, (n * k, d), dY)
     dweights = _new(dweights, "dweights", torch.float32, (n, k), weights)
-    with _on(dev):
-        rc = L.vs_combine_rows_backward(_ptr(dY), _ptr(Ys), n, d, code, _ptr(slot),
-                                        _ptr(weights), _ptr(offsets), offsets.numel() - 1, k,
-                                        _ptr(out), _ptr(dweights), _stream(dev))
-    _check(rc, "vs_combine_rows_backward")
+    _run("vs_combine_rows_backward", dev, dY.data_ptr(), Ys.data_ptr(), n, d, code, slot_at,
+         weights.data_ptr(), offsets_at, offsets.numel() - 1, k, out.data_ptr(),
+         dweights.data_ptr())
     return out, dweights
 
 
@@ -1181,10 +1189,8 @@ def vs_q4_quantize(T, group: int = 32, scale_dtype=None, codes=None, scales=None
     scale_code = _dtype(scale_dtype, "scale_dtype")
     codes = _new(codes, "codes", torch.uint8, (nc, (d + 1) // 2), T)
     scales = _new(scales, "scales", scale_dtype, (nc, (d + group - 1) // group), T)
-    with _on(dev):
-        rc = L.vs_q4_quantize(_ptr(T), nc, d, code, group, scale_code, _ptr(codes),
-                              _ptr(scales), _stream(dev))
-    _check(rc, "vs_q4_quantize")
+    _run("vs_q4_quantize", dev, T.data_ptr(), nc, d, code, group, scale_code, codes.data_ptr(),
+         scales.data_ptr())
     return codes, scales
 
 
@@ -1203,9 +1209,7 @@ def vs_q4_layout(codes, scales, d: int, group: int = 32, out=None):
     if codes.shape[1] != (d + 1) // 2 or tuple(scales.shape) != (nc, (d + group - 1) // group):
         raise ValueError(f"codes and scales disagree with {nc} rows of {d} in groups of {group}")
     out = _new(out, "out", torch.uint8, (L.vs_q4_bytes(nc, d, group),), codes)
-    with _on(dev):
-        rc = L.vs_q4_layout(_ptr(codes), _ptr(scales), nc, d, group, _ptr(out), _stream(dev))
-    _check(rc, "vs_q4_layout")
+    _run("vs_q4_layout", dev, codes.data_ptr(), scales.data_ptr(), nc, d, group, out.data_ptr())
     return out
 
 
@@ -1217,7 +1221,9 @@ def vs_q4_scores(x, table, nc: int, group: int = 32, scale_dtype=None, out=None)
     L = lib()
     code = _rows_arg(x, "x")
     dev = x.device
-    _same_dev(table, "table", torch.uint8, dev)
+    _dev(table, "table", torch.uint8)
+    if table.device != dev:
+        raise ValueError(f"table is on {table.device}, x on {dev}")
     nq, d = x.shape
     nc, group = int(nc), _q4_group(group)
     scale_dtype = torch.float16 if scale_dtype is None else scale_dtype
@@ -1226,10 +1232,8 @@ def vs_q4_scores(x, table, nc: int, group: int = 32, scale_dtype=None, out=None)
         raise ValueError(f"table holds {table.numel()} bytes, {nc} rows of {d} take {need}")
     scale_code = _dtype(scale_dtype, "scale_dtype")
     out = _new(out, "out", torch.float32, (nq, nc), x)
-    with _on(dev):
-        rc = L.vs_q4_scores(_ptr(x), nq, d, code, _ptr(table), nc, group, scale_code, _ptr(out),
-                            _stream(dev))
-    _check(rc, "vs_q4_scores")
+    _run("vs_q4_scores", dev, x.data_ptr(), nq, d, code, table.data_ptr(), nc, group, scale_code,
+         out.data_ptr())
     return out
 
 

@@ -79,13 +79,15 @@ __global__ __launch_bounds__(256) void k_q4_quantize(const T *__restrict__ table
 }
 
 // ---- layout: plain codes and scales into blocks ------------------------------
+//
+// words: every row of codes starts on a 4-byte boundary.
 
 constexpr int block_bytes(int per) { return 1024 + kBlockRows * 2 * per; }  // per: groups a block
 
 __global__ __launch_bounds__(256) void k_q4_layout(const uint8_t *__restrict__ codes,
                                                    const uint16_t *__restrict__ scales, int64_t nc,
                                                    int32_t d, int group, int64_t nrb, int64_t ncb,
-                                                   uint8_t *__restrict__ out) {
+                                                   uint8_t *__restrict__ out, int words) {
     const int64_t bytes = ((int64_t)d + 1) / 2;
     const int per = kBlockCols / group;
     const int64_t groups = (d + group - 1) / group;
@@ -96,14 +98,23 @@ __global__ __launch_bounds__(256) void k_q4_layout(const uint8_t *__restrict__ c
         const int lane = (int)threadIdx.x >> 2, t = (int)threadIdx.x & 3;
         const int64_t row = rb * kBlockRows + (lane & 15);
         const int64_t k0 = cb * kBlockCols + 32 * t + 8 * (lane >> 4);
+        uint32_t plain = 0x88888888u;  // columns k0 .. k0 + 7, four bits each; 8 stands for 0
+        if (row < nc && k0 < d) {
+            const uint8_t *from = codes + row * bytes + k0 / 2;
+            if (words && k0 + 8 <= d) {
+                plain = *reinterpret_cast<const uint32_t *>(from);
+            } else {
+                plain = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    plain |= (k0 + e < d ? (uint32_t)(from[e / 2] >> (4 * (e & 1))) & 15 : 8u)
+                             << (4 * e);
+            }
+        }
         uint32_t w = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            uint32_t c = 8;  // stands for 0
-            if (row < nc && k0 + e < d)
-                c = (codes[row * bytes + (k0 + e) / 2] >> (4 * (e & 1))) & 15;
-            w |= c << (4 * (e >> 1) + 16 * (e & 1));
-        }
+        for (int e = 0; e < 8; ++e)
+            w |= ((plain >> (4 * e)) & 15) << (4 * (e >> 1) + 16 * (e & 1));
         reinterpret_cast<uint32_t *>(to)[threadIdx.x] = w;
         if ((int)threadIdx.x < per * kBlockRows) {
             const int in = threadIdx.x;
@@ -612,7 +623,8 @@ hipError_t launch_q4_layout(const uint8_t *codes, const void *scales, int64_t nc
     const int64_t nrb = row_blocks(nc), ncb = col_blocks(d);
     const int64_t most = (int64_t)n_cu * 64, want = nrb * ncb;
     hipLaunchKernelGGL(k_q4_layout, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st,
-                       codes, (const uint16_t *)scales, nc, d, group, nrb, ncb, (uint8_t *)out);
+                       codes, (const uint16_t *)scales, nc, d, group, nrb, ncb, (uint8_t *)out,
+                       (int)(((d + 1) / 2) % 4 == 0 && (reinterpret_cast<uintptr_t>(codes) & 3) == 0));
     return hipGetLastError();
 }
 
