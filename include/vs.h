@@ -5,6 +5,9 @@
  * table -- nearest or farthest by squared Euclidean distance, or most/least
  * similar by cosine on unit-norm rows -- optionally skipping candidates a
  * per-query bit mask excludes, with the lowest candidate index winning ties.
+ * The table operators (vs_group_rows and below) take the indices and the
+ * table further: rows by index and by unit, their gradients, and scores over
+ * a table held in 4 bits.
  *
  * Sources (web pages, cited by title and section):
  *  [BMU] "From 80x to 385x: A Best-Matching-Unit Search at the L2 Roof,
@@ -502,7 +505,7 @@ int vs_row_lookup_backward(const void *dY, int64_t n, int32_t d, int32_t dtype,
  *                             set to zero) and dweights[e] = dY[i] .
  *                             Ys[slot[e]], 0 for a dropped entry.
  * X, Y, dX, dY are n x d, Xs, Ys, dXs, dYs m x d, all of `dtype`; weights and
- * dweights float32[m].  What belongs to a dropped entry is never read.  Sums
+ * dweights float32[m].  What belongs to a dropped entry is never used.  Sums
  * are fp32, over j in order, and rounded once.  n k <= 2^31-1, k in [1, 1024],
  * n_groups in [1, 2^31-2], d in [1, 2^20]; n == 0 is a no-op.  A slot outside
  * [-1, m) is taken as dropped.  Inputs and outputs must not overlap.
