@@ -63,13 +63,18 @@ __global__ __launch_bounds__(256) void k_row_lookup(const T *__restrict__ table,
 //
 // The sorted order cuts into one run of rows per unit, summed by the lanes of
 // one unit.  Units differ widely in length (padding, common tokens), so one
-// with more than kRun rows is cut at multiples of kRun places: each piece's
+// with more than `run` rows is cut at multiples of `run` places: each piece's
 // sum goes to the workspace in fp32 and a second kernel adds a unit's pieces,
 // always in the same order.  A long unit covers the first or the last place
-// of every stretch of kRun places it touches, so a stretch holds at most two
+// of every stretch of `run` places it touches, so a stretch holds at most two
 // pieces: part 0 of the unit at its first place, part 1 of the one at its
 // last if that unit starts inside the stretch.
-constexpr int kRun = 64;
+//
+// run is 64, and 16 for few rows, where a long unit's rows would come one
+// behind the other with the GPU idle (1,023 x 257 f16 rows into 1,000 units:
+// the first kernel 5.5 us with 16, 9.3 us
+// with 64).
+inline int run_of(int64_t n) { return n <= 4096 ? 16 : 64; }
 constexpr int kAhead = 8;        // rows in flight per lane
 constexpr int kJoinWaves = 8;
 
@@ -154,7 +159,7 @@ template <typename T, typename O, int N>
 __global__ __launch_bounds__(256) void k_row_lookup_bwd(
     const T *__restrict__ dY, int64_t n, int32_t d, const int32_t *__restrict__ ids,
     const int32_t *__restrict__ order, const int32_t *__restrict__ offsets, int64_t G, float scale,
-    O *__restrict__ dT, float *__restrict__ part, unsigned piece_blocks, int lsh,
+    O *__restrict__ dT, float *__restrict__ part, int run, unsigned piece_blocks, int lsh,
     unsigned cols) {
     const int lane = threadIdx.x & ((1 << lsh) - 1);
     const int per = 256 >> lsh;
@@ -165,17 +170,17 @@ __global__ __launch_bounds__(256) void k_row_lookup_bwd(
         const int64_t step = (int64_t)piece_blocks * per;
         for (int64_t item = (int64_t)blockIdx.x * per + (threadIdx.x >> lsh);; item += step) {
             const int64_t s = item / cols;
-            if (s * kRun >= kept) break;
+            if (s * run >= kept) break;
             const int c = ((int)(item - s * cols) << lsh) + lane;
             if (c >= vecs) continue;
-            const int64_t p0 = s * kRun, p1 = p0 + kRun < kept ? p0 + kRun : kept;
+            const int64_t p0 = s * run, p1 = p0 + run < kept ? p0 + run : kept;
             const int64_t g0 = unit_at(ids, order, p0, n, G);
             const int64_t g1 = unit_at(ids, order, p1 - 1, n, G);
             for (int b = 0; b < 2; ++b) {
                 const int64_t g = b ? g1 : g0;
                 if (g < 0 || (b && g1 == g0)) continue;
                 Span u = unit_span(offsets, g, n);
-                if (u.hi - u.lo <= kRun) continue;
+                if (u.hi - u.lo <= run) continue;
                 u.lo = u.lo > p0 ? u.lo : p0;
                 u.hi = u.hi < p1 ? u.hi : p1;
                 float acc[N] = {};
@@ -196,7 +201,7 @@ __global__ __launch_bounds__(256) void k_row_lookup_bwd(
         const int c = ((int)(item - g * cols) << lsh) + lane;
         if (c >= vecs) continue;
         const Span u = unit_span(offsets, g, n);
-        if (u.hi - u.lo > kRun) continue;
+        if (u.hi - u.lo > run) continue;
         float acc[N] = {};
         sum_rows<T, N>(dY, n, d, order, u, c, acc);
         store_row<O, N>(dT, g, d, c, u.hi > u.lo ? scale : 0.0f, acc);
@@ -210,7 +215,7 @@ template <typename O, int N>
 __global__ __launch_bounds__(kJoinWaves * 64) void k_row_lookup_join(
     int64_t n, int32_t d, const int32_t *__restrict__ ids, const int32_t *__restrict__ order,
     const int32_t *__restrict__ offsets, int64_t G, float scale, const float *__restrict__ part,
-    O *__restrict__ dT) {
+    int run, O *__restrict__ dT) {
     using V = Vec<float, N>;
     __shared__ V sums[kJoinWaves][64];
     __shared__ int32_t unit[kJoinWaves];  // -1: no long unit starts in the stretch
@@ -220,14 +225,14 @@ __global__ __launch_bounds__(kJoinWaves * 64) void k_row_lookup_join(
     const bool in = c < d / N;
     int64_t kept = offsets[G];
     kept = kept > n ? n : kept;
-    for (int64_t s0 = (int64_t)blockIdx.x * kJoinWaves; s0 * kRun < kept;
+    for (int64_t s0 = (int64_t)blockIdx.x * kJoinWaves; s0 * run < kept;
          s0 += (int64_t)gridDim.x * kJoinWaves) {
         if (lane == 0) {
-            const int64_t p0 = (s0 + w) * kRun, p1 = p0 + kRun < kept ? p0 + kRun : kept;
+            const int64_t p0 = (s0 + w) * run, p1 = p0 + run < kept ? p0 + run : kept;
             int64_t g = p0 < kept ? unit_at(ids, order, p1 - 1, n, G) : -1;
             if (g >= 0) {
                 const Span u = unit_span(offsets, g, n);
-                if (u.hi - u.lo <= kRun || u.lo < p0 || u.lo >= p1) g = -1;
+                if (u.hi - u.lo <= run || u.lo < p0 || u.lo >= p1) g = -1;
                 span[w] = u;
             }
             unit[w] = (int32_t)g;
@@ -238,14 +243,14 @@ __global__ __launch_bounds__(kJoinWaves * 64) void k_row_lookup_join(
             if (g < 0) continue;  // uniform over the workgroup
             const int64_t s = s0 + f;
             const Span u = span[f];
-            const int64_t last = (u.hi - 1) / kRun;
+            const int64_t last = (u.hi - 1) / run;
             V sum;
 #pragma unroll
             for (int t = 0; t < N; ++t) sum.v[t] = 0.0f;
             if (in)
 #pragma unroll 8
                 for (int64_t q = s + w; q <= last; q += kJoinWaves) {
-                    const int64_t slot = 2 * q + (q == s && u.lo > s * kRun ? 1 : 0);
+                    const int64_t slot = 2 * q + (q == s && u.lo > s * run ? 1 : 0);
                     const V v = reinterpret_cast<const V *>(part + slot * d)[c];
 #pragma unroll
                     for (int t = 0; t < N; ++t) sum.v[t] += v.v[t];
@@ -501,10 +506,11 @@ hipError_t launch_row_lookup(const void *table, int64_t G, int32_t d, int dtype,
     });
 }
 
-// Two fp32 rows per stretch of kRun places; none where no unit can be long.
+// Two fp32 rows per stretch of run_of(n) places; none where no unit can be long.
 size_t row_lookup_bwd_workspace(int64_t n, int32_t d) {
-    if (n <= kRun) return 0;
-    const size_t stretches = (size_t)((n + kRun - 1) / kRun);
+    const int run = run_of(n);
+    if (n <= run) return 0;
+    const size_t stretches = (size_t)((n + run - 1) / run);
     return stretches * 2 * (size_t)d * 4;
 }
 
@@ -526,23 +532,24 @@ static hipError_t lookup_bwd(const void *dY, int64_t n, int32_t d, const int32_t
         if (idle_lanes(vecs, less) < idle_lanes(vecs, lsh)) lsh = less;
     const int per = 256 >> lsh;
     const unsigned cols = (unsigned)((vecs + (1 << lsh) - 1) >> lsh);
-    const int64_t stretches = (n + kRun - 1) / kRun, most = (int64_t)n_cu * 32;
+    const int run = run_of(n);
+    const int64_t stretches = (n + run - 1) / run, most = (int64_t)n_cu * 32;
     const int64_t pb = (stretches * cols + per - 1) / per;
     const int64_t ub = (G * cols + per - 1) / per;
     const unsigned pieces = (unsigned)(pb < most ? pb : most);
     const unsigned units = (unsigned)(ub < most ? ub : most);
     timing_before(st, "k_row_lookup_bwd");
     hipLaunchKernelGGL((k_row_lookup_bwd<T, O, N>), dim3(pieces + units), dim3(256), 0, st,
-                       (const T *)dY, n, d, ids, order, offsets, G, scale, (O *)dT, part, pieces,
+                       (const T *)dY, n, d, ids, order, offsets, G, scale, (O *)dT, part, run, pieces,
                        lsh, cols);
     timing_after(st);
-    if (n > kRun) {  // else no unit is long
+    if (n > run) {  // else no unit is long
         const unsigned jc = (unsigned)((vecs + 63) / 64);
         const int64_t looks = (stretches + kJoinWaves - 1) / kJoinWaves;
         hipLaunchKernelGGL((k_row_lookup_join<O, N>),
                            dim3((unsigned)(looks < most ? looks : most), jc),
                            dim3(kJoinWaves * 64), 0, st, n, d, ids, order, offsets, G, scale, part,
-                           (O *)dT);
+                           run, (O *)dT);
     }
     return hipGetLastError();
 }

@@ -77,9 +77,11 @@ def test_row_lookup_backward(L):
         assert call(**bad) == SHAPE
     for name in ("dY", "ids", "order", "offsets", "dT"):
         assert call(**{name: 0}) == NULL
-    assert call(n=65, ws=0) == NULL     # units of more than 64 rows may occur
-    assert L.vs_row_lookup_backward_workspace(64, 8) == 0
-    assert L.vs_row_lookup_backward_workspace(65, 8) == 4 * 8 * 4
+    # two float32 rows per 16 rows (64 beyond 4,096 rows), none up to 16
+    assert call(n=17, ws=0) == NULL
+    assert L.vs_row_lookup_backward_workspace(16, 8) == 0
+    assert L.vs_row_lookup_backward_workspace(17, 8) == 2 * 2 * 8 * 4
+    assert L.vs_row_lookup_backward_workspace(4097, 8) == 65 * 2 * 8 * 4
     assert call(n=0, dY=0, ids=0, order=0, dT=0) == NULL  # the gradient is still written
     for name in ("ids", "order", "offsets"):
         assert call(**{name: FAKE + 2}) == ALIGN

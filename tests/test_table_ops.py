@@ -227,7 +227,8 @@ def test_row_lookup_backward(n, G, d, kind, t):
 @pytest.mark.parametrize("t", TYPES)
 @pytest.mark.parametrize("lens", [
     [64, 65, 63, 128, 129, 1, 0, 200, 64, 0, 64], [65], [0, 0, 64, 0], [640, 640], [1, 191, 1],
-    [63, 66, 62, 67, 126, 130], [2, 3, 4, 5, 6, 7, 8, 9, 15, 16, 17]])
+    [63, 66, 62, 67, 126, 130], [2, 3, 4, 5, 6, 7, 8, 9, 15, 16, 17], [17], [16, 17, 15, 32, 33],
+    [64, 65, 63, 128, 129, 1, 0, 200, 64, 0, 64] * 6, [4097], [1, 5000, 1]])
 def test_row_lookup_backward_unit_lengths(lens, t):
     """Units about the length at which they are cut, at every alignment."""
     r = rng(15, len(lens), sum(lens))
