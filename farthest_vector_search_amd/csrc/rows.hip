@@ -72,8 +72,7 @@ __global__ __launch_bounds__(256) void k_row_lookup(const T *__restrict__ table,
 //
 // run is 64, and 16 for few rows, where a long unit's rows would come one
 // behind the other with the GPU idle (1,023 x 257 f16 rows into 1,000 units:
-// the first kernel 5.5 us with 16, 9.3 us
-// with 64).
+// the first kernel 5.5 us with 16, 9.3 us with 64).
 inline int run_of(int64_t n) { return n <= 4096 ? 16 : 64; }
 constexpr int kAhead = 8;        // rows in flight per lane
 constexpr int kJoinWaves = 8;
