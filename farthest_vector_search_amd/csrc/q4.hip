@@ -262,8 +262,8 @@ __device__ __forceinline__ int frag_place(int chunk, int ct, int c) {
 // its segment with kBlocksAhead blocks in flight and no barrier.  A row block
 // cut by a segment's border is finished by the wave that began it, from the
 // parts (heads) the next waves leave in LDS, added in their order.  Bound by
-// the stream: 65,536 x 4,096 (group 128) for 16 f16 queries 32.8 us, 4.5 TB/s;
-// 262,144 x 256 (group 32) for one bf16 query 10.1 us, 3.8 TB/s, of which about
+// the stream: 65,536 x 4,096 (group 128) for 16 f16 queries 32.0 us, 4.6 TB/s;
+// 262,144 x 256 (group 32) for one bf16 query 10.0 us, 3.9 TB/s, of which about
 // 4 us are the launch, the staging and the first blocks.  8 waves and twice the
 // workgroups took 48 us of 33 (the queries staged twice), 3 or 4 blocks ahead
 // gained nothing.
