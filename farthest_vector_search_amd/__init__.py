@@ -1178,7 +1178,8 @@ def _q4_group(group):
 def vs_q4_quantize(T, group: int = 32, scale_dtype=None, codes=None, scales=None):
     """4-bit codes and group scales of the table T (nc x d): (codes uint8
     [nc, ceil(d / 2)], scales [nc, ceil(d / group)] of torch.float16 (default)
-    or torch.bfloat16); T[i, k] ~ scales[i, k // group] * (code - 8)."""
+    or torch.bfloat16); T[i, k] ~ scales[i, k // group] * (code - 8).  A group
+    that holds a NaN gets a NaN scale."""
     torch = _torch()
     L = lib()
     code = _rows_arg(T, "T")

@@ -44,7 +44,13 @@ inline int64_t col_blocks(int64_t d) { return (d + kBlockCols - 1) / kBlockCols;
 //
 // One lane per two columns (a byte of codes); the lanes of a group share its
 // largest magnitude.  s = max / 7 rounded to the scale type and held inside
-// its finite range; c = rint(v / s) held in -8 .. 7, ties to even, plus 8.
+// its finite range; c = rint(v / s) held in -8 .. 7, ties to even, plus 8.  No
+// code stands for a NaN, so a group that holds one gets a NaN for its scale
+// (and codes of 8): its row's scores are NaN, as the row's products are.
+__device__ __forceinline__ float larger(float a, float b) {  // a NaN if either is one
+    return a >= b || a != a ? a : b;
+}
+
 template <typename T, typename S>
 __global__ __launch_bounds__(256) void k_q4_quantize(const T *__restrict__ table, int64_t nc,
                                                      int32_t d, int group,
@@ -64,9 +70,9 @@ __global__ __launch_bounds__(256) void k_q4_quantize(const T *__restrict__ table
         const T *src = table + row * d;
         const float v0 = k < d ? widen(src[k]) : 0.0f;
         const float v1 = k + 1 < d ? widen(src[k + 1]) : 0.0f;
-        float m = fmaxf(fabsf(v0), fabsf(v1));
-        for (int s = 1; s < lanes; s <<= 1) m = fmaxf(m, __shfl_xor(m, s));
-        const S sc = narrow<S>(fminf(m / 7.0f, top));
+        float m = larger(fabsf(v0), fabsf(v1));
+        for (int s = 1; s < lanes; s <<= 1) m = larger(m, __shfl_xor(m, s));
+        const S sc = narrow<S>(m / 7.0f > top ? top : m / 7.0f);
         const float s = widen(sc);
         int c0 = 8, c1 = 8;
         if (s > 0.0f) {

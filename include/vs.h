@@ -533,6 +533,9 @@ int vs_combine_rows_backward(const void *dY, const void *Ys, int64_t n, int32_t 
  *                held inside its finite range; code = 8 + T / s rounded to the
  *                nearest whole number, ties to even, held in -8 .. 7 (8 where
  *                s is 0, and in the unused half of an odd row's last byte).
+ *                A group that holds a NaN gets a NaN scale and codes of 8, so
+ *                that every score of its row is NaN; an infinity gets
+ *                the last code of its sign.
  *   vs_q4_layout the plain form in the order the scores read it (blocks
  *                of 16 rows x 128 columns, each with its scales): out is caller-owned,
  *                vs_q4_bytes(nc, d, group) bytes, 16-byte aligned.

@@ -1,0 +1,47 @@
+"""Table operators on the GPU at the values, sizes and addresses where they could
+go wrong, against plain implementations in 64 bits (tolerances as derived in
+test_table_ops)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import farthest_vector_search_amd as vs  # noqa: E402
+from test_table_ops import TYPES, rng, rows, unpack  # noqa: E402
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("st", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_q4_quantize_keeps_a_nan(group, st, t):
+    """A group that holds a NaN (alone, filled with them, in the cut last group,
+    next to an infinity) gets a NaN scale, its row NaN scores; no other group
+    changes."""
+    r = rng(20, group)
+    d = 2 * group + 5
+    T, _ = rows(r, (8, d), t)
+    nan = float("nan")
+    T[0, 0] = nan
+    T[1, group - 1] = nan
+    T[2, group + group // 2 + 1] = nan
+    T[3, :group] = nan
+    T[4, 2 * group:] = nan
+    T[5, d - 1] = nan
+    T[6, 3], T[6, 4] = float("inf"), nan
+    held = [(0, 0), (1, 0), (2, 1), (3, 0), (4, 2), (5, 2), (6, 0)]
+    codes, scales = vs.vs_q4_quantize(T, group, st)
+    bad = torch.zeros(8, 3, dtype=torch.bool)
+    for at in held:
+        bad[at] = True
+    assert torch.equal(torch.isnan(scales).cpu(), bad)
+    got = unpack(codes, d)
+    over = np.repeat(bad.numpy(), group, 1)[:, :d]
+    assert (got[over] == 8).all()
+    plain_codes, plain_scales = vs.vs_q4_quantize(torch.nan_to_num(T, 0.0, 1.0, -1.0), group, st)
+    assert torch.equal(scales.cpu()[~bad], plain_scales.cpu()[~bad])
+    assert np.array_equal(got[~over], unpack(plain_codes, d)[~over])
+    x, _ = rows(r, (2, d), t)
+    table = vs.vs_q4_layout(codes, scales, d, group)
+    y = vs.vs_q4_scores(x, table, 8, group, st)
+    assert torch.isnan(y[:, :7]).all() and torch.isfinite(y[:, 7]).all()
