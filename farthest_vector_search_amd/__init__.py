@@ -1197,7 +1197,10 @@ def vs_q4_quantize(T, group: int = 32, scale_dtype=None, codes=None, scales=None
 
 def vs_q4_layout(codes, scales, d: int, group: int = 32, out=None):
     """The laid-out table vs_q4_scores reads, from plain codes and scales (of
-    vs_q4_quantize, or a stored model's): a flat uint8 tensor."""
+    vs_q4_quantize, or a stored model's): a flat tensor of bytes, torch.uint8
+    for float16 scales and torch.int8 for bfloat16 ones, by which vs_q4_scores
+    tells them apart (copies and saved tables keep it).  out may be either; pass
+    on what is returned, which shares its memory and has the scales' type."""
     torch = _torch()
     L = lib()
     _dev(codes, "codes", torch.uint8, 2)
@@ -1209,25 +1212,33 @@ def vs_q4_layout(codes, scales, d: int, group: int = 32, out=None):
     nc, d, group = codes.shape[0], int(d), _q4_group(group)
     if codes.shape[1] != (d + 1) // 2 or tuple(scales.shape) != (nc, (d + group - 1) // group):
         raise ValueError(f"codes and scales disagree with {nc} rows of {d} in groups of {group}")
-    out = _new(out, "out", torch.uint8, (L.vs_q4_bytes(nc, d, group),), codes)
+    made = torch.uint8 if scales.dtype == torch.float16 else torch.int8
+    given = torch.int8 if getattr(out, "dtype", None) == torch.int8 else torch.uint8
+    out = _new(out, "out", given, (L.vs_q4_bytes(nc, d, group),), codes)
     _run("vs_q4_layout", dev, codes.data_ptr(), scales.data_ptr(), nc, d, group, out.data_ptr())
-    return out
+    return out if out.dtype == made else out.view(made)
 
 
 def vs_q4_scores(x, table, nc: int, group: int = 32, scale_dtype=None, out=None):
     """Scores [nq, nc] (float32) of the queries x (nq x d) over a table of nc
-    rows laid out by vs_q4_layout with this group and scale type (default
-    torch.float16)."""
+    rows laid out by vs_q4_layout with this group.  scale_dtype defaults to
+    what the table's element type says (see vs_q4_layout); a torch.uint8 table
+    may be said to hold torch.bfloat16 scales, a torch.int8 one holds no
+    others."""
     torch = _torch()
     L = lib()
     code = _rows_arg(x, "x")
     dev = x.device
-    _dev(table, "table", torch.uint8)
+    bf16 = getattr(table, "dtype", None) is torch.int8
+    _dev(table, "table", torch.int8 if bf16 else torch.uint8)
     if table.device != dev:
         raise ValueError(f"table is on {table.device}, x on {dev}")
     nq, d = x.shape
     nc, group = int(nc), _q4_group(group)
-    scale_dtype = torch.float16 if scale_dtype is None else scale_dtype
+    if scale_dtype is None:
+        scale_dtype = torch.bfloat16 if bf16 else torch.float16
+    elif bf16 and scale_dtype != torch.bfloat16:
+        raise ValueError(f"table was laid out with bfloat16 scales, scale_dtype is {scale_dtype}")
     need = L.vs_q4_bytes(nc, d, group)
     if table.numel() != need:
         raise ValueError(f"table holds {table.numel()} bytes, {nc} rows of {d} take {need}")

@@ -8,7 +8,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import farthest_vector_search_amd as vs  # noqa: E402
-from test_table_ops import TYPES, rng, rows, unpack  # noqa: E402
+from test_table_ops import TYPES, dev, rng, rows, unpack  # noqa: E402
 
 
 @pytest.mark.parametrize("t", TYPES)
@@ -45,3 +45,26 @@ def test_q4_quantize_keeps_a_nan(group, st, t):
     table = vs.vs_q4_layout(codes, scales, d, group)
     y = vs.vs_q4_scores(x, table, 8, group, st)
     assert torch.isnan(y[:, :7]).all() and torch.isfinite(y[:, 7]).all()
+
+
+@pytest.mark.parametrize("t", TYPES)
+def test_q4_scores_scale_type(t):
+    """The laid-out table carries its scales' type, also through copies and views;
+    another one asked for is refused.  Plain bytes are taken as the caller says."""
+    r = rng(21)
+    nc, d = 50, 160
+    T, _ = rows(r, (nc, d), torch.float32)
+    x, _ = rows(r, (3, d), t)
+    for st in (torch.float16, torch.bfloat16):
+        codes, scales = vs.vs_q4_quantize(T, 32, st)
+        table = vs.vs_q4_layout(codes, scales, d, 32)
+        want = vs.vs_q4_scores(x, table, nc, 32, st)
+        for same in (table, table.clone(), table[:]):
+            assert torch.equal(vs.vs_q4_scores(x, same, nc, 32), want)
+    with pytest.raises(ValueError, match="scale"):
+        vs.vs_q4_scores(x, table, nc, 32, torch.float16)
+    buf = torch.empty(table.numel(), dtype=torch.uint8, device=dev())
+    again = vs.vs_q4_layout(codes, scales, d, 32, out=buf)
+    assert again.data_ptr() == buf.data_ptr()
+    assert torch.equal(vs.vs_q4_scores(x, again, nc, 32), want)
+    assert torch.equal(vs.vs_q4_scores(x, buf, nc, 32, torch.bfloat16), want)
