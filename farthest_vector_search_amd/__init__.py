@@ -4,7 +4,9 @@ Argument marshalling only: every step of every search runs in the HIP
 kernels of ``libvs.so``, called through its C ABI (``include/vs.h``) on the
 current torch stream.  PyTorch supplies device memory and streams.  There is
 no CPU fallback: if the library is missing or no gfx950 GPU is present the
-calls raise.
+calls raise.  Results are outside autograd: gradients come from the *_backward
+calls, and a call that has one, or the 4-bit scores, warns when gradients are
+being recorded and an input requires one.
 
 Functions (same names as the C entry points):
     vs_bmu_search(Q, C, metric)                        -> (idx, score)
@@ -37,6 +39,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import warnings
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libvs.so")
@@ -1027,6 +1030,17 @@ def _run(name, device, *args):
         raise VsError(rc, name)
 
 
+def _outside_autograd(name, *inputs):
+    """The library's calls record nothing for autograd: say so where one is
+    given a tensor that wants its gradient."""
+    for t in inputs:
+        if t.requires_grad and _torch().is_grad_enabled():
+            warnings.warn(f"{name}: an input requires a gradient, but the result is outside "
+                          "autograd (gradients come from the *_backward calls; call this one "
+                          "under torch.no_grad() or in a torch.autograd.Function)", stacklevel=3)
+            return
+
+
 def vs_group_rows(ids, n_groups: int, order=None, offsets=None, slot=None, workspace=None,
                   want_slot: bool = True):
     """Entries grouped by unit: a stable sort of the int32 ids (any shape, taken
@@ -1056,6 +1070,7 @@ def vs_row_lookup(T, ids, scale: float = 1.0, out=None):
     code = _rows_arg(T, "T")
     dev = T.device
     at = _index_arg(ids, "ids", dev)
+    _outside_autograd("vs_row_lookup", T)
     g, d = T.shape
     n = ids.numel()
     out = _new(out, "out", T.dtype, (n, d), T)
@@ -1078,6 +1093,7 @@ def vs_row_lookup_backward(dY, ids, order, offsets, scale: float = 1.0, grad_dty
     g = offsets.numel() - 1
     if ids.numel() != n or order.numel() < n:
         raise ValueError("ids and order must hold one entry per row of dY")
+    _outside_autograd("vs_row_lookup_backward", dY)
     grad_dtype = dY.dtype if grad_dtype is None else grad_dtype
     grad_code = _dtype(grad_dtype, "grad_dtype")
     out = _new(out, "out", grad_dtype, (max(g, 0), d), dY)
@@ -1104,6 +1120,7 @@ def vs_route_rows(X, slot, offsets, k: int, out=None):
     n, d = X.shape
     k = int(k)
     slot_at, offsets_at = _slots(slot, n, k, dev), _index_arg(offsets, "offsets", dev)
+    _outside_autograd("vs_route_rows", X)
     out = _new(out, "out", X.dtype, (n * k, d), X)
     _run("vs_route_rows", dev, X.data_ptr(), n, d, code, slot_at, offsets_at, offsets.numel() - 1, k,
          out.data_ptr())
@@ -1121,6 +1138,7 @@ def vs_route_rows_backward(dXs, slot, k: int, out=None):
         raise ValueError(f"dXs must hold k = {k} rows per row")
     n = m // k
     slot_at = _slots(slot, n, k, dev)
+    _outside_autograd("vs_route_rows_backward", dXs)
     out = _new(out, "out", dXs.dtype, (n, d), dXs)
     _run("vs_route_rows_backward", dev, dXs.data_ptr(), n, d, code, slot_at, k, out.data_ptr())
     return out
@@ -1139,6 +1157,7 @@ def vs_combine_rows(Ys, slot, weights, out=None):
     if Ys.shape[0] != n * k:
         raise ValueError("Ys must hold one row per entry of weights")
     slot_at = _slots(slot, n, k, dev)
+    _outside_autograd("vs_combine_rows", Ys, weights)
     out = _new(out, "out", Ys.dtype, (n, d), Ys)
     _run("vs_combine_rows", dev, Ys.data_ptr(), n, d, code, slot_at, weights.data_ptr(), k,
          out.data_ptr())
@@ -1160,6 +1179,7 @@ def vs_combine_rows_backward(dY, Ys, slot, weights, offsets, out=None, dweights=
     if dY.shape[0] != n or tuple(Ys.shape) != (n * k, d):
         raise ValueError("dY must be n x d and Ys (n * k) x d for weights n x k")
     slot_at, offsets_at = _slots(slot, n, k, dev), _index_arg(offsets, "offsets", dev)
+    _outside_autograd("vs_combine_rows_backward", dY, Ys, weights)
     out = _new(out, "out", dY.dtype, (n * k, d), dY)
     dweights = _new(dweights, "dweights", torch.float32, (n, k), weights)
     _run("vs_combine_rows_backward", dev, dY.data_ptr(), Ys.data_ptr(), n, d, code, slot_at,
@@ -1243,6 +1263,7 @@ def vs_q4_scores(x, table, nc: int, group: int = 32, scale_dtype=None, out=None)
     if table.numel() != need:
         raise ValueError(f"table holds {table.numel()} bytes, {nc} rows of {d} take {need}")
     scale_code = _dtype(scale_dtype, "scale_dtype")
+    _outside_autograd("vs_q4_scores", x)
     out = _new(out, "out", torch.float32, (nq, nc), x)
     _run("vs_q4_scores", dev, x.data_ptr(), nq, d, code, table.data_ptr(), nc, group, scale_code,
          out.data_ptr())

@@ -1,6 +1,8 @@
 """Table operators on the GPU at the values, sizes and addresses where they could
 go wrong, against plain implementations in 64 bits (tolerances as derived in
 test_table_ops)."""
+import warnings
+
 import numpy as np
 import pytest
 
@@ -8,7 +10,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import farthest_vector_search_amd as vs  # noqa: E402
-from test_table_ops import TYPES, dev, rng, rows, unpack  # noqa: E402
+from test_table_ops import TYPES, dev, host, i32, rng, rows, unpack  # noqa: E402
 
 
 @pytest.mark.parametrize("t", TYPES)
@@ -68,3 +70,53 @@ def test_q4_scores_scale_type(t):
     assert again.data_ptr() == buf.data_ptr()
     assert torch.equal(vs.vs_q4_scores(x, again, nc, 32), want)
     assert torch.equal(vs.vs_q4_scores(x, buf, nc, 32, torch.bfloat16), want)
+
+
+def test_inputs_that_require_a_gradient_warn():
+    """Results are outside autograd: a warning says so where one is expected."""
+    n, k, G, d = 6, 2, 4, 8
+    r = rng(22)
+    X, _ = rows(r, (n, d), torch.float32)
+    T, _ = rows(r, (G, d), torch.float32)
+    Ys, _ = rows(r, (n * k, d), torch.float32)
+    w = torch.ones(n, k, device=dev())
+    ids = i32(r.integers(0, G, n * k))
+    order, offsets, slot = vs.vs_group_rows(ids, G)
+    table = vs.vs_q4_layout(*vs.vs_q4_quantize(T, 32), d, 32)
+    g = lambda a: a.clone().requires_grad_()  # noqa: E731
+    calls = [lambda q: vs.vs_row_lookup(q(T), ids), lambda q: vs.vs_route_rows(q(X), slot, offsets, k),
+             lambda q: vs.vs_combine_rows(q(Ys), slot, w), lambda q: vs.vs_combine_rows(Ys, slot, q(w)),
+             lambda q: vs.vs_q4_scores(q(X), table, G, 32)]
+    for call in calls:
+        with pytest.warns(UserWarning, match="gradient"):
+            a = call(g)
+        assert not a.requires_grad
+        with warnings.catch_warnings():
+            warnings.simplefilter("error")
+            call(lambda z: z)
+            with torch.no_grad():
+                assert torch.equal(call(g), a)
+
+
+def test_calls_inside_an_autograd_function():
+    """The way the gradient is meant to be had: quiet, and equal to the formula."""
+    class Lookup(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, T, ids):
+            order, offsets, _ = vs.vs_group_rows(ids, T.shape[0])
+            ctx.save_for_backward(ids, order, offsets)
+            return vs.vs_row_lookup(T, ids, scale=2.0)
+
+        @staticmethod
+        def backward(ctx, dY):
+            return vs.vs_row_lookup_backward(dY.contiguous(), *ctx.saved_tensors, scale=2.0), None
+    r = rng(27)
+    T = torch.from_numpy(r.integers(-3, 4, (5, 8)).astype(np.float32)).to(dev()).requires_grad_()
+    R64 = r.integers(-3, 4, (9, 8)).astype(np.float64)
+    ids = r.integers(0, 5, 9).astype(np.int32)
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        (Lookup.apply(T, i32(ids)) * torch.from_numpy(R64).float().to(dev())).sum().backward()
+    want = np.zeros((5, 8))
+    np.add.at(want, ids, 2 * R64)
+    assert np.array_equal(host(T.grad), want)
