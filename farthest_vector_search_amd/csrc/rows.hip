@@ -567,8 +567,11 @@ hipError_t launch_row_lookup_bwd(const void *dY, int64_t n, int32_t d, int dtype
         if (grad_dtype == dtype)
             return lookup_bwd<T, T, N>(dY, n, d, ids, order, offsets, G, scale, dT, (float *)ws,
                                        st, n_cu);
-        return lookup_bwd<T, float, N>(dY, n, d, ids, order, offsets, G, scale, dT, (float *)ws,
-                                       st, n_cu);
+        // N is 4 at most for fp32 rows
+        if constexpr (N <= 4)
+            return lookup_bwd<T, float, N>(dY, n, d, ids, order, offsets, G, scale, dT,
+                                           (float *)ws, st, n_cu);
+        return hipErrorInvalidValue;
     });
 }
 

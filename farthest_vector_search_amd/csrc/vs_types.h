@@ -19,8 +19,11 @@ __device__ __forceinline__ float widen(T x) { return (float)x; }
 template <typename T>
 __device__ __forceinline__ T narrow(float x) { return (T)x; }
 
+// N elements, accessed 16 bytes at a time at most: longer ones (the scales of
+// a block, a row of fp32 partial sums) claim no more alignment than that, which
+// is what callers' arrays are asked for.
 template <typename T, int N>
-struct alignas(sizeof(T) * N) Vec {
+struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Vec {
     T v[N];
 };
 
@@ -36,8 +39,6 @@ template <>
 struct RawBits<8> { typedef __attribute__((ext_vector_type(2))) uint32_t type; };
 template <>
 struct RawBits<16> { typedef __attribute__((ext_vector_type(4))) uint32_t type; };
-template <>
-struct RawBits<32> { typedef __attribute__((ext_vector_type(8))) uint32_t type; };
 
 template <typename V>
 __device__ __forceinline__ V load_once(const V *p) {

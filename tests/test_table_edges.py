@@ -10,7 +10,7 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import farthest_vector_search_amd as vs  # noqa: E402
-from test_table_ops import TYPES, dev, host, i32, rng, rows, unpack  # noqa: E402
+from test_table_ops import TYPES, dev, host, i32, pack, rng, rows, unpack  # noqa: E402
 
 
 @pytest.mark.parametrize("t", TYPES)
@@ -120,3 +120,21 @@ def test_calls_inside_an_autograd_function():
     want = np.zeros((5, 8))
     np.add.at(want, ids, 2 * R64)
     assert np.array_equal(host(T.grad), want)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_q4_scores_table_at_16_bytes(group):
+    """A table on a 16-byte boundary that is no 32-byte one."""
+    r = rng(23)
+    nc, d = 70, 300
+    c = r.integers(0, 16, (nc, d))
+    s = torch.from_numpy(2.0 ** r.integers(-2, 1, (nc, -(-d // group)))).half().to(dev())
+    x64 = r.integers(-4, 5, (2, d)).astype(np.float64)
+    x = torch.from_numpy(x64).half().to(dev())
+    need = vs.lib().vs_q4_bytes(nc, d, group)
+    buf = torch.empty(need + 64, dtype=torch.uint8, device=dev())
+    at = (16 - buf.data_ptr()) % 32
+    table = vs.vs_q4_layout(pack(c), s, d, group, out=buf[at:at + need])
+    assert table.data_ptr() % 32 == 16
+    full = (c - 8.0) * np.repeat(host(s), group, 1)[:, :d]
+    assert np.array_equal(host(vs.vs_q4_scores(x, table, nc, group)), x64 @ full.T)
