@@ -969,7 +969,15 @@ def _rows_arg(t, name, device=None, dtype=None):
         raise ValueError(f"{name} must be contiguous")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other inputs on {device}")
+    _fits_int32(t.shape[1], name)
     return code
+
+
+def _fits_int32(size, name):
+    """Columns and entries per row are 32 bits in the C interface: a larger
+    number is refused here, where ctypes would cut it off."""
+    if not -2147483648 <= size <= 2147483647:
+        raise VsError(2, name)
 
 
 _int32 = None
@@ -1104,6 +1112,7 @@ def vs_row_lookup_backward(dY, ids, order, offsets, scale: float = 1.0, grad_dty
 
 
 def _slots(slot, n, k, dev):
+    _fits_int32(k, "k")
     at = _index_arg(slot, "slot", dev)
     if slot.numel() != n * k:
         raise ValueError(f"slot holds {slot.numel()} entries, {n} rows of {k} need {n * k}")
@@ -1230,6 +1239,7 @@ def vs_q4_layout(codes, scales, d: int, group: int = 32, out=None):
         raise TypeError("scales must be float16 or bfloat16")
     _rows_arg(scales, "scales", dev)
     nc, d, group = codes.shape[0], int(d), _q4_group(group)
+    _fits_int32(d, "d")
     if codes.shape[1] != (d + 1) // 2 or tuple(scales.shape) != (nc, (d + group - 1) // group):
         raise ValueError(f"codes and scales disagree with {nc} rows of {d} in groups of {group}")
     made = torch.uint8 if scales.dtype == torch.float16 else torch.int8

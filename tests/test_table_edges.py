@@ -138,3 +138,27 @@ def test_q4_scores_table_at_16_bytes(group):
     assert table.data_ptr() % 32 == 16
     full = (c - 8.0) * np.repeat(host(s), group, 1)[:, :d]
     assert np.array_equal(host(vs.vs_q4_scores(x, table, nc, group)), x64 @ full.T)
+
+
+def test_wide_sizes_are_refused():
+    """Sizes that do not fit the C interface's 32 bits are refused, not cut off."""
+    big = 2 ** 32 + 8
+    e = lambda *s, t=torch.bfloat16: torch.empty(s, dtype=t, device=dev())  # noqa: E731
+    ids = e(0, t=torch.int32)
+    off = i32([0, 0])
+    calls = [lambda: vs.vs_row_lookup(e(1, big), ids),
+             lambda: vs.vs_route_rows(e(0, big), ids, off, 2),
+             lambda: vs.vs_route_rows(e(0, 8), ids, off, 2 ** 32 + 2),
+             lambda: vs.vs_route_rows_backward(e(0, big), ids, 2),
+             lambda: vs.vs_route_rows_backward(e(0, 8), ids, 2 ** 32 + 2),
+             lambda: vs.vs_combine_rows(e(0, big), ids, e(0, 2, t=torch.float32)),
+             lambda: vs.vs_combine_rows(e(0, 8), ids, e(0, 2 ** 32 + 2, t=torch.float32)),
+             lambda: vs.vs_combine_rows_backward(e(0, big), e(0, big), ids,
+                                                 e(0, 2, t=torch.float32), off),
+             lambda: vs.vs_q4_quantize(e(1, big)),
+             lambda: vs.vs_q4_layout(e(0, 4, t=torch.uint8), e(0, 1, t=torch.float16), big),
+             lambda: vs.vs_q4_scores(e(0, big), e(1152, t=torch.uint8), 3)]
+    for i, call in enumerate(calls):
+        with pytest.raises(vs.VsError) as err:
+            call()
+        assert err.value.status == 2, i
