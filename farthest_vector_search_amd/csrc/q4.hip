@@ -472,7 +472,7 @@ __global__ __launch_bounds__(kWideWaves * 64) void k_q4_scores_wide(
     constexpr int QT = 16 / F::pieces;     // queries per tile of columns
     constexpr int PER = kBlockCols / GROUP;  // groups per block
     __shared__ float red[kWideWaves][16][17];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const int col = lane & 15, part = lane >> 4;
     const int64_t tiles = (nq + QT - 1) / QT;
     const int piece = col / QT;
@@ -484,7 +484,7 @@ __global__ __launch_bounds__(kWideWaves * 64) void k_q4_scores_wide(
         for (int64_t rb = blockIdx.x; rb < nrb; rb += gridDim.x) {
             const int64_t q = col < QT * F::pieces ? ct * QT + col % QT : nq;
             f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-            for (int64_t cb = w; cb < ncb; cb += waves) {
+            for (int64_t cb = w; cb < ncb; cb += kWideWaves) {
                 const int64_t blk = rb * ncb + cb;
                 Block<S, PER> now;
                 now.load(table, blk, lane);
@@ -510,11 +510,11 @@ __global__ __launch_bounds__(kWideWaves * 64) void k_q4_scores_wide(
 #pragma unroll
             for (int r = 0; r < 4; ++r) red[w][col][4 * part + r] = acc[r];
             __syncthreads();
-            for (int o = threadIdx.x; o < QT * 16; o += blockDim.x) {
+            for (int o = threadIdx.x; o < QT * 16; o += kWideWaves * 64) {
                 const int r = o & 15, qq = o >> 4;
                 float sum = 0.0f;
                 for (int p = F::pieces - 1; p >= 0; --p)
-                    for (int v = 0; v < waves; ++v) sum += red[v][qq + p * QT][r];
+                    for (int v = 0; v < kWideWaves; ++v) sum += red[v][qq + p * QT][r];
                 const int64_t row = rb * kBlockRows + r, query = ct * QT + qq;
                 if (row < nc && query < nq) y[query * nc + row] = sum;
             }
@@ -569,9 +569,8 @@ hipError_t scores_group(const X *x, int64_t nq, int32_t d, const uint8_t *table,
     else {
         const dim3 grid((unsigned)(nrb < (1 << 20) ? nrb : 1 << 20),
                         (unsigned)(tiles < 64 ? tiles : 64));
-        const dim3 block(64 * (unsigned)(ncb < kWideWaves ? ncb : kWideWaves));
-        hipLaunchKernelGGL((k_q4_scores_wide<X, S, GROUP>), grid, block, 0, st, x, nq, nc, d, nrb,
-                           ncb, table, y, wide);
+        hipLaunchKernelGGL((k_q4_scores_wide<X, S, GROUP>), grid, dim3(kWideWaves * 64), 0, st, x,
+                           nq, nc, d, nrb, ncb, table, y, wide);
     }
     timing_after(st);
     return hipGetLastError();

@@ -162,3 +162,22 @@ def test_wide_sizes_are_refused():
         with pytest.raises(vs.VsError) as err:
             call()
         assert err.value.status == 2, i
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("nq,d", [(33, 768), (33, 769), (64, 700), (17, 2048), (17, 2049), (3, 4608),
+                                  (16, 4608), (3, 4609), (17, 4616), (5, 768), (11, 768), (6, 2048),
+                                  (6, 2049)])
+def test_q4_scores_where_the_form_changes(nq, d, t):
+    """Widths and query counts on both sides of each change of kernel form: the
+    last ones whose operands just fit in LDS (160 KiB), and one column more.
+    Small whole numbers, scales powers of two: exact."""
+    nc, group = 37, 64
+    r = rng(24, nq, d)
+    c = r.integers(0, 16, (nc, d))
+    s = torch.from_numpy(2.0 ** r.integers(-2, 1, (nc, -(-d // group)))).half().to(dev())
+    x64 = r.integers(-4, 5, (nq, d)).astype(np.float64)
+    x = torch.from_numpy(x64).to(t).to(dev())
+    table = vs.vs_q4_layout(pack(c), s, d, group)
+    full = (c - 8.0) * np.repeat(host(s), group, 1)[:, :d]
+    assert np.array_equal(host(vs.vs_q4_scores(x, table, nc, group)), x64 @ full.T)
