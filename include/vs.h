@@ -540,11 +540,16 @@ int vs_combine_rows_backward(const void *dY, const void *Ys, int64_t n, int32_t 
  *                of 16 rows x 128 columns, each with its scales): out is caller-owned,
  *                vs_q4_bytes(nc, d, group) bytes, 16-byte aligned.
  *   vs_q4_scores y[q][i] = x[q] . T[i], float32[nq x nc], from the laid-out
- *                table; x is nq x d of `dtype`.  Products are exact and sums
- *                fp32, a group at a time.  Queries are assumed finite, with
+ *                table; x is nq x d of `dtype`.  Products are exact (but for
+ *                bits of a VS_F32 query below 2^-133, which are dropped) and
+ *                sums fp32, a group at a time.  A group is summed as
+ *                (16 + code) x minus 24 x, so its roundings are relative to
+ *                scale (code + 40) |x|, also where the codes lie near 8 and
+ *                the score is far smaller.  Queries are assumed finite, with
  *                magnitudes below 2^115; a query that is not affects its own
- *                scores only.  Made for few queries (the table is read once
- *                for every 16; for every 5 of VS_F32).
+ *                scores only.  Made for few queries: the table is read once
+ *                for every 64 of them up to d = 768, for every 32 up to
+ *                d = 2,048 and for every 16 beyond (VS_F32: 20, 10 and 5).
  * group is 32, 64 or 128; nc in [1, 2^31-1], d in [1, 2^20], nq in [0, 2^31-1]
  * (0: no-op).  vs_q4_bytes returns 0 for invalid sizes.
  */

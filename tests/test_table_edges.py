@@ -10,7 +10,8 @@ torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 
 import farthest_vector_search_amd as vs  # noqa: E402
-from test_table_ops import TYPES, dev, host, i32, pack, rng, rows, unpack  # noqa: E402
+from test_table_ops import (TYPES, V, close, dev, host, i32, pack, rng, rows,  # noqa: E402
+                            unpack)
 
 
 @pytest.mark.parametrize("t", TYPES)
@@ -181,3 +182,70 @@ def test_q4_scores_where_the_form_changes(nq, d, t):
     table = vs.vs_q4_layout(pack(c), s, d, group)
     full = (c - 8.0) * np.repeat(host(s), group, 1)[:, :d]
     assert np.array_equal(host(vs.vs_q4_scores(x, table, nc, group)), x64 @ full.T)
+
+
+@pytest.mark.parametrize("t", TYPES)
+def test_q4_scores_codes_near_zero(t):
+    """Rows of one large value a group, nearly all other codes at 7 .. 9."""
+    r = rng(25)
+    nc, d, group, nq = 60, 512, 128, 4
+    T = torch.from_numpy((r.standard_normal((nc, d)) * 0.01).astype(np.float32))
+    T[:, ::group] = 1.0
+    T = T.to(dev())
+    codes, scales = vs.vs_q4_quantize(T, group)
+    table = vs.vs_q4_layout(codes, scales, d, group)
+    x, x64 = rows(r, (nq, d), t)
+    c = unpack(codes, d)
+    assert (np.abs(c - 8) <= 1).mean() > 0.9
+    rep = np.repeat(host(scales), group, 1)[:, :d]
+    want = x64 @ ((c - 8.0) * rep).T
+    tol = 2 * V * (2 * group + d // group + 4) * (np.abs(x64) @ ((c + 40.0) * rep).T)
+    close(vs.vs_q4_scores(x, table, nc, group), want, tol)
+
+
+@pytest.mark.parametrize("t", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("e", [-105, -112, -120, -126, -130])
+def test_q4_scores_tiny_queries(e, t):
+    """Queries about the smallest normal number.  Beside the usual bound: what an
+    f32 query loses below 2^-133, less than that per column, times |code - 8|,
+    and half the smallest subnormal, 2^-150, per fp32 operation."""
+    r = rng(28, -e)
+    nc, d, group, nq = 40, 160, 32, 3
+    c = r.integers(0, 16, (nc, d))
+    s = torch.ones(nc, 5, dtype=torch.float16, device=dev())
+    table = vs.vs_q4_layout(pack(c), s, d, group)
+    x = torch.from_numpy(r.standard_normal((nq, d)) * 2.0 ** e).to(t).to(dev())
+    x64 = host(x)
+    ops = 2 * group + d // group + 4
+    tol = 2 * V * ops * (np.abs(x64) @ (c + 40.0).T) + ops * d // group * 2.0 ** -150
+    if t == torch.float32:
+        tol = tol + 2.0 ** -133 * np.abs(c - 8.0).sum(1)
+    close(vs.vs_q4_scores(x, table, nc, group), x64 @ (c - 8.0).T, tol)
+
+
+def test_subnormal_rows_pass_unchanged():
+    """Subnormal values are moved and summed, not flushed."""
+    for t, step in ((torch.float32, 2.0 ** -149), (torch.float16, 2.0 ** -24), (torch.bfloat16, 2.0 ** -133)):
+        v = np.arange(-40, 40).reshape(2, 40) * step
+        T = torch.from_numpy(v).to(t).to(dev())
+        assert np.array_equal(host(T), v)
+        ids = i32([1, 0])
+        assert np.array_equal(host(vs.vs_row_lookup(T, ids)), v[::-1]), t
+        order, offsets, slot = vs.vs_group_rows(ids, 2)
+        assert np.array_equal(host(vs.vs_row_lookup_backward(T, ids, order, offsets)), v[::-1]), t
+        assert np.array_equal(host(vs.vs_route_rows_backward(T, slot, 1)), v[::-1]), t
+
+
+@pytest.mark.parametrize("n,G", [(131072, 2), (1 << 20, 1), (300000, 8)])
+def test_row_lookup_backward_hot_units(n, G):
+    """Units of a great many rows.  Whole numbers, partial sums below 2^24: exact."""
+    r = rng(26, n)
+    d = 64
+    ids = r.integers(0, G, n).astype(np.int32)
+    g = torch.Generator(device=dev()).manual_seed(3)
+    # whole numbers, |sum| < 2^24: exact
+    dY = torch.empty(n, d, device=dev()).random_(-4, 5, generator=g)
+    order, offsets, _ = vs.vs_group_rows(i32(ids), G)
+    got = vs.vs_row_lookup_backward(dY, i32(ids), order, offsets)
+    want = np.stack([host(dY[torch.from_numpy(ids == u).to(dev())]).sum(0) for u in range(G)])
+    assert np.array_equal(host(got), want)
