@@ -185,9 +185,15 @@ def lib() -> ctypes.CDLL:
 
 # ---------------------------------------------------------------- helpers --
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _metric(m) -> int:
@@ -956,6 +962,11 @@ def _dtype(t, name):
     return code
 
 
+# Columns and entries per row are 32 bits in the C interface: a larger number is
+# refused by the binding, where ctypes would cut it off.
+_MAX_I32 = 2147483647
+
+
 def _rows_arg(t, name, device=None, dtype=None):
     """The vs_dtype of a table operator's contiguous matrix on the call's device."""
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
@@ -969,15 +980,7 @@ def _rows_arg(t, name, device=None, dtype=None):
         raise ValueError(f"{name} must be contiguous")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other inputs on {device}")
-    _fits_int32(t.shape[1], name)
     return code
-
-
-def _fits_int32(size, name):
-    """Columns and entries per row are 32 bits in the C interface: a larger
-    number is refused here, where ctypes would cut it off."""
-    if not -2147483648 <= size <= 2147483647:
-        raise VsError(2, name)
 
 
 _int32 = None
@@ -1038,15 +1041,13 @@ def _run(name, device, *args):
         raise VsError(rc, name)
 
 
-def _outside_autograd(name, *inputs):
+def _outside_autograd(name):
     """The library's calls record nothing for autograd: say so where one is
-    given a tensor that wants its gradient."""
-    for t in inputs:
-        if t.requires_grad and _torch().is_grad_enabled():
-            warnings.warn(f"{name}: an input requires a gradient, but the result is outside "
-                          "autograd (gradients come from the *_backward calls; call this one "
-                          "under torch.no_grad() or in a torch.autograd.Function)", stacklevel=3)
-            return
+    given a tensor that requires a gradient."""
+    if _torch().is_grad_enabled():
+        warnings.warn(f"{name}: an input requires a gradient, but the result is outside "
+                      "autograd (gradients come from the *_backward calls; call this one "
+                      "under torch.no_grad() or in a torch.autograd.Function)", stacklevel=3)
 
 
 def vs_group_rows(ids, n_groups: int, order=None, offsets=None, slot=None, workspace=None,
@@ -1078,9 +1079,12 @@ def vs_row_lookup(T, ids, scale: float = 1.0, out=None):
     code = _rows_arg(T, "T")
     dev = T.device
     at = _index_arg(ids, "ids", dev)
-    _outside_autograd("vs_row_lookup", T)
+    if T.requires_grad:
+        _outside_autograd("vs_row_lookup")
     g, d = T.shape
     n = ids.numel()
+    if d > _MAX_I32:
+        raise VsError(2, "d")
     out = _new(out, "out", T.dtype, (n, d), T)
     _run("vs_row_lookup", dev, T.data_ptr(), g, d, code, at, n, float(scale), out.data_ptr())
     return out
@@ -1099,9 +1103,12 @@ def vs_row_lookup_backward(dY, ids, order, offsets, scale: float = 1.0, grad_dty
                                     _index_arg(offsets, "offsets", dev))
     n, d = dY.shape
     g = offsets.numel() - 1
+    if d > _MAX_I32:
+        raise VsError(2, "d")
     if ids.numel() != n or order.numel() < n:
         raise ValueError("ids and order must hold one entry per row of dY")
-    _outside_autograd("vs_row_lookup_backward", dY)
+    if dY.requires_grad:
+        _outside_autograd("vs_row_lookup_backward")
     grad_dtype = dY.dtype if grad_dtype is None else grad_dtype
     grad_code = _dtype(grad_dtype, "grad_dtype")
     out = _new(out, "out", grad_dtype, (max(g, 0), d), dY)
@@ -1112,7 +1119,8 @@ def vs_row_lookup_backward(dY, ids, order, offsets, scale: float = 1.0, grad_dty
 
 
 def _slots(slot, n, k, dev):
-    _fits_int32(k, "k")
+    if not -_MAX_I32 <= k <= _MAX_I32:
+        raise VsError(2, "k")
     at = _index_arg(slot, "slot", dev)
     if slot.numel() != n * k:
         raise ValueError(f"slot holds {slot.numel()} entries, {n} rows of {k} need {n * k}")
@@ -1128,8 +1136,11 @@ def vs_route_rows(X, slot, offsets, k: int, out=None):
     dev = X.device
     n, d = X.shape
     k = int(k)
+    if d > _MAX_I32:
+        raise VsError(2, "d")
     slot_at, offsets_at = _slots(slot, n, k, dev), _index_arg(offsets, "offsets", dev)
-    _outside_autograd("vs_route_rows", X)
+    if X.requires_grad:
+        _outside_autograd("vs_route_rows")
     out = _new(out, "out", X.dtype, (n * k, d), X)
     _run("vs_route_rows", dev, X.data_ptr(), n, d, code, slot_at, offsets_at, offsets.numel() - 1, k,
          out.data_ptr())
@@ -1143,11 +1154,14 @@ def vs_route_rows_backward(dXs, slot, k: int, out=None):
     dev = dXs.device
     m, d = dXs.shape
     k = int(k)
+    if d > _MAX_I32:
+        raise VsError(2, "d")
     if k < 1 or m % k:
         raise ValueError(f"dXs must hold k = {k} rows per row")
     n = m // k
     slot_at = _slots(slot, n, k, dev)
-    _outside_autograd("vs_route_rows_backward", dXs)
+    if dXs.requires_grad:
+        _outside_autograd("vs_route_rows_backward")
     out = _new(out, "out", dXs.dtype, (n, d), dXs)
     _run("vs_route_rows_backward", dev, dXs.data_ptr(), n, d, code, slot_at, k, out.data_ptr())
     return out
@@ -1163,10 +1177,13 @@ def vs_combine_rows(Ys, slot, weights, out=None):
     _rows_arg(weights, "weights", dev, torch.float32)
     n, k = weights.shape
     d = Ys.shape[1]
+    if d > _MAX_I32:
+        raise VsError(2, "d")
     if Ys.shape[0] != n * k:
         raise ValueError("Ys must hold one row per entry of weights")
     slot_at = _slots(slot, n, k, dev)
-    _outside_autograd("vs_combine_rows", Ys, weights)
+    if Ys.requires_grad or weights.requires_grad:
+        _outside_autograd("vs_combine_rows")
     out = _new(out, "out", Ys.dtype, (n, d), Ys)
     _run("vs_combine_rows", dev, Ys.data_ptr(), n, d, code, slot_at, weights.data_ptr(), k,
          out.data_ptr())
@@ -1185,10 +1202,13 @@ def vs_combine_rows_backward(dY, Ys, slot, weights, offsets, out=None, dweights=
     _rows_arg(weights, "weights", dev, torch.float32)
     n, k = weights.shape
     d = dY.shape[1]
+    if d > _MAX_I32:
+        raise VsError(2, "d")
     if dY.shape[0] != n or tuple(Ys.shape) != (n * k, d):
         raise ValueError("dY must be n x d and Ys (n * k) x d for weights n x k")
     slot_at, offsets_at = _slots(slot, n, k, dev), _index_arg(offsets, "offsets", dev)
-    _outside_autograd("vs_combine_rows_backward", dY, Ys, weights)
+    if dY.requires_grad or Ys.requires_grad or weights.requires_grad:
+        _outside_autograd("vs_combine_rows_backward")
     out = _new(out, "out", dY.dtype, (n * k, d), dY)
     dweights = _new(dweights, "dweights", torch.float32, (n, k), weights)
     _run("vs_combine_rows_backward", dev, dY.data_ptr(), Ys.data_ptr(), n, d, code, slot_at,
@@ -1215,6 +1235,8 @@ def vs_q4_quantize(T, group: int = 32, scale_dtype=None, codes=None, scales=None
     dev = T.device
     nc, d = T.shape
     group = _q4_group(group)
+    if d > _MAX_I32:
+        raise VsError(2, "d")
     scale_dtype = torch.float16 if scale_dtype is None else scale_dtype
     scale_code = _dtype(scale_dtype, "scale_dtype")
     codes = _new(codes, "codes", torch.uint8, (nc, (d + 1) // 2), T)
@@ -1239,7 +1261,8 @@ def vs_q4_layout(codes, scales, d: int, group: int = 32, out=None):
         raise TypeError("scales must be float16 or bfloat16")
     _rows_arg(scales, "scales", dev)
     nc, d, group = codes.shape[0], int(d), _q4_group(group)
-    _fits_int32(d, "d")
+    if not -_MAX_I32 <= d <= _MAX_I32:
+        raise VsError(2, "d")
     if codes.shape[1] != (d + 1) // 2 or tuple(scales.shape) != (nc, (d + group - 1) // group):
         raise ValueError(f"codes and scales disagree with {nc} rows of {d} in groups of {group}")
     made = torch.uint8 if scales.dtype == torch.float16 else torch.int8
@@ -1265,6 +1288,8 @@ def vs_q4_scores(x, table, nc: int, group: int = 32, scale_dtype=None, out=None)
         raise ValueError(f"table is on {table.device}, x on {dev}")
     nq, d = x.shape
     nc, group = int(nc), _q4_group(group)
+    if d > _MAX_I32:
+        raise VsError(2, "d")
     if scale_dtype is None:
         scale_dtype = torch.bfloat16 if bf16 else torch.float16
     elif bf16 and scale_dtype != torch.bfloat16:
@@ -1273,7 +1298,8 @@ def vs_q4_scores(x, table, nc: int, group: int = 32, scale_dtype=None, out=None)
     if table.numel() != need:
         raise ValueError(f"table holds {table.numel()} bytes, {nc} rows of {d} take {need}")
     scale_code = _dtype(scale_dtype, "scale_dtype")
-    _outside_autograd("vs_q4_scores", x)
+    if x.requires_grad:
+        _outside_autograd("vs_q4_scores")
     out = _new(out, "out", torch.float32, (nq, nc), x)
     _run("vs_q4_scores", dev, x.data_ptr(), nq, d, code, table.data_ptr(), nc, group, scale_code,
          out.data_ptr())
