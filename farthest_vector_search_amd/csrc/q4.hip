@@ -47,6 +47,8 @@ inline int64_t col_blocks(int64_t d) { return (d + kBlockCols - 1) / kBlockCols;
 // its finite range; c = rint(v / s) held in -8 .. 7, ties to even, plus 8.  No
 // code stands for a NaN, so a group that holds one gets a NaN for its scale
 // (and codes of 8): its row's scores are NaN, as the row's products are.
+// Two columns and two divisions a lane: 65,536 x 4,096 bf16 (group 128) 541 us,
+// 1.3 TB/s; it runs once per table.
 __device__ __forceinline__ float larger(float a, float b) {  // a NaN if either is one
     return a >= b || a != a ? a : b;
 }
@@ -86,7 +88,8 @@ __global__ __launch_bounds__(256) void k_q4_quantize(const T *__restrict__ table
 
 // ---- layout: plain codes and scales into blocks ------------------------------
 //
-// words: every row of codes starts on a 4-byte boundary.
+// words: every row of codes starts on a 4-byte boundary.  A word a thread:
+// 65,536 x 4,096 (group 128) 120 us, 2.3 TB/s; it runs once per table.
 
 constexpr int block_bytes(int per) { return 1024 + kBlockRows * 2 * per; }  // per: groups a block
 
@@ -268,9 +271,12 @@ __device__ __forceinline__ int frag_place(int chunk, int ct, int c) {
 // its segment with kBlocksAhead blocks in flight and no barrier.  A row block
 // cut by a segment's border is finished by the wave that began it, from the
 // parts (heads) the next waves leave in LDS, added in their order.  Bound by
-// the stream: 65,536 x 4,096 (group 128) for 16 f16 queries 32.0 us, 4.6 TB/s;
-// 262,144 x 256 (group 32) for one bf16 query 10.0 us, 3.9 TB/s, of which about
-// 4 us are the launch, the staging and the first blocks.  8 waves and twice the
+// the stream: 65,536 x 4,096 (group 128) for 16 f16 queries 33 us, 4.4 TB/s;
+// 262,144 x 256 (group 32) for one bf16 query 11.3 us (10.1 us a pass among
+// others, 3.9 TB/s), of which about 4 us are the launch, the staging and the
+// first blocks.  Tables of some thousand rows leave CUs idle, since a workgroup
+// takes whole row blocks (8,359 x 767, five f32 queries: 7.2 us).  16 f32 queries
+// fill 48 columns: 65,536 x 4,096 is read four times, 136 us.  8 waves and twice the
 // workgroups took 48 us of 33 (the queries staged twice), 3 or 4 blocks ahead
 // gained nothing.
 constexpr int kStreamWaves = 16;
@@ -459,7 +465,9 @@ __global__ __launch_bounds__(kStreamWaves * 64) void k_q4_scores_stream(
 
 // Wide queries whose operands do not fit in LDS: a workgroup per row block and
 // tile of columns, its waves taking the row block's blocks in turn and the
-// queries straight from memory.
+// queries straight from memory.  Bound by those reads, four times the codes':
+// 4,096 x 14,336 (group 128) for one bf16 query 15.3 us, 2.0 TB/s, for 16 18.2 us;
+// 28,672 x 8,192 for one 48 us, 2.5 TB/s, for 16 70 us.
 constexpr int kWideWaves = 16;
 
 template <typename X, typename S, int GROUP>
@@ -559,7 +567,9 @@ hipError_t scores_group(const X *x, int64_t nq, int32_t d, const uint8_t *table,
     const int64_t tiles = (nq + QT - 1) / QT;
     timing_before(st, "k_q4_scores");
     // the table is read once per launch row of column tiles: as many tiles as
-    // the queries need and LDS holds
+    // the queries need and LDS holds (1 / 2 / 4 tiles, us: 65,536 x 768 for 32
+    // bf16 queries 16.7 / 12.3, for 64 29 / 22 / 17; 8,192 x 512 for 48 f16
+    // queries 8.7 / 7.5 / 6.1; 65,536 x 2,048 for 32 bf16 queries 31 / 23)
     if (tiles > 2 && stream_lds(ncb, 4) <= kLds)
         launch_stream<X, S, GROUP, 4>(x, nq, d, table, nc, y, wide, st, n_cu);
     else if (tiles > 1 && stream_lds(ncb, 2) <= kLds)

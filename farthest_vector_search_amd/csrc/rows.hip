@@ -71,8 +71,12 @@ __global__ __launch_bounds__(256) void k_row_lookup(const T *__restrict__ table,
 // last if that unit starts inside the stretch.
 //
 // run is 64, and 16 for few rows, where a long unit's rows would come one
-// behind the other with the GPU idle (1,023 x 257 f16 rows into 1,000 units:
-// the first kernel 5.5 us with 16, 9.3 us with 64).
+// behind the other with the GPU idle.  Both kernels, us, 16 / 64 (even ids; in
+// brackets frequencies about 1 / rank): 1,023 x 257 f16 into 1,000 units 6.5 /
+// 6.5 (9.4 / 12.1); 2,048 x 256 f32 into 100 units 12.3 / 7.2 (10.0 / 11.8);
+// 4,096 x 768 bf16 into 64 units 13.5 / 23.8 (16.1 / 22.9); 16,384 x 256 f32
+// into 256 units 13.6 / 21.1 (15.7 / 18.4), so 16 would pay for some rows more;
+// 131,072 x 768 bf16 into 65,536 units 85 / 75 (97 / 84).
 inline int run_of(int64_t n) { return n <= 4096 ? 16 : 64; }
 constexpr int kAhead = 8;        // rows in flight per lane
 constexpr int kJoinWaves = 8;
@@ -150,10 +154,12 @@ __device__ __forceinline__ void store_row(O *__restrict__ dT, int64_t g, int32_t
 // Workgroups 0 .. piece_blocks - 1 sum the pieces of long units, the others a
 // short unit per group of lanes.  Neighbouring groups take the blocks of
 // columns of one row, so that a row is read in one go.  Bound by memory:
-// 65,536 x 256 f32 rows into 16,384 units in 15.7 us (5.3 TB/s); 131,072 x 768
-// bf16 rows into 65,536 units, a few of which hold half of them, in 73 us and
-// 10 us for the join (short random rows, 3.7 TB/s).  Several units per group
-// or several vectors per lane came out slower (101 and 87 to 90 us for 83).
+// 65,536 x 256 f32 rows into 16,384 units in 15.5 us (5.4 TB/s); 131,072 x 768
+// bf16 rows into 65,536 units, a few of which hold half of them, in 73 us (short
+// random rows, 4.1 TB/s) and 10 us for the join.  Rows of odd width in 16 bits
+// go 2 bytes a lane: 65,536 x 767 bf16 into 16,384 units 79 us, x 768 30 us.
+// Several units per group or several vectors per lane came out slower (101 and
+// 87 to 90 us for 83).
 template <typename T, typename O, int N>
 __global__ __launch_bounds__(256) void k_row_lookup_bwd(
     const T *__restrict__ dY, int64_t n, int32_t d, const int32_t *__restrict__ ids,
@@ -209,7 +215,10 @@ __global__ __launch_bounds__(256) void k_row_lookup_bwd(
 
 // A workgroup looks at kJoinWaves stretches, a wave each, for long units that
 // start there (most hold none); for each it found, its waves take the unit's
-// pieces in turn, and the waves' sums are added in their order.
+// pieces in turn, and the waves' sums are added in their order.  It takes 3.8 us
+// where it finds nothing (65,536 rows), and as long as its longest unit needs,
+// since one workgroup a block of columns adds that unit's pieces: 131,072 x 256
+// f32 rows in two units 13.6 us after 28, 1,048,576 in one 228 us after 202.
 template <typename O, int N>
 __global__ __launch_bounds__(kJoinWaves * 64) void k_row_lookup_join(
     int64_t n, int32_t d, const int32_t *__restrict__ ids, const int32_t *__restrict__ order,
@@ -286,8 +295,9 @@ __device__ __forceinline__ void zero_tail(T *__restrict__ Xs, int64_t kept, int6
 }
 
 // UV vectors of a row are loaded before they are stored k times over, past the
-// caches (65,536 x 2,048 bf16 rows of 16,384: 87 us one at a time through
-// them, 53 us four past them, 6.4 TB/s).
+// caches (65,536 x 2,048 bf16 rows of 16,384, calls back to back, so that X
+// stays in the last-level cache: 87 us one at a time through them, 53 us four
+// past them; 64 us behind other kernels, 5.2 TB/s).
 template <typename T, int N, int UV>
 __global__ __launch_bounds__(256) void k_route_rows(const T *__restrict__ X, int64_t n, int32_t d,
                                                     const int32_t *__restrict__ slot,
@@ -391,8 +401,8 @@ __global__ __launch_bounds__(256) void k_combine_rows(const T *__restrict__ Ys, 
 
 // dY is read once for its KC entries; two vectors of each are in flight and all
 // stores come behind the loads, which would else wait for them (65,536 x 2,048
-// bf16 rows four to one, past the caches: 118 us, 5.1 TB/s; one vector at a
-// time through them 139 us).
+// bf16 rows four to one, calls back to back: 118 us, one vector at a time
+// through the caches 139 us; behind other kernels 127 us, 4.8 TB/s).
 template <typename T, int N, int KC>
 __global__ __launch_bounds__(256) void k_combine_rows_bwd(
     const T *__restrict__ dY, const T *__restrict__ Ys, int64_t n, int32_t d,
@@ -470,7 +480,11 @@ hipError_t with_type(int dtype, int n, F f) {
     }
 }
 
-// f(vectors a lane takes at a time) for rows of `vecs` vectors and 64 lanes
+// f(vectors a lane takes at a time) for rows of `vecs` vectors and 64 lanes: as
+// many as the row has for it, four at most.  It matters for long rows (1 / 2 / 4
+// at a time, us: 16,384 x 4 rows of 256 vectors 64 / 58 / 52, 16,384 x 2 of 192
+// 24.3 / 24.2 / 23.6); 65,536 x 2 rows of 64 and 32,768 x 2 of 128 take 31 us
+// with any.
 template <typename F>
 hipError_t with_vectors(int vecs, F f) {
     if (vecs <= 64) return f(std::integral_constant<int, 1>());
