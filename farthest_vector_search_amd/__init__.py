@@ -5,8 +5,8 @@ kernels of ``libvs.so``, called through its C ABI (``include/vs.h``) on the
 current torch stream.  PyTorch supplies device memory and streams.  There is
 no CPU fallback: if the library is missing or no gfx950 GPU is present the
 calls raise.  Results are outside autograd: gradients come from the *_backward
-calls, and a call that has one, or the 4-bit scores, warns when gradients are
-being recorded and an input requires one.
+calls, and a call that has one, or gives 4-bit scores, 8-bit codes or 8-bit
+scores, warns when gradients are being recorded and an input requires one.
 
 Functions (same names as the C entry points):
     vs_bmu_search(Q, C, metric)                        -> (idx, score)
@@ -30,6 +30,13 @@ Functions (same names as the C entry points):
     vs_q4_quantize(T, group)                           -> (codes, scales)
     vs_q4_layout(codes, scales, d, group)              -> table (4-bit, laid out)
     vs_q4_scores(x, table, nc, group)                  -> scores
+    vs_unit_products(Xs, W, offsets)                   -> Ys (rows times their unit's matrix)
+    vs_unit_products_backward(dYs, Xs, W, offsets)     -> (dXs, dW)
+    vs_norm_rows(X, weight, eps, residual)             -> (Y, H, rstd)
+    vs_norm_rows_q8(X, weight, eps, residual)          -> (codes, scales, H)
+    vs_norm_rows_backward(dY, H, weight, rstd, dH)     -> (dX, dweight)
+    vs_q8_quantize(T)                                  -> (codes, scales)
+    vs_q8_scores(x, x_scales, table, table_scales)     -> scores
     vs_candidate_norms(C, feature_major=False)         -> norms
     vs_tile_rows(cache_bytes, d, bytes_per_value)      -> int (host only)
 Metrics: VS_L2SQ_MIN, VS_L2SQ_MAX, VS_COS_MAX, VS_COS_MIN.
@@ -67,6 +74,9 @@ EXPORTS = ["vs_bmu_search_workspace", "vs_bmu_search", "vs_bmu_search_noalloc",
            "vs_row_lookup_backward_workspace", "vs_row_lookup_backward", "vs_route_rows",
            "vs_route_rows_backward", "vs_combine_rows", "vs_combine_rows_backward",
            "vs_q4_bytes", "vs_q4_quantize", "vs_q4_layout", "vs_q4_scores",
+           "vs_unit_products", "vs_unit_products_backward", "vs_norm_rows", "vs_norm_rows_q8",
+           "vs_norm_rows_backward_workspace", "vs_norm_rows_backward", "vs_q8_quantize",
+           "vs_q8_scores",
            "vs_candidate_norms", "vs_tile_rows", "vs_timing_enable", "vs_timing_read",
            "vs_timing_kernel_name", "vs_status_str", "vs_last_hip_error", "vs_version"]
 
@@ -153,6 +163,15 @@ def lib() -> ctypes.CDLL:
     L.vs_q4_quantize.argtypes = [P, I64, I32, I32, I32, I32, P, P, P]
     L.vs_q4_layout.argtypes = [P, P, I64, I32, I32, P, P]
     L.vs_q4_scores.argtypes = [P, I64, I32, I32, P, I64, I32, I32, P, P]
+    L.vs_unit_products.argtypes = [P, I64, I32, I32, P, P, I64, I32, P, P]
+    L.vs_unit_products_backward.argtypes = [P, P, I64, I32, I32, P, P, I64, I32, P, I32, P, P]
+    L.vs_norm_rows.argtypes = [P, P, P, I64, I32, I32, F, P, P, P, P]
+    L.vs_norm_rows_q8.argtypes = [P, P, P, I64, I32, I32, F, P, P, P, P]
+    L.vs_norm_rows_backward_workspace.argtypes = [I64, I32]
+    L.vs_norm_rows_backward_workspace.restype = SZ
+    L.vs_norm_rows_backward.argtypes = [P, P, P, P, P, I64, I32, I32, P, I32, P, P, SZ, P]
+    L.vs_q8_quantize.argtypes = [P, I64, I32, I32, P, P, P]
+    L.vs_q8_scores.argtypes = [P, P, I64, I32, P, P, I64, I32, P, P]
     L.vs_candidate_norms.argtypes = [P, I64, I32, I32, P, P]
     L.vs_tile_rows.argtypes = [I64, I32, I32]
     L.vs_tile_rows.restype = I64
@@ -176,6 +195,8 @@ def lib() -> ctypes.CDLL:
                  "vs_group_rows", "vs_row_lookup", "vs_row_lookup_backward", "vs_route_rows",
                  "vs_route_rows_backward", "vs_combine_rows", "vs_combine_rows_backward",
                  "vs_q4_quantize", "vs_q4_layout", "vs_q4_scores",
+                 "vs_unit_products", "vs_unit_products_backward", "vs_norm_rows",
+                 "vs_norm_rows_q8", "vs_norm_rows_backward", "vs_q8_quantize", "vs_q8_scores",
                  "vs_candidate_norms", "vs_timing_enable", "vs_timing_read",
                  "vs_last_hip_error"):
         getattr(L, name).restype = ctypes.c_int
@@ -1303,6 +1324,232 @@ def vs_q4_scores(x, table, nc: int, group: int = 32, scale_dtype=None, out=None)
     out = _new(out, "out", torch.float32, (nq, nc), x)
     _run("vs_q4_scores", dev, x.data_ptr(), nq, d, code, table.data_ptr(), nc, group, scale_code,
          out.data_ptr())
+    return out
+
+
+def _unit_tables(W, d, dtype, dev):
+    """The units' matrices [n_groups, cols, d], checked; (n_groups, cols)."""
+    if not isinstance(W, _torch().Tensor) or not W.is_cuda:
+        raise TypeError("W must be a CUDA (HIP) torch tensor")
+    if W.dtype != dtype:
+        raise TypeError(f"W must be {dtype}, got {W.dtype}")
+    if W.dim() != 3 or W.shape[2] != d:
+        raise ValueError(f"W must be n_groups x cols x {d}")
+    if not W.is_contiguous():
+        raise ValueError("W must be contiguous")
+    if W.device != dev:
+        raise ValueError(f"W is on {W.device}, the other inputs on {dev}")
+    if W.shape[1] > _MAX_I32 or d > _MAX_I32:
+        raise VsError(2, "W")
+    return W.shape[0], W.shape[1]
+
+
+def _unit_offsets(offsets, g, dev):
+    at = _index_arg(offsets, "offsets", dev)
+    if offsets.numel() != g + 1:
+        raise ValueError(f"offsets holds {offsets.numel()} places, {g} units need {g + 1}")
+    return at
+
+
+def vs_unit_products(Xs, W, offsets, out=None):
+    """Rows in unit order times their unit's matrix: out[p] = Xs[p] @ W[g].T for
+    offsets[g] <= p < offsets[g + 1], zeros in the rows of no unit.  W is
+    n_groups x cols x d; Xs and offsets come from vs_route_rows and
+    vs_group_rows."""
+    lib()
+    code = _rows_arg(Xs, "Xs")
+    dev = Xs.device
+    m, d = Xs.shape
+    g, cols = _unit_tables(W, d, Xs.dtype, dev)
+    offsets_at = _unit_offsets(offsets, g, dev)
+    if Xs.requires_grad or W.requires_grad:
+        _outside_autograd("vs_unit_products")
+    out = _new(out, "out", Xs.dtype, (m, cols), Xs)
+    _run("vs_unit_products", dev, Xs.data_ptr(), m, d, code, W.data_ptr(), offsets_at, g, cols,
+         out.data_ptr())
+    return out
+
+
+def vs_unit_products_backward(dYs, Xs, W, offsets, grad_dtype=None, out=None, dW=None,
+                              want_dXs: bool = True, want_dW: bool = True):
+    """Gradients of vs_unit_products: (dXs, dW), dXs[p] = dYs[p] @ W[g] (zeros in
+    the rows of no unit) and dW[g] = dYs[g's rows].T @ Xs[g's rows], of
+    grad_dtype (dYs's type, the default, or torch.float32).  What is not wanted
+    is None."""
+    lib()
+    code = _rows_arg(dYs, "dYs")
+    dev = dYs.device
+    _rows_arg(Xs, "Xs", dev, dYs.dtype)
+    m, d = Xs.shape
+    g, cols = _unit_tables(W, d, dYs.dtype, dev)
+    if tuple(dYs.shape) != (m, cols):
+        raise ValueError(f"dYs must be {m} x {cols}, as Xs and W say")
+    offsets_at = _unit_offsets(offsets, g, dev)
+    if dYs.requires_grad or Xs.requires_grad or W.requires_grad:
+        _outside_autograd("vs_unit_products_backward")
+    grad_dtype = dYs.dtype if grad_dtype is None else grad_dtype
+    grad_code = _dtype(grad_dtype, "grad_dtype")
+    want_dXs, want_dW = want_dXs or out is not None, want_dW or dW is not None
+    if not (want_dXs or want_dW):
+        raise ValueError("neither dXs nor dW is wanted")
+    out = _new(out, "out", dYs.dtype, (m, d), dYs) if want_dXs else None
+    dW = _new(dW, "dW", grad_dtype, (g, cols, d), dYs) if want_dW else None
+    _run("vs_unit_products_backward", dev, dYs.data_ptr(), Xs.data_ptr(), m, d, code, W.data_ptr(),
+         offsets_at, g, cols, _ptr(out), grad_code, _ptr(dW))
+    return out, dW
+
+
+def _norm_args(X, weight, residual, name="X", rname="residual"):
+    """The type, rows and columns of a norm's input; addresses of the weight and
+    of the residual (None: none)."""
+    code = _rows_arg(X, name)
+    n, d = X.shape
+    if d > _MAX_I32:
+        raise VsError(2, "d")
+    w = r = None
+    if weight is not None:
+        _dev(weight, "weight", X.dtype, 1)
+        if weight.device != X.device:
+            raise ValueError(f"weight is on {weight.device}, {name} on {X.device}")
+        if weight.numel() != d:
+            raise ValueError(f"weight holds {weight.numel()} values, the rows {d}")
+        w = weight.data_ptr()
+    if residual is not None:
+        _rows_arg(residual, rname, X.device, X.dtype)
+        if residual.shape != X.shape:
+            raise ValueError(f"{rname} must be {n} x {d}, as {name} is")
+        r = residual.data_ptr()
+    return code, n, d, w, r
+
+
+def _norm_sum(X, H, residual):
+    """Where the sum of X and the residual goes; X itself without a residual."""
+    if residual is None:
+        if H is not None:
+            raise ValueError("H is written only with a residual")
+        return X, None
+    H = _new(H, "H", X.dtype, tuple(X.shape), X)
+    return H, H.data_ptr()
+
+
+def _grad_wanted(*tensors):
+    return any(t is not None and t.requires_grad for t in tensors)
+
+
+def vs_norm_rows(X, weight=None, eps: float = 1e-6, residual=None, out=None, H=None, rstd=None):
+    """Rows over their root mean square: (Y, H, rstd) with H = X + residual (X
+    itself without one), rstd = 1 / sqrt(mean(H^2) + eps) per row, float32, and
+    Y = H * rstd * weight (a vector; None: 1).  H may be X or residual in place.
+    With weight d^-1/2 and eps 0 the rows of Y have unit norm, as the cosine
+    metrics take them."""
+    lib()
+    code, n, d, w, r = _norm_args(X, weight, residual)
+    if _grad_wanted(X, weight, residual):
+        _outside_autograd("vs_norm_rows")
+    out = _new(out, "out", X.dtype, (n, d), X)
+    H, h = _norm_sum(X, H, residual)
+    rstd = _new(rstd, "rstd", _torch().float32, (n,), X)
+    _run("vs_norm_rows", X.device, X.data_ptr(), r, w, n, d, code, float(eps), h, out.data_ptr(),
+         rstd.data_ptr())
+    return out, H, rstd
+
+
+def vs_norm_rows_q8(X, weight=None, eps: float = 1e-6, residual=None, codes=None, scales=None,
+                    H=None):
+    """vs_norm_rows with its output in 8 bits: (codes int8 [n, d], scales float32
+    [n], H); codes * scales[:, None] stands for H * rstd * weight, the largest
+    magnitude of a row at 127."""
+    torch = _torch()
+    lib()
+    code, n, d, w, r = _norm_args(X, weight, residual)
+    if _grad_wanted(X, weight, residual):
+        _outside_autograd("vs_norm_rows_q8")
+    codes = _new(codes, "codes", torch.int8, (n, d), X)
+    scales = _new(scales, "scales", torch.float32, (n,), X)
+    H, h = _norm_sum(X, H, residual)
+    _run("vs_norm_rows_q8", X.device, X.data_ptr(), r, w, n, d, code, float(eps), h,
+         codes.data_ptr(), scales.data_ptr())
+    return codes, scales, H
+
+
+def vs_norm_rows_backward(dY, H, weight, rstd, dH=None, grad_dtype=None, out=None, dweight=None,
+                          workspace=None, want_dweight: bool = True):
+    """Gradients of vs_norm_rows: (dX, dweight).  dX is the gradient of X and of
+    the residual; H and rstd are vs_norm_rows's, dH the gradient that reaches H
+    besides (None: none).  dweight has grad_dtype (the rows' type, the default,
+    or torch.float32); None where it is not wanted or weight is None."""
+    L = lib()
+    code, n, d, w, at_dh = _norm_args(dY, weight, dH, "dY", "dH")
+    dev = dY.device
+    _rows_arg(H, "H", dev, dY.dtype)
+    if H.shape != dY.shape:
+        raise ValueError(f"H must be {n} x {d}, as dY is")
+    _dev(rstd, "rstd", _torch().float32)
+    if rstd.device != dev or rstd.numel() != n:
+        raise ValueError(f"rstd must hold {n} values on {dev}")
+    if _grad_wanted(dY, H, weight, dH):
+        _outside_autograd("vs_norm_rows_backward")
+    grad_dtype = dY.dtype if grad_dtype is None else grad_dtype
+    grad_code = _dtype(grad_dtype, "grad_dtype")
+    if weight is None and dweight is not None:
+        raise ValueError("dweight without a weight")
+    want_dweight = weight is not None and (want_dweight or dweight is not None)
+    out = _new(out, "out", dY.dtype, (n, d), dY)
+    dweight = _new(dweight, "dweight", grad_dtype, (d,), dY) if want_dweight else None
+    need = L.vs_norm_rows_backward_workspace(n, d) if want_dweight else 0
+    ws, size, _held = _scratch(need, dY, workspace)
+    _run("vs_norm_rows_backward", dev, dY.data_ptr(), H.data_ptr(), w, at_dh, rstd.data_ptr(), n, d,
+         code, out.data_ptr(), grad_code, _ptr(dweight), ws, size)
+    return out, dweight
+
+
+def vs_q8_quantize(T, codes=None, scales=None):
+    """8-bit codes and row scales of T (n x d): (codes int8 [n, d], scales float32
+    [n]); T ~ codes * scales[:, None], the largest magnitude of a row at 127."""
+    torch = _torch()
+    lib()
+    code, n, d, _, _ = _norm_args(T, None, None, "T")
+    if T.requires_grad:
+        _outside_autograd("vs_q8_quantize")
+    codes = _new(codes, "codes", torch.int8, (n, d), T)
+    scales = _new(scales, "scales", torch.float32, (n,), T)
+    _run("vs_q8_quantize", T.device, T.data_ptr(), n, d, code, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def _q8_arg(t, name, scales, dev):
+    """8-bit codes with one float32 scale per row; their addresses."""
+    torch = _torch()
+    _dev(t, name, torch.int8, 2)
+    _dev(scales, f"{name}_scales", torch.float32)
+    if t.device != dev or scales.device != dev:
+        raise ValueError(f"{name} is on {t.device} and its scales on {scales.device}, x on {dev}")
+    if scales.numel() != t.shape[0]:
+        raise ValueError(f"{name}_scales holds {scales.numel()} values for {t.shape[0]} rows")
+    return t.data_ptr(), scales.data_ptr()
+
+
+def vs_q8_scores(x, x_scales, table, table_scales, out_dtype=None, out=None):
+    """Scores [nq, nc] of queries over a table, both in 8-bit codes with a scale
+    per row (vs_q8_quantize, vs_norm_rows_q8): x_scales[q] * table_scales[i] *
+    (x[q] . table[i]), the sum exact, of out_dtype (torch.float32 by default)."""
+    torch = _torch()
+    lib()
+    dev = getattr(x, "device", None)
+    x_at, xs_at = _q8_arg(x, "x", x_scales, dev)
+    t_at, ts_at = _q8_arg(table, "table", table_scales, dev)
+    nq, d = x.shape
+    nc = table.shape[0]
+    if table.shape[1] != d:
+        raise ValueError(f"table has {table.shape[1]} columns, x {d}")
+    if d > _MAX_I32:
+        raise VsError(2, "d")
+    out_dtype = torch.float32 if out_dtype is None else out_dtype
+    out_code = _dtype(out_dtype, "out_dtype")
+    if x_scales.requires_grad or table_scales.requires_grad:
+        _outside_autograd("vs_q8_scores")
+    out = _new(out, "out", out_dtype, (nq, nc), x)
+    _run("vs_q8_scores", dev, x_at, xs_at, nq, d, t_at, ts_at, nc, out_code, out.data_ptr())
     return out
 
 

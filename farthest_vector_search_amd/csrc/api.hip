@@ -1201,6 +1201,154 @@ VS_API int vs_q4_scores(const void *x, int64_t nq, int32_t d, int32_t dtype, con
     return VS_OK;
 }
 
+// ---- products of rows in unit order with their unit's matrix ---------------------
+
+static int unit_check(int64_t m, int32_t d, int32_t dtype, int64_t n_groups, int32_t cols) {
+    if (bad_dtype(dtype)) return VS_ERR_DTYPE;
+    if (bad_group_shape(m, n_groups) || d < 1 || d > kMaxDim || cols < 1 || cols > kMaxDim)
+        return VS_ERR_SHAPE;
+    return VS_OK;
+}
+
+VS_API int vs_unit_products(const void *Xs, int64_t m, int32_t d, int32_t dtype, const void *W,
+                            const int32_t *offsets, int64_t n_groups, int32_t cols, void *Ys,
+                            void *stream) {
+    if (const int s = unit_check(m, d, dtype, n_groups, cols)) return s;
+    if (m == 0) return VS_OK;
+    if (!Xs || !W || !offsets || !Ys) return VS_ERR_NULL;
+    if (!al_type(Xs, dtype) || !al_type(W, dtype) || !al4(offsets) || !al_type(Ys, dtype))
+        return VS_ERR_ALIGN;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    VS_TRY_HIP(vs::launch_unit_rows(Xs, m, d, dtype, W, offsets, n_groups, cols, false, Ys,
+                                    reinterpret_cast<hipStream_t>(stream), n_cu));
+    return VS_OK;
+}
+
+VS_API int vs_unit_products_backward(const void *dYs, const void *Xs, int64_t m, int32_t d,
+                                     int32_t dtype, const void *W, const int32_t *offsets,
+                                     int64_t n_groups, int32_t cols, void *dXs,
+                                     int32_t grad_dtype, void *dW, void *stream) {
+    if (bad_dtype(dtype) || bad_dtype(grad_dtype) ||
+        (grad_dtype != dtype && grad_dtype != vs::kF32))
+        return VS_ERR_DTYPE;
+    if (const int s = unit_check(m, d, dtype, n_groups, cols)) return s;
+    if ((m > 0 && (!dYs || (dXs && !W) || (dW && !Xs))) || !offsets || (!dXs && !dW && m > 0))
+        return VS_ERR_NULL;
+    if (!al_type(dYs, dtype) || !al_type(Xs, dtype) || !al_type(W, dtype) || !al4(offsets) ||
+        !al_type(dXs, dtype) || !al_type(dW, grad_dtype))
+        return VS_ERR_ALIGN;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+    if (dXs && m > 0)
+        VS_TRY_HIP(vs::launch_unit_rows(dYs, m, cols, dtype, W, offsets, n_groups, d, true, dXs,
+                                        st, n_cu));
+    if (dW)  // units without rows get zeros, so also where m is 0
+        VS_TRY_HIP(vs::launch_unit_mats(dYs, Xs, m, d, dtype, offsets, n_groups, cols, grad_dtype,
+                                        dW, st, n_cu));
+    return VS_OK;
+}
+
+// ---- rows over their root mean square, and tables in 8-bit codes -----------------
+
+static int norm_check(int64_t n, int32_t d, int32_t dtype, float eps) {
+    if (bad_dtype(dtype)) return VS_ERR_DTYPE;
+    if (n < 0 || n > kMaxIndex || d < 1 || d > kMaxDim || !(eps >= 0.0f && eps <= 3.0e38f))
+        return VS_ERR_SHAPE;
+    return VS_OK;
+}
+
+VS_API int vs_norm_rows(const void *X, const void *R, const void *weight, int64_t n, int32_t d,
+                        int32_t dtype, float eps, void *H, void *Y, float *rstd, void *stream) {
+    if (const int s = norm_check(n, d, dtype, eps)) return s;
+    if (n == 0) return VS_OK;
+    if (!X || !Y || (R && !H)) return VS_ERR_NULL;
+    if (!al_type(X, dtype) || !al_type(R, dtype) || !al_type(weight, dtype) ||
+        !al_type(H, dtype) || !al_type(Y, dtype) || !al4(rstd))
+        return VS_ERR_ALIGN;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    VS_TRY_HIP(vs::launch_norm_rows(X, R, weight, n, d, dtype, eps, R ? H : nullptr, Y, rstd,
+                                    reinterpret_cast<hipStream_t>(stream), n_cu));
+    return VS_OK;
+}
+
+VS_API int vs_norm_rows_q8(const void *X, const void *R, const void *weight, int64_t n, int32_t d,
+                           int32_t dtype, float eps, void *H, int8_t *codes, float *scales,
+                           void *stream) {
+    if (const int s = norm_check(n, d, dtype, eps)) return s;
+    if (n == 0) return VS_OK;
+    if (!X || !codes || !scales || (R && !H)) return VS_ERR_NULL;
+    if (!al_type(X, dtype) || !al_type(R, dtype) || !al_type(weight, dtype) ||
+        !al_type(H, dtype) || !al4(scales))
+        return VS_ERR_ALIGN;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    VS_TRY_HIP(vs::launch_norm_rows_q8(X, R, weight, n, d, dtype, eps, R ? H : nullptr, codes,
+                                       scales, reinterpret_cast<hipStream_t>(stream), n_cu));
+    return VS_OK;
+}
+
+VS_API size_t vs_norm_rows_backward_workspace(int64_t n, int32_t d) {
+    if (n < 0 || n > kMaxIndex || d < 1 || d > kMaxDim) return 0;
+    return vs::norm_bwd_workspace(n, d);
+}
+
+VS_API int vs_norm_rows_backward(const void *dY, const void *H, const void *weight,
+                                 const void *dH, const float *rstd, int64_t n, int32_t d,
+                                 int32_t dtype, void *dX, int32_t grad_dtype, void *dweight,
+                                 void *workspace, size_t workspace_bytes, void *stream) {
+    if (bad_dtype(grad_dtype) || (grad_dtype != dtype && grad_dtype != vs::kF32))
+        return VS_ERR_DTYPE;
+    if (const int s = norm_check(n, d, dtype, 0.0f)) return s;
+    if (n == 0 && !dweight) return VS_OK;
+    const size_t need = dweight ? vs::norm_bwd_workspace(n, d) : 0;
+    if ((n > 0 && (!dY || !H || !rstd || !dX)) || (need > 0 && !workspace)) return VS_ERR_NULL;
+    if (!al_type(dY, dtype) || !al_type(H, dtype) || !al_type(weight, dtype) ||
+        !al_type(dH, dtype) || !al4(rstd) || !al_type(dX, dtype) ||
+        !al_type(dweight, grad_dtype) || (need > 0 && !al256(workspace)))
+        return VS_ERR_ALIGN;
+    if (workspace_bytes < need) return VS_ERR_WORKSPACE;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    VS_TRY_HIP(vs::launch_norm_rows_bwd(dY, H, weight, dH, rstd, n, d, dtype, dX, grad_dtype,
+                                        dweight, workspace, reinterpret_cast<hipStream_t>(stream),
+                                        n_cu));
+    return VS_OK;
+}
+
+constexpr int32_t kMaxQ8Dim = 131071;  // 128 x 128 x 131,071 < 2^31
+
+VS_API int vs_q8_quantize(const void *T, int64_t n, int32_t d, int32_t dtype, int8_t *codes,
+                          float *scales, void *stream) {
+    if (const int s = norm_check(n, d, dtype, 0.0f)) return s;
+    if (n == 0) return VS_OK;
+    if (!T || !codes || !scales) return VS_ERR_NULL;
+    if (!al_type(T, dtype) || !al4(scales)) return VS_ERR_ALIGN;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    VS_TRY_HIP(vs::launch_q8_quantize(T, n, d, dtype, codes, scales,
+                                      reinterpret_cast<hipStream_t>(stream), n_cu));
+    return VS_OK;
+}
+
+VS_API int vs_q8_scores(const int8_t *x, const float *x_scales, int64_t nq, int32_t d,
+                        const int8_t *table, const float *table_scales, int64_t nc,
+                        int32_t out_dtype, void *y, void *stream) {
+    if (bad_dtype(out_dtype)) return VS_ERR_DTYPE;
+    if (nq < 0 || nq > kMaxIndex || nc < 1 || nc > kMaxIndex || d < 1 || d > kMaxQ8Dim)
+        return VS_ERR_SHAPE;
+    if (nq == 0) return VS_OK;
+    if (!x || !x_scales || !table || !table_scales || !y) return VS_ERR_NULL;
+    if (!al4(x_scales) || !al4(table_scales) || !al_type(y, out_dtype)) return VS_ERR_ALIGN;
+    int n_cu = 0;
+    if (const int s = device_ready(&n_cu)) return s;
+    VS_TRY_HIP(vs::launch_q8_scores(x, x_scales, nq, d, table, table_scales, nc, out_dtype, y,
+                                    reinterpret_cast<hipStream_t>(stream), n_cu));
+    return VS_OK;
+}
+
 VS_API int64_t vs_tile_rows(int64_t cache_bytes, int32_t d, int32_t bytes_per_value) {
     if (cache_bytes <= 0 || d < 1 || bytes_per_value < 1) return 0;
     // floor(cache * 0.85 / (d * b)) in exact integer arithmetic: 0.85 = 17/20

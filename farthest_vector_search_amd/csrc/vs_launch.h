@@ -154,6 +154,31 @@ hipError_t launch_q4_layout(const uint8_t *codes, const void *scales, int64_t nc
 hipError_t launch_q4_scores(const void *x, int64_t nq, int32_t d, int dtype, const void *table,
                             int64_t nc, int group, int scale_dtype, float *y, hipStream_t st,
                             int n_cu);
+// Rows in unit order times their unit's matrix (units.hip): out[p][j] = sum_k
+// A[p][k] W[g][j][k], across: W[g][k][j]; and the matrices' gradient.
+hipError_t launch_unit_rows(const void *A, int64_t m, int32_t K, int dtype, const void *W,
+                            const int32_t *offsets, int64_t G, int32_t out_cols, bool across,
+                            void *out, hipStream_t st, int n_cu);
+hipError_t launch_unit_mats(const void *dY, const void *X, int64_t m, int32_t d, int dtype,
+                            const int32_t *offsets, int64_t G, int32_t cols, int grad_dtype,
+                            void *dW, hipStream_t st, int n_cu);
+// Rows over their root mean square (norm.hip); R, w, H, rstd, dH, dw may be null
+hipError_t launch_norm_rows(const void *X, const void *R, const void *w, int64_t n, int32_t d,
+                            int dtype, float eps, void *H, void *Y, float *rstd, hipStream_t st,
+                            int n_cu);
+hipError_t launch_norm_rows_q8(const void *X, const void *R, const void *w, int64_t n, int32_t d,
+                               int dtype, float eps, void *H, int8_t *codes, float *scales,
+                               hipStream_t st, int n_cu);
+size_t norm_bwd_workspace(int64_t n, int32_t d);
+hipError_t launch_norm_rows_bwd(const void *dY, const void *H, const void *w, const void *dH,
+                                const float *rstd, int64_t n, int32_t d, int dtype, void *dX,
+                                int grad_dtype, void *dw, void *ws, hipStream_t st, int n_cu);
+// Tables in 8-bit codes (norm.hip: rows to codes; q8.hip: scores)
+hipError_t launch_q8_quantize(const void *X, int64_t n, int32_t d, int dtype, int8_t *codes,
+                              float *scales, hipStream_t st, int n_cu);
+hipError_t launch_q8_scores(const int8_t *x, const float *xs, int64_t nq, int32_t d,
+                            const int8_t *table, const float *ts, int64_t nc, int out_dtype,
+                            void *y, hipStream_t st, int n_cu);
 
 // Timing hook (api.hip).
 void timing_before(hipStream_t st, const char *name);

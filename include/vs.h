@@ -562,6 +562,94 @@ int vs_q4_scores(const void *x, int64_t nq, int32_t d, int32_t dtype, const void
                  int64_t nc, int32_t group, int32_t scale_dtype, float *y, void *stream);
 
 /*
+ * Rows in unit order (as vs_route_rows makes them) times their unit's matrix,
+ * and the gradients.  W holds a matrix of `cols` rows x d for each unit.
+ *   vs_unit_products  Ys[p] = W[g] Xs[p], offsets[g] <= p < offsets[g + 1]:
+ *                     Ys[p][j] = the product of row p with row j of W[g].
+ *   vs_unit_products_backward  dXs[p] = dYs[p] W[g], and dW[g] = the sum over
+ *                     g's rows of dYs[p]^T Xs[p], of `grad_dtype` (`dtype` or
+ *                     VS_F32, else VS_ERR_DTYPE); zeros for a unit without
+ *                     rows.  dXs or dW may be NULL, then it is not computed;
+ *                     Xs may be NULL where dW is, W where dXs is.
+ * Rows of no unit (offsets[n_groups] .. m - 1) give rows of zeros, and what they
+ * hold is never used.  Xs, dXs are m x d, Ys, dYs m x cols, all of `dtype`, as
+ * is W (n_groups x cols x d).  Sums are fp32 (products of VS_F16 and VS_BF16
+ * values are exact) and rounded once.  offsets is taken as
+ * vs_group_rows makes it, int32[n_groups + 1]; a place read from it that lies
+ * outside [0, m] is held inside, and nothing outside the arrays is read.
+ * m in [0, 2^31-1] (0: only dW is written), n_groups in [1, 2^31-2], d and cols
+ * in [1, 2^20].  Addresses are aligned to their element.  Inputs and outputs
+ * must not overlap.
+ */
+int vs_unit_products(const void *Xs, int64_t m, int32_t d, int32_t dtype, const void *W,
+                     const int32_t *offsets, int64_t n_groups, int32_t cols, void *Ys,
+                     void *stream);
+int vs_unit_products_backward(const void *dYs, const void *Xs, int64_t m, int32_t d,
+                              int32_t dtype, const void *W, const int32_t *offsets,
+                              int64_t n_groups, int32_t cols, void *dXs, int32_t grad_dtype,
+                              void *dW, void *stream);
+
+/*
+ * Rows divided by their root mean square (with weight d^-1/2 and eps 0: the
+ * unit rows the cosine metrics take), after an addition, in the rows' type or
+ * in 8-bit codes; and the gradients.
+ *   h = X[i] + R[i] rounded to `dtype` (h = X[i] where R is NULL)
+ *   rstd = 1 / sqrt(mean of h^2 + eps), 0 where that is not finite (rows of
+ *   zeros with eps 0; root mean squares below about 2^-127)
+ *   vs_norm_rows      H[i] = h (only with R), Y[i] = h rstd weight (weight NULL:
+ *                     1), rstd[i] (may be NULL).  A row that holds a NaN or an
+ *                     infinity gives NaN.
+ *   vs_norm_rows_q8   the same in 8 bits: codes = the whole number nearest to
+ *                     127 v / max |v| (ties to even), v = h weight in fp32, so
+ *                     -127 .. 127, and scales[i] = max |v| rstd / 127: code
+ *                     times scale stands for h rstd weight.  Rows of zeros get
+ *                     codes and a scale of 0; rows with a v that is not finite
+ *                     codes of 0 and a scale of NaN.
+ *   vs_norm_rows_backward  dX = the gradient of X (and of R, the same): rstd
+ *                     (weight dY - x^ mean(weight dY x^)) + dH, x^ = H rstd;
+ *                     dweight (may be NULL) = the sum over the rows of dY x^, of
+ *                     `grad_dtype` (`dtype` or VS_F32, else VS_ERR_DTYPE).  H is
+ *                     X where there was no R; dH, the gradient that reaches
+ *                     h besides, may be NULL.
+ * X, R, H, Y, dY, dH, dX are n x d of `dtype`, weight float[d] of `dtype`, rstd and
+ * scales float32[n], codes int8[n x d].  Sums are fp32, results rounded once.
+ * n in [0, 2^31-1] (0: only dweight is written), d in [1, 2^20], eps >= 0 and
+ * finite, else VS_ERR_SHAPE.  H may be X or R and Y may be X where there is no R,
+ * dX may be dY, H or dH; other overlaps are not allowed.  Addresses are aligned
+ * to their element.
+ */
+int vs_norm_rows(const void *X, const void *R, const void *weight, int64_t n, int32_t d,
+                 int32_t dtype, float eps, void *H, void *Y, float *rstd, void *stream);
+int vs_norm_rows_q8(const void *X, const void *R, const void *weight, int64_t n, int32_t d,
+                    int32_t dtype, float eps, void *H, int8_t *codes, float *scales,
+                    void *stream);
+size_t vs_norm_rows_backward_workspace(int64_t n, int32_t d);
+int vs_norm_rows_backward(const void *dY, const void *H, const void *weight, const void *dH,
+                          const float *rstd, int64_t n, int32_t d, int32_t dtype, void *dX,
+                          int32_t grad_dtype, void *dweight, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * A table in 8-bit codes with one scale per row, and its scores.
+ *   vs_q8_quantize  codes int8[n x d] and scales float32[n] of the rows of T
+ *                   (n x d, `dtype`): codes as vs_norm_rows_q8 with v the row
+ *                   itself, scale = max |v| / 127.
+ *   vs_q8_scores    y[q][i] = x_scales[q] table_scales[i] (x[q] . table[i]),
+ *                   nq x nc of `out_dtype`, for codes -128 .. 127 of queries
+ *                   (nq x d) and table (nc x d).  The sum is exact; it is
+ *                   rounded to fp32, multiplied by x_scales[q] and then by
+ *                   table_scales[i], and the result rounded to out_dtype.
+ * nq and n in [0, 2^31-1] (0: no-op), nc in [1, 2^31-1], d in [1, 2^20] for the
+ * codes and in [1, 131,071] for the scores.  Codes may start at any address;
+ * rows on 16-byte boundaries are fastest.  Inputs and outputs must not overlap.
+ */
+int vs_q8_quantize(const void *T, int64_t n, int32_t d, int32_t dtype, int8_t *codes,
+                   float *scales, void *stream);
+int vs_q8_scores(const int8_t *x, const float *x_scales, int64_t nq, int32_t d,
+                 const int8_t *table, const float *table_scales, int64_t nc, int32_t out_dtype,
+                 void *y, void *stream);
+
+/*
  * Squared L2 norms of candidates, float32, fixed summation order (the same
  * values the searches use).  feature_major == 0: C is nc x d (row j);
  * otherwise C is d x nc (column j).  norms_out is float32[nc].
