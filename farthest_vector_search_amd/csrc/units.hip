@@ -12,14 +12,15 @@
 // of units alone (a unit's spare tile ends at once).  T rises, and a wave finds
 // its tile's unit by looking at 64 of them at a time.  The rows of no unit count
 // as one unit more.
+#include <type_traits>
+
+#include "tile.h"
 #include "vs_internal.h"
 #include "vs_types.h"
 
 namespace vs {
 
 namespace {
-
-constexpr int kTile = 64, kDepth = 16;
 
 __device__ __forceinline__ int64_t offset_of(const int32_t *__restrict__ offsets, int64_t g,
                                              int64_t G, int64_t m) {
@@ -56,85 +57,71 @@ __device__ __forceinline__ RowTile row_tile(const int32_t *__restrict__ offsets,
     return t;
 }
 
-// One 64 x 64 tile of C = A B^T: A(i, k), B(j, k) and the place of C by functions.
-template <typename FA, typename FB, typename FC>
-__device__ __forceinline__ void tile_product(int64_t K, FA fa, FB fb, FC fc) {
-    __shared__ float As[kDepth][kTile + 1], Bs[kDepth][kTile + 1];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int64_t k0 = 0; k0 < K; k0 += kDepth) {
-        __syncthreads();
-        for (int e = threadIdx.x; e < kTile * kDepth; e += 256) {
-            As[e % kDepth][e / kDepth] = fa(e / kDepth, k0 + e % kDepth);
-            Bs[e % kDepth][e / kDepth] = fb(e / kDepth, k0 + e % kDepth);
-        }
-        __syncthreads();
-        for (int k = 0; k < kDepth; ++k)
+// four neighbouring results of a row of `cols`, from column c
+template <typename O, typename Acc>
+__device__ __forceinline__ void store4(O *row, int64_t c, int64_t cols, const Acc &v, bool whole) {
+    if (whole && c + 4 <= cols) {
+        Vec<O, 4> o;
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+        for (int t = 0; t < 4; ++t) o.v[t] = narrow<O>(v[t]);
+        *reinterpret_cast<Vec<O, 4> *>(row + c) = o;
+    } else {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    acc[r][c] = __builtin_fmaf(As[k][ty + 16 * r], Bs[k][tx + 16 * c], acc[r][c]);
+        for (int t = 0; t < 4; ++t)
+            if (c + t < cols) row[c + t] = narrow<O>(v[t]);
     }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) fc(ty + 16 * r, tx + 16 * c, acc[r][c]);
 }
 
-// out[p][j] = sum_k A[p][k] B(g)(j, k): B = W[g][j][k], or W[g][k][j] (ACROSS)
-template <typename T, bool ACROSS>
-__global__ __launch_bounds__(256) void k_unit_rows(const T *__restrict__ A, int64_t m, int32_t K,
-                                                   const T *__restrict__ W,
-                                                   const int32_t *__restrict__ offsets, int64_t G,
-                                                   int32_t out_cols, T *__restrict__ out,
-                                                   int64_t tiles) {
-    const int64_t ctiles = (out_cols + kTile - 1) / kTile;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const RowTile rt = row_tile(offsets, G, m, kTile, tile / ctiles);
+// out[p][j] = sum_k A[p][k] B(g)(j, k): B = W[g][j][k], or W[g][k][j] (ACROSS).
+// `whole`: rows of out start where four neighbours can be stored at once.
+template <typename T, int BM, int BN, int WM, int WN, bool ACROSS, bool ALIGNED>
+__global__ __launch_bounds__(WM *WN * 64, BM * BN > 128 * 128 ? 1 : 2) void k_unit_rows(
+    const T *__restrict__ A, int64_t m, int32_t K, const T *__restrict__ W,
+    const int32_t *__restrict__ offsets, int64_t G, int32_t cols, T *__restrict__ out,
+    int64_t slots, bool whole) {
+    using C = tile::Core<T, BM, BN, WM, WN, false, ACROSS, ALIGNED>;
+    __shared__ __attribute__((aligned(1024))) char bufs[2 * C::kBytes];
+    const int64_t ctiles = (cols + BN - 1) / BN, total = slots * ctiles;
+    for (int64_t id = blockIdx.x; id < (total + 7) / 8 * 8; id += gridDim.x) {
+        const int64_t at = tile::xcd_order(id, total);
+        if (at >= total) continue;
+        const tile::Place pl = tile::place(at, slots, ctiles);
+        const RowTile rt = row_tile(offsets, G, m, BM, pl.row);
         if (rt.lo >= rt.hi) continue;
-        const int64_t j0 = tile % ctiles * kTile;
-        const T *w = W + (rt.unit < G ? rt.unit : 0) * (int64_t)K * out_cols;
-        tile_product(
-            rt.unit < G ? K : 0,
-            [&](int r, int64_t k) {
-                return rt.lo + r < rt.hi && k < K ? widen(A[(rt.lo + r) * K + k]) : 0.0f;
-            },
-            [&](int c, int64_t k) {
-                const int64_t j = j0 + c;
-                if (j >= out_cols || k >= K) return 0.0f;
-                return widen(ACROSS ? w[k * out_cols + j] : w[j * K + k]);
-            },
-            [&](int r, int c, float v) {
-                if (rt.lo + r < rt.hi && j0 + c < out_cols)
-                    out[(rt.lo + r) * out_cols + j0 + c] = narrow<T>(v);
-            });
+        const int64_t j0 = pl.col * BN;
+        const int64_t jn = cols - j0 < BN ? cols - j0 : BN;
+        const bool none = rt.unit >= G;
+        const T *w = W + (none ? 0 : rt.unit) * (int64_t)K * cols;
+        C core;
+        core.run({A + rt.lo * K, K, (int)(rt.hi - rt.lo)},
+                 {ACROSS ? w + j0 : w + j0 * K, ACROSS ? cols : K, (int)jn}, none ? 0 : K, bufs);
+        core.each([&](int i, int j, const tile::f32x4 &v) {
+            if (rt.lo + i < rt.hi) store4(out + (rt.lo + i) * cols, j0 + j, cols, v, whole);
+        });
     }
 }
 
-template <typename T, typename O>
-__global__ __launch_bounds__(256) void k_unit_mats(const T *__restrict__ dY,
-                                                   const T *__restrict__ X, int64_t m, int32_t d,
-                                                   const int32_t *__restrict__ offsets, int64_t G,
-                                                   int32_t cols, O *__restrict__ dW,
-                                                   int64_t tiles) {
-    const int64_t jt = (cols + kTile - 1) / kTile, kt = (d + kTile - 1) / kTile;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int64_t g = tile / (jt * kt);
-        const int64_t j0 = tile / kt % jt * kTile, k0 = tile % kt * kTile;
+// dW[g][j][k] = sum over g's rows p of dY[p][j] X[p][k]: both sides across
+template <typename T, typename O, int BM, int BN, int WM, int WN, bool ALIGNED>
+__global__ __launch_bounds__(WM *WN * 64, BM * BN > 128 * 128 ? 1 : 2) void k_unit_mats(
+    const T *__restrict__ dY, const T *__restrict__ X, int64_t m, int32_t d,
+    const int32_t *__restrict__ offsets, int64_t G, int32_t cols, O *__restrict__ dW, bool whole) {
+    using C = tile::Core<T, BM, BN, WM, WN, true, true, ALIGNED>;
+    __shared__ __attribute__((aligned(1024))) char bufs[2 * C::kBytes];
+    const int64_t jt = (cols + BM - 1) / BM, kt = (d + BN - 1) / BN, total = G * jt * kt;
+    for (int64_t id = blockIdx.x; id < (total + 7) / 8 * 8; id += gridDim.x) {
+        const int64_t at = tile::xcd_order(id, total);
+        if (at >= total) continue;
+        const int64_t g = at / (jt * kt);
+        const tile::Place pl = tile::place(at - g * jt * kt, jt, kt);
+        const int64_t j0 = pl.row * BM, k0 = pl.col * BN;
         const int64_t lo = offset_of(offsets, g, G, m), hi = offset_of(offsets, g + 1, G, m);
-        tile_product(
-            hi - lo,
-            [&](int r, int64_t p) {
-                return j0 + r < cols && lo + p < hi ? widen(dY[(lo + p) * cols + j0 + r]) : 0.0f;
-            },
-            [&](int c, int64_t p) {
-                return k0 + c < d && lo + p < hi ? widen(X[(lo + p) * d + k0 + c]) : 0.0f;
-            },
-            [&](int r, int c, float v) {
-                if (j0 + r < cols && k0 + c < d)
-                    dW[(g * cols + j0 + r) * d + k0 + c] = narrow<O>(v);
-            });
+        const int64_t jn = cols - j0 < BM ? cols - j0 : BM, kn = d - k0 < BN ? d - k0 : BN;
+        C core;
+        core.run({dY + lo * cols + j0, cols, (int)jn}, {X + lo * d + k0, d, (int)kn}, hi - lo, bufs);
+        core.each([&](int i, int k, const tile::f32x4 &v) {
+            if (i < jn) store4(dW + (g * cols + j0 + i) * d, k0 + k, d, v, whole);
+        });
     }
 }
 
@@ -147,31 +134,62 @@ hipError_t by_type(int dtype, F f) {
     }
 }
 
-inline unsigned grid_for(int64_t tiles) {
-    const int64_t most = 1 << 24;
-    return (unsigned)(tiles < most ? tiles : most);
+inline uintptr_t addr(const void *p) { return reinterpret_cast<uintptr_t>(p); }
+// rows of `cols` elements of a matrix at p start on multiples of `bytes`
+inline bool on(uintptr_t p, int64_t cols, int esize, uintptr_t bytes) {
+    return ((p | (uintptr_t)(cols * esize)) & (bytes - 1)) == 0;
+}
+
+template <typename T, int BM, int BN, int WM, int WN>
+hipError_t unit_rows(const void *A, int64_t m, int32_t K, const void *W, const int32_t *offsets,
+                     int64_t G, int32_t cols, bool across, void *out, hipStream_t st) {
+    const int64_t slots = m / BM + G + 1;
+    const dim3 grid(tile::grid_of(slots * ((cols + BN - 1) / BN))), block(WM * WN * 64);
+    const int es = (int)sizeof(T);
+    const bool aligned = on(addr(A), K, es, 16) && on(addr(W), across ? cols : K, es, 16);
+    const bool whole = on(addr(out), cols, es, 4 * es);
+    auto go = [&](auto ac, auto al) {
+        hipLaunchKernelGGL((k_unit_rows<T, BM, BN, WM, WN, decltype(ac)::value, decltype(al)::value>),
+                           grid, block, 0, st, (const T *)A, m, K, (const T *)W, offsets, G, cols,
+                           (T *)out, slots, whole);
+    };
+    timing_before(st, "k_unit_rows");
+    if (across && aligned) go(std::true_type(), std::true_type());
+    else if (across) go(std::true_type(), std::false_type());
+    else if (aligned) go(std::false_type(), std::true_type());
+    else go(std::false_type(), std::false_type());
+    timing_after(st);
+    return hipGetLastError();
+}
+
+template <typename T, typename O, int BM, int BN, int WM, int WN>
+hipError_t unit_mats(const void *dY, const void *X, int64_t m, int32_t d, const int32_t *offsets,
+                     int64_t G, int32_t cols, void *dW, hipStream_t st) {
+    const int64_t total = G * ((cols + BM - 1) / BM) * ((d + BN - 1) / BN);
+    const dim3 grid(tile::grid_of(total)), block(WM * WN * 64);
+    const int es = (int)sizeof(T);
+    const bool aligned = on(addr(dY), cols, es, 16) && on(addr(X), d, es, 16);
+    const bool whole = on(addr(dW), d, (int)sizeof(O), 4 * sizeof(O));
+    timing_before(st, "k_unit_mats");
+    if (aligned)
+        hipLaunchKernelGGL((k_unit_mats<T, O, BM, BN, WM, WN, true>), grid, block, 0, st,
+                           (const T *)dY, (const T *)X, m, d, offsets, G, cols, (O *)dW, whole);
+    else
+        hipLaunchKernelGGL((k_unit_mats<T, O, BM, BN, WM, WN, false>), grid, block, 0, st,
+                           (const T *)dY, (const T *)X, m, d, offsets, G, cols, (O *)dW, whole);
+    timing_after(st);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_unit_rows(const void *A, int64_t m, int32_t K, int dtype, const void *W,
-                            const int32_t *offsets, int64_t G, int32_t out_cols, bool across,
-                            void *out, hipStream_t st, int n_cu) {
+                            const int32_t *offsets, int64_t G, int32_t cols, bool across, void *out,
+                            hipStream_t st, int n_cu) {
     (void)n_cu;
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
-        const int64_t tiles = (m / kTile + G + 1) * ((out_cols + kTile - 1) / kTile);
-        timing_before(st, "k_unit_rows");
-        if (across)
-            hipLaunchKernelGGL((k_unit_rows<T, true>), dim3(grid_for(tiles)), dim3(256), 0, st,
-                               (const T *)A, m, K, (const T *)W, offsets, G, out_cols, (T *)out,
-                               tiles);
-        else
-            hipLaunchKernelGGL((k_unit_rows<T, false>), dim3(grid_for(tiles)), dim3(256), 0, st,
-                               (const T *)A, m, K, (const T *)W, offsets, G, out_cols, (T *)out,
-                               tiles);
-        timing_after(st);
-        return hipGetLastError();
+        return unit_rows<T, 128, 128, 2, 2>(A, m, K, W, offsets, G, cols, across, out, st);
     });
 }
 
@@ -181,17 +199,11 @@ hipError_t launch_unit_mats(const void *dY, const void *X, int64_t m, int32_t d,
     (void)n_cu;
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
-        return by_type(grad_dtype, [&](auto o) {
+        auto go = [&](auto o) {
             using O = decltype(o);
-            const int64_t tiles =
-                G * ((cols + kTile - 1) / kTile) * ((d + kTile - 1) / kTile);
-            timing_before(st, "k_unit_mats");
-            hipLaunchKernelGGL((k_unit_mats<T, O>), dim3(grid_for(tiles)), dim3(256), 0, st,
-                               (const T *)dY, (const T *)X, m, d, offsets, G, cols, (O *)dW,
-                               tiles);
-            timing_after(st);
-            return hipGetLastError();
-        });
+            return unit_mats<T, O, 128, 128, 2, 2>(dY, X, m, d, offsets, G, cols, dW, st);
+        };
+        return grad_dtype == dtype ? go(T()) : go(float());
     });
 }
 
