@@ -6,6 +6,7 @@
 // result rounded to the output's type.
 #include <type_traits>
 
+#include "few.h"
 #include "tile.h"
 #include "vs_internal.h"
 #include "vs_types.h"
@@ -15,68 +16,116 @@ namespace vs {
 namespace {
 
 template <typename O, int BM, int BN, int WM, int WN, bool ALIGNED>
-__global__ __launch_bounds__(WM *WN * 64, BM * BN > 128 * 128 ? 1 : 2) void k_q8_scores(
+__global__ __launch_bounds__(WM *WN * 64, 2) void k_q8_scores(
     const int8_t *__restrict__ x, const float *__restrict__ xs, int64_t nq, int32_t d,
-    const int8_t *__restrict__ t, const float *__restrict__ ts, int64_t nc, O *__restrict__ y,
-    bool whole) {
+    const int8_t *__restrict__ t, const float *__restrict__ ts, int64_t nc, O *__restrict__ y) {
     using C = tile::Core<int8_t, BM, BN, WM, WN, false, false, ALIGNED>;
     __shared__ __attribute__((aligned(1024))) char bufs[2 * C::kBytes];
-    const int64_t qt = (nq + BM - 1) / BM, it = (nc + BN - 1) / BN, total = qt * it;
-    for (int64_t id = blockIdx.x; id < (total + 7) / 8 * 8; id += gridDim.x) {
-        const int64_t at = tile::xcd_order(id, total);
-        if (at >= total) continue;
-        const tile::Place pl = tile::place(at, qt, it);
-        const int64_t q0 = pl.row * BM, i0 = pl.col * BN;
-        const int64_t qn = nq - q0 < BM ? nq - q0 : BM, in = nc - i0 < BN ? nc - i0 : BN;
-        C core;
-        core.run({x + q0 * d, d, (int)qn}, {t + i0 * d, d, (int)in}, d, bufs);
-        core.each([&](int q, int i, const tile::i32x4 &v) {
-            if (q >= qn) return;
-            const float s = xs[q0 + q];
-            O *row = y + (q0 + q) * nc + i0;
-            if (whole && i + 4 <= in) {
-                Vec<O, 4> o;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) o.v[u] = narrow<O>((float)v[u] * s * ts[i0 + i + u]);
-                *reinterpret_cast<Vec<O, 4> *>(row + i) = o;
-            } else {
+    const int64_t qt = (nq + BM - 1) / BM, it = (nc + BN - 1) / BN;
+    tile::run_tiles<C, int8_t, O>(
+        qt * it, bufs,
+        [&](int64_t at, tile::Job<int8_t, O> &j) {
+            const tile::Place pl = tile::place(at, qt, it);
+            const int64_t q0 = pl.row * BM, i0 = pl.col * BN;
+            j.depth = d;
+            j.m = {x + q0 * d, d, (int)(nq - q0 < BM ? nq - q0 : BM)};
+            j.n = {t + i0 * d, d, (int)(nc - i0 < BN ? nc - i0 : BN)};
+            j.out = y + q0 * nc + i0;
+            j.ld = nc;
+            j.mscale = xs + q0;
+            j.nscale = ts + i0;
+            return true;
+        });
+}
+
+// Few queries, 16 a turn, `groups` workgroups for each.
+template <typename O, int NB>
+__global__ __launch_bounds__(few::kWaves * 64) void k_q8_scores_few(
+    const int8_t *__restrict__ x, const float *__restrict__ xs, int64_t nq, int32_t d,
+    const int8_t *__restrict__ t, const float *__restrict__ ts, int64_t nc, O *__restrict__ y,
+    int64_t groups, int share) {
+    const int per = few::kWaves / share * NB * 16;
+    const int64_t total = (nq + 15) / 16 * groups;
+    for (int64_t id = blockIdx.x; id < total; id += gridDim.x) {
+        const int64_t q0 = id / groups * 16, i0 = id % groups * per;
+        const int qn = (int)(nq - q0 < 16 ? nq - q0 : 16);
+        __syncthreads();  // the last turn's sums have been read
+        few::products<int8_t, 1, NB>(
+            x + q0 * d, qn, t, i0, nc, d, share, [&](int q, int64_t i, const tile::i32x4 &v) {
+                const float s = xs[q0 + q];
+                tile::f32x4 f;
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                    if (i + u < in) row[i + u] = narrow<O>((float)v[u] * s * ts[i0 + i + u]);
-            }
-        });
+                    f[u] = (float)v[u] * s * ts[i + u < nc ? i + u : nc - 1];
+                few::store4(y + (q0 + q) * nc, i, nc, f);
+            });
     }
+}
+
+inline int64_t tiles_of(int64_t n, int tile) { return (n + tile - 1) / tile; }
+
+template <typename O>
+hipError_t q8_scores_few(const int8_t *x, const float *xs, int64_t nq, int32_t d, const int8_t *t,
+                         const float *ts, int64_t nc, O *y, hipStream_t st, int n_cu) {
+    const few::Deal e = few::deal(tiles_of(nc, 16), tiles_of(nq, 16), d, n_cu);
+    const int64_t total = tiles_of(nq, 16) * e.groups, most = 1 << 24;
+    const dim3 grid((unsigned)(total < most ? total : most)), block(few::kWaves * 64);
+    timing_before(st, "k_q8_scores_few");
+    if (e.nb == 2)
+        hipLaunchKernelGGL((k_q8_scores_few<O, 2>), grid, block, 0, st, x, xs, nq, d, t, ts, nc, y,
+                           e.groups, e.share);
+    else
+        hipLaunchKernelGGL((k_q8_scores_few<O, 1>), grid, block, 0, st, x, xs, nq, d, t, ts, nc, y,
+                           e.groups, e.share);
+    timing_after(st);
+    return hipGetLastError();
 }
 
 template <typename O, int BM, int BN, int WM, int WN>
 hipError_t q8_scores(const int8_t *x, const float *xs, int64_t nq, int32_t d, const int8_t *t,
-                     const float *ts, int64_t nc, O *y, hipStream_t st) {
-    const dim3 grid(tile::grid_of(((nq + BM - 1) / BM) * ((nc + BN - 1) / BN)));
-    const dim3 block(WM * WN * 64);
-    const bool aligned =
-        ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(t) | (uintptr_t)d) & 15) == 0;
-    const bool whole =
-        ((reinterpret_cast<uintptr_t>(y) | (uintptr_t)(nc * sizeof(O))) & (4 * sizeof(O) - 1)) == 0;
+                     const float *ts, int64_t nc, bool aligned, O *y, hipStream_t st) {
+    const dim3 grid(tile::grid_of(tiles_of(nq, BM) * tiles_of(nc, BN))), block(WM * WN * 64);
+    auto go = [&](auto al) {
+        hipLaunchKernelGGL((k_q8_scores<O, BM, BN, WM, WN, decltype(al)::value>), grid, block, 0, st,
+                           x, xs, nq, d, t, ts, nc, y);
+    };
     timing_before(st, "k_q8_scores");
-    if (aligned)
-        hipLaunchKernelGGL((k_q8_scores<O, BM, BN, WM, WN, true>), grid, block, 0, st, x, xs, nq, d,
-                           t, ts, nc, y, whole);
-    else
-        hipLaunchKernelGGL((k_q8_scores<O, BM, BN, WM, WN, false>), grid, block, 0, st, x, xs, nq,
-                           d, t, ts, nc, y, whole);
+    if constexpr (BM < 256) {  // the largest tile is for aligned rows only
+        if (!aligned) go(std::false_type());
+    }
+    if (aligned) go(std::true_type());
     timing_after(st);
     return hipGetLastError();
 }
 
 }  // namespace
 
+// Which kernel, in brackets us of it and of its neighbour:
+//   few.h      up to 4 queries (1 over 262,144 x 256: 15, 64 x 64 17), up to 16 where
+//              rows are long (16 over 65,536 x 4,096: 59 and 67; 16 over 8,359 x 767:
+//              14 and 10), and more where tiles of 64 x 64 leave half the CUs idle (64
+//              over 4,096 x 4,096: 17.5 with tiles)
+//   64 x 64    up to 64 queries (37 over 8,359 x 767: 10, 128 x 128 13), or too few
+//              tiles of 128 x 128 for the GPU
+//   128 x 128  96 over 65,536 x 4,096: 74, 64 x 64 85; 1,000 over 20,000 x 1,000: 53,
+//              256 x 256 57
+//   256 x 256  two tiles for every CU, rows on 16-byte boundaries (8,192 over 16,384 x
+//              4,096: 500, 128 x 128 604)
 hipError_t launch_q8_scores(const int8_t *x, const float *xs, int64_t nq, int32_t d,
                             const int8_t *table, const float *ts, int64_t nc, int out_dtype,
                             void *y, hipStream_t st, int n_cu) {
-    (void)n_cu;
+    const bool aligned = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(table) |
+                           (uintptr_t)d) & 15) == 0;
+    auto tiles = [&](int b) { return tiles_of(nq, b) * tiles_of(nc, b); };
     auto go = [&](auto o) {
         using O = decltype(o);
-        return q8_scores<O, 128, 128, 2, 2>(x, xs, nq, d, table, ts, nc, (O *)y, st);
+        if (nq <= 4 || (d >= 1024 && (nq <= 16 || tiles(64) * 2 < n_cu)))
+            return q8_scores_few<O>(x, xs, nq, d, table, ts, nc, (O *)y, st, n_cu);
+        if (aligned && nq >= 192 && tiles(256) >= 2 * (int64_t)n_cu)
+            return q8_scores<O, 256, 256, 2, 4>(x, xs, nq, d, table, ts, nc, aligned, (O *)y, st);
+        if (nq > 64 && tiles(128) >= n_cu)
+            return q8_scores<O, 128, 128, 2, 2>(x, xs, nq, d, table, ts, nc, aligned, (O *)y, st);
+        return q8_scores<O, 64, 64, 2, 2>(x, xs, nq, d, table, ts, nc, aligned, (O *)y, st);
     };
     switch (out_dtype) {
     case kF32: return go(float());

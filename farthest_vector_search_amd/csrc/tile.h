@@ -125,14 +125,15 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
     return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
                      (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
 }
-__device__ __forceinline__ const char *uniform(const char *p) {
-    return reinterpret_cast<const char *>(uniform((int64_t)(uintptr_t)p));
+template <typename P>
+__device__ __forceinline__ P *uniform(P *p) {
+    return reinterpret_cast<P *>(uniform((int64_t)(uintptr_t)p));
 }
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // R rows of a side, moved by W waves.  ALIGNED: 16-byte loads straight into LDS; all
 // addresses, ld and (along) the number of k's are multiples of 16 bytes.  Else
-// through registers, 16 bytes a load at any address, and by elements where 16 bytes
-// would leave a row.
+// through registers, 16 bytes a load at any address.
 template <typename T, int R, int W, bool ACROSS, bool ALIGNED>
 struct Mover {
     static constexpr int ES = (int)sizeof(T);
@@ -141,12 +142,17 @@ struct Mover {
     static constexpr int kChunks = R * ES / 16;     // chunks of a k's row (across)
     static constexpr int kLoads = R / 8 / W;        // loads a wave
     static_assert(R % (8 * W) == 0, "every wave moves the same number of pieces");
+    typedef unsigned __int128 Bits;
+    typedef typename std::conditional<
+        ES == 1, uint8_t, typename std::conditional<ES == 2, uint16_t, uint32_t>::type>::type Whole;
     const T *base;
     int64_t ld;
     uint32_t off[kLoads];  // bytes from a step's first k to the lane's chunk
     int part[kLoads];      // the chunk's first k inside the step (along), its k (across)
     int left[kLoads];      // across, unaligned: elements from the chunk's first to the row's end
     u32x4 held[ALIGNED ? 1 : kLoads];
+    int held_have;  // k's of the step in `held`
+    bool tiny;
 
     __device__ __forceinline__ void set(const Side<T> &s, int wave, int lane) {
         base = s.base;
@@ -156,7 +162,7 @@ struct Mover {
             const int piece = wave * kLoads + i;  // 64 chunks, 1 KiB of LDS
             if constexpr (!ACROSS) {
                 const int r = piece * 8 + lane / 8;
-                const int c = (lane & 7) ^ (lane / 8);
+                const int c = (lane & 7) ^ (r >> 1 & 7);
                 const int row = r < s.rows ? r : s.rows - 1;
                 off[i] = (uint32_t)row * (uint32_t)(s.ld * ES) + c * 16;
                 part[i] = c * N;
@@ -189,32 +195,51 @@ struct Mover {
     }
 
     // Not ALIGNED: the step at k0, of which `have` k's are there, into registers ...
-    __device__ __forceinline__ void read(int64_t k0, int64_t have) {
+    // Of a chunk that ends behind its row, the row's last 16 bytes are loaded, and
+    // shifted into place when they are written, so that all loads are whole and none
+    // waits for another.  Rows of fewer than 16 bytes go by elements.
+    __device__ __forceinline__ int there(int i) const {  // of a chunk's elements
+        if constexpr (!ACROSS) return held_have - part[i];
+        return part[i] < held_have ? left[i] : 0;
+    }
+    __device__ __forceinline__ void read(int64_t k0, int64_t have, int64_t row) {
+        held_have = have < K ? (int)have : K;
+        tiny = row < N;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const T *p = reinterpret_cast<const T *>(from(k0) + off[i]);
-            int n = N;  // elements that may be read
+            const int n = there(i);
+            if (tiny) {
+                Bits bits = 0;
+#pragma unroll 1
+                for (int t = 0; t < n && t < N; ++t)
+                    bits |= (Bits)reinterpret_cast<const Whole *>(p)[t] << (t * ES * 8);
+                held[i] = __builtin_bit_cast(u32x4, bits);
+                continue;
+            }
             if constexpr (!ACROSS) {
-                if (have - part[i] < N) n = (int)(have - part[i]);
+                if (n <= 0) p = base;
+                else if (n < N) p -= N - n;
             } else {
-                if (left[i] < N) n = left[i];
-                if (part[i] >= have) n = 0;
+                if (n <= 0) p -= (int64_t)part[i] * ld;  // the same chunk of k0, which is there
+                if (left[i] < N) p -= N - left[i];
             }
-            if (n >= N) {
-                __builtin_memcpy(&held[i], p, 16);
-            } else {
-                T e[N];
-#pragma unroll
-                for (int t = 0; t < N; ++t) e[t] = t < n ? p[t] : T(0);
-                __builtin_memcpy(&held[i], e, 16);
-            }
+            __builtin_memcpy(&held[i], p, 16);
         }
     }
     // ... and from there into LDS.
     __device__ __forceinline__ void write(char *lds, int wave, int lane) const {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            *reinterpret_cast<u32x4 *>(lds + (wave * kLoads + i) * 1024 + lane * 16) = held[i];
+        for (int i = 0; i < kLoads; ++i) {
+            u32x4 v = held[i];
+            const int n = there(i);
+            if (!tiny && n < N) {
+                Bits bits = __builtin_bit_cast(Bits, v);
+                bits = n <= 0 ? 0 : bits >> ((N - n) * ES * 8);
+                v = __builtin_bit_cast(u32x4, bits);
+            }
+            *reinterpret_cast<u32x4 *>(lds + (wave * kLoads + i) * 1024 + lane * 16) = v;
+        }
     }
 };
 
@@ -225,7 +250,7 @@ __device__ __forceinline__ u32x4 fragment(const char *lds, int b, int h, int lan
     const int i = lane & 15, j = lane >> 4;
     if constexpr (!ACROSS) {
         return *reinterpret_cast<const u32x4 *>(lds + (b * 16 + i) * kStep +
-                                                (((h * 4 + j) ^ (lane & 7)) << 4));
+                                                (((h * 4 + j) ^ (i >> 1)) << 4));
     } else if constexpr (sizeof(T) == 2) {
         typedef __attribute__((address_space(3))) s16x4 *P;
         const char *p = lds + (h * 32 + 8 * j + i / 4) * (R * 2) +
@@ -281,8 +306,7 @@ struct Core {
     // (or two have it), and what it waits for has to be asked for in time.
     template <bool READ, bool LOAD>
     __device__ __forceinline__ void half(const Frags &f, Frags &g, const char *next, int h,
-                                         const MMover &mm, const NMover &nm, const char *mstep,
-                                         const char *nstep, uint32_t to) {
+                                         const char *mstep, const char *nstep, uint32_t to) {
         constexpr int kAll = MB * NB, kFrags = MB + NB;
         constexpr int kLoads = MMover::kLoads + NMover::kLoads;
         count_to<kAll>([&](auto qc) {
@@ -307,33 +331,59 @@ struct Core {
     }
     static constexpr int least(int a, int b) { return a < b ? a : b; }
 
-    // The sums over k = 0 .. depth - 1; all threads of the workgroup take part.
-    // bufs: two buffers of kBytes.  A caller that writes into them, or calls again,
-    // has a barrier in between (run begins with one).
-    __device__ __forceinline__ void run(const Side<T> &ms, const Side<T> &ns, int64_t depth,
-                                        char *bufs) {
+    MMover mm;
+    NMover nm;
+    int64_t depth;
+
+    __device__ __forceinline__ Core() {
         lane = threadIdx.x & 63;
         wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
         wm = wave / WN;
         wn = wave % WN;
+    }
+
+    // Begins a product over k = 0 .. k_count - 1: its first step is on its way into the
+    // first of the two buffers at `bufs`, whose earlier contents no wave needs any
+    // more.  The first step is the one that may be short, so that all others are whole.
+    __device__ __forceinline__ void begin(const Side<T> &ms, const Side<T> &ns, int64_t k_count,
+                                          char *bufs) {
+        depth = uniform(k_count);
+        if (depth <= 0) return;
+        const int l = fresh(lane);
+        mm.set(ms, wave, l);
+        nm.set(ns, wave, l);
+        if constexpr (ALIGNED) {
+            const int first = (int)((depth - 1) % K) + 1;
+            count_to<MMover::kLoads>(
+                [&](auto i) { mm.load_part(i, mm.from(0), lds_at(bufs), wave, first); });
+            count_to<NMover::kLoads>(
+                [&](auto i) { nm.load_part(i, nm.from(0), lds_at(bufs) + kSide, wave, first); });
+        } else {
+            read(0);
+        }
+    }
+    __device__ __forceinline__ void read(int64_t k0) {
+        mm.read(k0, depth - k0, M_ACROSS ? mm.ld : depth);
+        nm.read(k0, depth - k0, N_ACROSS ? nm.ld : depth);
+    }
+    // the lane as a value of its own: what follows from it is computed again for every
+    // tile instead of being held in registers that the sums need
+    static __device__ __forceinline__ int fresh(int l) {
+        asm volatile("" : "+v"(l));
+        return l;
+    }
+    static __device__ __forceinline__ uint32_t lds_at(char *p) {
+        return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)p;
+    }
+
+    // The sums, in acc.  All waves are through with both buffers behind a barrier.
+    __device__ __forceinline__ void sum(char *bufs) {
         count_to<MB * NB>([&](auto q) { acc[q / NB][q % NB] = Acc{0, 0, 0, 0}; });
         if (depth <= 0) return;
-        MMover mm;
-        NMover nm;
-        mm.set(ms, wave, lane);
-        nm.set(ns, wave, lane);
-        depth = uniform(depth);
         const int64_t steps = (depth + K - 1) / K;
         if constexpr (ALIGNED) {
-            // The first step is the one that may be short, so that all others are whole.
-            const int first = (int)(depth - (steps - 1) * K);
-            const uint32_t lds = (uint32_t)(uintptr_t)(
-                __attribute__((address_space(3))) char *)bufs;
-            lds_barrier();
-            count_to<MMover::kLoads>(
-                [&](auto i) { mm.load_part(i, mm.from(0), lds, wave, first); });
-            count_to<NMover::kLoads>(
-                [&](auto i) { nm.load_part(i, nm.from(0), lds + kSide, wave, first); });
+            const int first = (int)((depth - 1) % K) + 1;
+            const uint32_t lds = lds_at(bufs);
             const char *mstep = uniform(mm.from(first)), *nstep = uniform(nm.from(first));  // step 1's
             const int64_t madd = uniform(mm.from(K) - mm.from(0));
             const int64_t nadd = uniform(nm.from(K) - nm.from(0));
@@ -355,10 +405,10 @@ struct Core {
             int64_t t = 0;
             auto turn = [&](auto load) {
                 const char *cur = bufs + now, *nxt = bufs + (kBytes - now);
-                half<true, false>(f, g, cur, 1, mm, nm, mstep, nstep, 0);
+                half<true, false>(f, g, cur, 1, mstep, nstep, 0);
                 asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
                 lds_barrier();
-                half<true, decltype(load)::value>(g, f, nxt, 0, mm, nm, mstep, nstep, lds + now);
+                half<true, decltype(load)::value>(g, f, nxt, 0, mstep, nstep, lds + now);
                 mstep += madd;
                 nstep += nadd;
                 now = kBytes - now;
@@ -366,19 +416,13 @@ struct Core {
             for (; t < steps - 2; ++t) turn(std::true_type());
             for (; t < steps; ++t) turn(std::false_type());
         } else {
-            __syncthreads();
-            mm.read(0, depth);
-            nm.read(0, depth);
             for (int64_t t = 0; t < steps; ++t) {
                 char *buf = bufs + (t & 1) * kBytes;
                 // step t - 2's reads of this buffer ended before the last barrier
                 mm.write(buf, wave, lane);
                 nm.write(buf + kSide, wave, lane);
                 __syncthreads();
-                if (t + 1 < steps) {
-                    mm.read((t + 1) * K, depth - (t + 1) * K);
-                    nm.read((t + 1) * K, depth - (t + 1) * K);
-                }
+                if (t + 1 < steps) read((t + 1) * K);
                 count_to<2>([&](auto h) {
                     Frags f;
                     count_to<MB + NB>([&](auto r) { take(f, r, buf, h); });
@@ -390,14 +434,81 @@ struct Core {
         }
     }
 
-    // f(m, n, four neighbours along n) for every block of the wave
-    template <typename F>
-    __device__ __forceinline__ void each(F f) const {
-        count_to<MB * NB>([&](auto q) {
-            f((wm * MB + q / NB) * 16 + (lane & 15), (wn * NB + q % NB) * 16 + (lane >> 4) * 4,
-              acc[q / NB][q % NB]);
+    // Results into rows of `out` (`ld` elements apart), rows 0 .. rows - 1 and
+    // columns 0 .. cols - 1 of the tile.  convert(a, b, sums of block row a and block
+    // column b) gives their floats.  A wave's blocks go through its part of the buffers, which no wave
+    // reads any more: stored from the matrix instruction's layout, 32 bytes
+    // of a row at a time, 8,192 x 8,192 bf16 results of 128 products each took 71 us,
+    // whole lines at a time OUT_TIME.
+    template <typename O, typename F>
+    __device__ __forceinline__ void put(char *bufs, O *out, int64_t ld, int rows, int cols,
+                                        F convert) const {
+        constexpr int kRow = NB * 16 * (int)sizeof(O);  // bytes of a row of the wave's part
+        constexpr int kChunks = kRow / 16;
+        constexpr int kPer = 16 / (int)sizeof(O);       // elements a chunk
+        constexpr int kTurns = (BM * BN * (int)sizeof(O) + 2 * kBytes - 1) / (2 * kBytes);
+        constexpr int kBlocks = MB / kTurns;            // blocks of rows a turn
+        static_assert(MB % kTurns == 0 && (kChunks & (kChunks - 1)) == 0, "whole turns");
+        char *mine = bufs + wave * (kBlocks * 16 * kRow);
+        const int l = fresh(lane), i = l & 15, j = l >> 4;
+        count_to<kTurns>([&](auto turn) {
+            count_to<kBlocks * NB>([&](auto q) {
+                constexpr int a = turn * kBlocks + q / NB, b = q % NB;
+                Vec<O, 4> v;
+                const f32x4 f = convert(a, b, acc[a][b]);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) v.v[t] = narrow<O>(f[t]);
+                const int byte = (b * 16 + j * 4) * (int)sizeof(O);
+                const int chunk = (byte >> 4) ^ (i & (kChunks - 1));
+                *reinterpret_cast<Vec<O, 4> *>(mine + (q / NB * 16 + i) * kRow + chunk * 16 +
+                                               (byte & 15)) = v;
+            });
+#pragma unroll 4
+            for (int e = l; e < kBlocks * 16 * kChunks; e += 64) {
+                const int r = e / kChunks, c = e % kChunks;
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(
+                    mine + r * kRow + ((c ^ (r & 15 & (kChunks - 1))) << 4));
+                const int m = (wm * MB + turn * kBlocks) * 16 + r;
+                const int n = wn * NB * 16 + c * kPer;
+                if (m >= rows || n >= cols) continue;
+                O *to = out + m * ld + n;
+                if (n + kPer <= cols) {
+                    __builtin_memcpy(to, &v, 16);
+                } else {
+                    O o[kPer];
+                    __builtin_memcpy(o, &v, 16);
+#pragma unroll
+                    for (int t = 0; t < kPer; ++t)
+                        if (n + t < cols) to[t] = o[t];
+                }
+            }
         });
     }
+
+    // int8: sums times their row's and their column's scale.  What a lane needs of the
+    // scales is loaded at once, from rows that are there.
+    template <typename O>
+    __device__ __forceinline__ void put_scaled(char *bufs, O *out, int64_t ld, int rows, int cols,
+                                               const float *mscale, const float *nscale) const {
+        const int l = fresh(lane);
+        float ms[MB];
+        f32x4 ns[NB];
+        count_to<MB>([&](auto a) {
+            ms[a] = mscale[least_of((wm * MB + a) * 16 + (l & 15), rows - 1)];
+        });
+        count_to<NB>([&](auto b) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                ns[b][t] = nscale[least_of((wn * NB + b) * 16 + (l >> 4) * 4 + t, cols - 1)];
+        });
+        put(bufs, out, ld, rows, cols, [&](int a, int b, const Acc &v) {
+            f32x4 f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) f[t] = (float)v[t] * ms[a] * ns[b][t];
+            return f;
+        });
+    }
+    static __device__ __forceinline__ int least_of(int a, int b) { return a < b ? a : b; }
 };
 
 // Tiles are numbered so that those of one XCD (workgroups are dealt out to the 8 in
@@ -414,6 +525,42 @@ __device__ __forceinline__ Place place(int64_t tile, int64_t rows, int64_t cols)
     const int64_t left = cols - group * 8, width = left < 8 ? left : 8;
     return Place{in / width, group * 8 + in % width};
 }
+// One tile's work: out[m][n] of its sides' rows.
+template <typename T, typename O>
+struct Job {
+    Side<T> m, n;
+    int64_t depth;
+    O *out;
+    int64_t ld;
+    const float *mscale, *nscale;  // int8: the rows' scales of either side
+};
+
+// A workgroup's tiles.  job(at, j) says what tile `at` of `total` is, or that there is
+// nothing to do.  As a rule a workgroup
+// has one tile: workgroups that stayed, took the next tile's first loads up before
+// they stored this one's results, and so saved its start, were no faster (65,536 x
+// 2,048 rows into 128 units of 2,048 columns, bf16, 557 us so, 589 us then), since
+// all of them store at the same time and the loads behind wait for the stores.
+template <typename C, typename T, typename O, typename FJ>
+__device__ __forceinline__ void run_tiles(int64_t total, char *bufs, FJ job) {
+    for (int64_t id = blockIdx.x; id < (total + 7) / 8 * 8; id += gridDim.x) {
+        const int64_t at = xcd_order(id, total);
+        Job<T, O> j;
+        if (at >= total || !job(at, j)) continue;
+        C core;
+        lds_barrier();  // the last tile's results have left the buffers
+        core.begin(j.m, j.n, j.depth, bufs);
+        core.sum(bufs);
+        lds_barrier();  // no wave reads the buffers any more
+        if constexpr (std::is_same<T, int8_t>::value) {
+            core.put_scaled(bufs, j.out, j.ld, j.m.rows, j.n.rows, j.mscale, j.nscale);
+        } else {
+            core.put(bufs, j.out, j.ld, j.m.rows, j.n.rows,
+                     [](int, int, const f32x4 &v) { return v; });
+        }
+    }
+}
+
 inline unsigned grid_of(int64_t total) {
     const int64_t want = (total + 7) / 8 * 8, most = 1 << 24;
     return (unsigned)(want < most ? want : most);

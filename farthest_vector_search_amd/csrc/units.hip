@@ -14,6 +14,7 @@
 // as one unit more.
 #include <type_traits>
 
+#include "few.h"
 #include "tile.h"
 #include "vs_internal.h"
 #include "vs_types.h"
@@ -57,72 +58,77 @@ __device__ __forceinline__ RowTile row_tile(const int32_t *__restrict__ offsets,
     return t;
 }
 
-// four neighbouring results of a row of `cols`, from column c
-template <typename O, typename Acc>
-__device__ __forceinline__ void store4(O *row, int64_t c, int64_t cols, const Acc &v, bool whole) {
-    if (whole && c + 4 <= cols) {
-        Vec<O, 4> o;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) o.v[t] = narrow<O>(v[t]);
-        *reinterpret_cast<Vec<O, 4> *>(row + c) = o;
-    } else {
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-            if (c + t < cols) row[c + t] = narrow<O>(v[t]);
-    }
-}
-
 // out[p][j] = sum_k A[p][k] B(g)(j, k): B = W[g][j][k], or W[g][k][j] (ACROSS).
-// `whole`: rows of out start where four neighbours can be stored at once.
 template <typename T, int BM, int BN, int WM, int WN, bool ACROSS, bool ALIGNED>
-__global__ __launch_bounds__(WM *WN * 64, BM * BN > 128 * 128 ? 1 : 2) void k_unit_rows(
+__global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_rows(
     const T *__restrict__ A, int64_t m, int32_t K, const T *__restrict__ W,
     const int32_t *__restrict__ offsets, int64_t G, int32_t cols, T *__restrict__ out,
-    int64_t slots, bool whole) {
+    int64_t slots) {
     using C = tile::Core<T, BM, BN, WM, WN, false, ACROSS, ALIGNED>;
     __shared__ __attribute__((aligned(1024))) char bufs[2 * C::kBytes];
-    const int64_t ctiles = (cols + BN - 1) / BN, total = slots * ctiles;
-    for (int64_t id = blockIdx.x; id < (total + 7) / 8 * 8; id += gridDim.x) {
-        const int64_t at = tile::xcd_order(id, total);
-        if (at >= total) continue;
-        const tile::Place pl = tile::place(at, slots, ctiles);
-        const RowTile rt = row_tile(offsets, G, m, BM, pl.row);
+    const int64_t ctiles = (cols + BN - 1) / BN;
+    tile::run_tiles<C, T, T>(
+        slots * ctiles, bufs,
+        [&](int64_t at, tile::Job<T, T> &j) {
+            const tile::Place pl = tile::place(at, slots, ctiles);
+            const RowTile rt = row_tile(offsets, G, m, BM, pl.row);
+            if (rt.lo >= rt.hi) return false;
+            const int64_t j0 = pl.col * BN;
+            const bool none = rt.unit >= G;
+            const T *w = W + (none ? 0 : rt.unit) * (int64_t)K * cols;
+            const int jn = (int)(cols - j0 < BN ? cols - j0 : BN);
+            j.depth = none ? 0 : K;
+            j.m = {A + rt.lo * K, K, (int)(rt.hi - rt.lo)};
+            j.n = {ACROSS ? w + j0 : w + j0 * K, ACROSS ? cols : K, jn};
+            j.out = out + rt.lo * cols + j0;
+            j.ld = cols;
+            return true;
+        });
+}
+
+// The same along k for units of few rows: 16 rows a tile, `groups` workgroups for each.
+template <typename T, int NB>
+__global__ __launch_bounds__(few::kWaves * 64) void k_unit_rows_few(
+    const T *__restrict__ A, int64_t m, int32_t K, const T *__restrict__ W,
+    const int32_t *__restrict__ offsets, int64_t G, int32_t cols, T *__restrict__ out,
+    int64_t slots, int64_t groups, int share) {
+    const int per = few::kWaves / share * NB * 16;
+    for (int64_t id = blockIdx.x; id < slots * groups; id += gridDim.x) {
+        const RowTile rt = row_tile(offsets, G, m, 16, id / groups);
         if (rt.lo >= rt.hi) continue;
-        const int64_t j0 = pl.col * BN;
-        const int64_t jn = cols - j0 < BN ? cols - j0 : BN;
+        const int64_t j0 = id % groups * per;
         const bool none = rt.unit >= G;
         const T *w = W + (none ? 0 : rt.unit) * (int64_t)K * cols;
-        C core;
-        core.run({A + rt.lo * K, K, (int)(rt.hi - rt.lo)},
-                 {ACROSS ? w + j0 : w + j0 * K, ACROSS ? cols : K, (int)jn}, none ? 0 : K, bufs);
-        core.each([&](int i, int j, const tile::f32x4 &v) {
-            if (rt.lo + i < rt.hi) store4(out + (rt.lo + i) * cols, j0 + j, cols, v, whole);
-        });
+        __syncthreads();  // the last turn's sums have been read
+        few::products<T, 1, NB>(A + rt.lo * K, (int)(rt.hi - rt.lo), w, j0, cols, none ? 0 : K,
+                                share, [&](int i, int64_t j, const tile::f32x4 &v) {
+                                    few::store4(out + (rt.lo + i) * cols, j, cols, v);
+                                });
     }
 }
 
 // dW[g][j][k] = sum over g's rows p of dY[p][j] X[p][k]: both sides across
 template <typename T, typename O, int BM, int BN, int WM, int WN, bool ALIGNED>
-__global__ __launch_bounds__(WM *WN * 64, BM * BN > 128 * 128 ? 1 : 2) void k_unit_mats(
+__global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_mats(
     const T *__restrict__ dY, const T *__restrict__ X, int64_t m, int32_t d,
-    const int32_t *__restrict__ offsets, int64_t G, int32_t cols, O *__restrict__ dW, bool whole) {
+    const int32_t *__restrict__ offsets, int64_t G, int32_t cols, O *__restrict__ dW) {
     using C = tile::Core<T, BM, BN, WM, WN, true, true, ALIGNED>;
     __shared__ __attribute__((aligned(1024))) char bufs[2 * C::kBytes];
-    const int64_t jt = (cols + BM - 1) / BM, kt = (d + BN - 1) / BN, total = G * jt * kt;
-    for (int64_t id = blockIdx.x; id < (total + 7) / 8 * 8; id += gridDim.x) {
-        const int64_t at = tile::xcd_order(id, total);
-        if (at >= total) continue;
-        const int64_t g = at / (jt * kt);
-        const tile::Place pl = tile::place(at - g * jt * kt, jt, kt);
-        const int64_t j0 = pl.row * BM, k0 = pl.col * BN;
-        const int64_t lo = offset_of(offsets, g, G, m), hi = offset_of(offsets, g + 1, G, m);
-        const int64_t jn = cols - j0 < BM ? cols - j0 : BM, kn = d - k0 < BN ? d - k0 : BN;
-        C core;
-        core.run({dY + lo * cols + j0, cols, (int)jn}, {X + lo * d + k0, d, (int)kn}, hi - lo, bufs);
-        core.each([&](int i, int k, const tile::f32x4 &v) {
-            if (i < jn) store4(dW + (g * cols + j0 + i) * d, k0 + k, d, v, whole);
+    const int64_t jt = (cols + BM - 1) / BM, kt = (d + BN - 1) / BN;
+    tile::run_tiles<C, T, O>(
+        G * jt * kt, bufs,
+        [&](int64_t at, tile::Job<T, O> &j) {
+            const int64_t g = at / (jt * kt);
+            const tile::Place pl = tile::place(at - g * jt * kt, jt, kt);
+            const int64_t j0 = pl.row * BM, k0 = pl.col * BN;
+            const int64_t lo = offset_of(offsets, g, G, m), hi = offset_of(offsets, g + 1, G, m);
+            j.depth = hi - lo;
+            j.m = {dY + lo * cols + j0, cols, (int)(cols - j0 < BM ? cols - j0 : BM)};
+            j.n = {X + lo * d + k0, d, (int)(d - k0 < BN ? d - k0 : BN)};
+            j.out = dW + (g * cols + j0) * d + k0;
+            j.ld = d;
+            return true;
         });
-    }
 }
 
 template <typename F>
@@ -140,68 +146,141 @@ inline bool on(uintptr_t p, int64_t cols, int esize, uintptr_t bytes) {
     return ((p | (uintptr_t)(cols * esize)) & (bytes - 1)) == 0;
 }
 
+inline int64_t tiles_of(int64_t n, int tile) { return (n + tile - 1) / tile; }
+// a width that tiles of 256 pad by more than a fifth beyond those of 128
+inline bool wasteful(int64_t n) { return tiles_of(n, 256) * 256 * 5 > tiles_of(n, 128) * 128 * 6; }
+
+// `aligned`: rows of A, and of W as the product takes them, lie on 16-byte boundaries
 template <typename T, int BM, int BN, int WM, int WN>
 hipError_t unit_rows(const void *A, int64_t m, int32_t K, const void *W, const int32_t *offsets,
-                     int64_t G, int32_t cols, bool across, void *out, hipStream_t st) {
+                     int64_t G, int32_t cols, bool across, bool aligned, void *out,
+                     hipStream_t st) {
     const int64_t slots = m / BM + G + 1;
-    const dim3 grid(tile::grid_of(slots * ((cols + BN - 1) / BN))), block(WM * WN * 64);
-    const int es = (int)sizeof(T);
-    const bool aligned = on(addr(A), K, es, 16) && on(addr(W), across ? cols : K, es, 16);
-    const bool whole = on(addr(out), cols, es, 4 * es);
+    const dim3 grid(tile::grid_of(slots * tiles_of(cols, BN))), block(WM * WN * 64);
     auto go = [&](auto ac, auto al) {
         hipLaunchKernelGGL((k_unit_rows<T, BM, BN, WM, WN, decltype(ac)::value, decltype(al)::value>),
                            grid, block, 0, st, (const T *)A, m, K, (const T *)W, offsets, G, cols,
-                           (T *)out, slots, whole);
+                           (T *)out, slots);
     };
     timing_before(st, "k_unit_rows");
-    if (across && aligned) go(std::true_type(), std::true_type());
-    else if (across) go(std::true_type(), std::false_type());
-    else if (aligned) go(std::false_type(), std::true_type());
-    else go(std::false_type(), std::false_type());
+    if constexpr (BM < 256) {  // the largest tile is for aligned rows only
+        if (!aligned) {
+            if (across) go(std::true_type(), std::false_type());
+            else go(std::false_type(), std::false_type());
+        }
+    }
+    if (aligned) {
+        if (across) go(std::true_type(), std::true_type());
+        else go(std::false_type(), std::true_type());
+    }
+    timing_after(st);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t unit_rows_few(const void *A, int64_t m, int32_t K, const void *W, const int32_t *offsets,
+                         int64_t G, int32_t cols, void *out, hipStream_t st, int n_cu) {
+    const int64_t slots = m / 16 + G + 1, units = G < m ? G : m;
+    const few::Deal d = few::deal(tiles_of(cols, 16), units, (int64_t)K * sizeof(T), n_cu);
+    const int64_t total = slots * d.groups, most = 1 << 24;
+    const dim3 grid((unsigned)(total < most ? total : most)), block(few::kWaves * 64);
+    timing_before(st, "k_unit_rows_few");
+    if (d.nb == 2)
+        hipLaunchKernelGGL((k_unit_rows_few<T, 2>), grid, block, 0, st, (const T *)A, m, K,
+                           (const T *)W, offsets, G, cols, (T *)out, slots, d.groups, d.share);
+    else
+        hipLaunchKernelGGL((k_unit_rows_few<T, 1>), grid, block, 0, st, (const T *)A, m, K,
+                           (const T *)W, offsets, G, cols, (T *)out, slots, d.groups, d.share);
     timing_after(st);
     return hipGetLastError();
 }
 
 template <typename T, typename O, int BM, int BN, int WM, int WN>
 hipError_t unit_mats(const void *dY, const void *X, int64_t m, int32_t d, const int32_t *offsets,
-                     int64_t G, int32_t cols, void *dW, hipStream_t st) {
-    const int64_t total = G * ((cols + BM - 1) / BM) * ((d + BN - 1) / BN);
-    const dim3 grid(tile::grid_of(total)), block(WM * WN * 64);
-    const int es = (int)sizeof(T);
-    const bool aligned = on(addr(dY), cols, es, 16) && on(addr(X), d, es, 16);
-    const bool whole = on(addr(dW), d, (int)sizeof(O), 4 * sizeof(O));
+                     int64_t G, int32_t cols, bool aligned, void *dW, hipStream_t st) {
+    const dim3 grid(tile::grid_of(G * tiles_of(cols, BM) * tiles_of(d, BN))), block(WM * WN * 64);
+    auto go = [&](auto al) {
+        hipLaunchKernelGGL((k_unit_mats<T, O, BM, BN, WM, WN, decltype(al)::value>), grid, block, 0,
+                           st, (const T *)dY, (const T *)X, m, d, offsets, G, cols, (O *)dW);
+    };
     timing_before(st, "k_unit_mats");
-    if (aligned)
-        hipLaunchKernelGGL((k_unit_mats<T, O, BM, BN, WM, WN, true>), grid, block, 0, st,
-                           (const T *)dY, (const T *)X, m, d, offsets, G, cols, (O *)dW, whole);
-    else
-        hipLaunchKernelGGL((k_unit_mats<T, O, BM, BN, WM, WN, false>), grid, block, 0, st,
-                           (const T *)dY, (const T *)X, m, d, offsets, G, cols, (O *)dW, whole);
+    if constexpr (BM < 256) {  // the largest tile is for aligned rows only
+        if (!aligned) go(std::false_type());
+    }
+    if (aligned) go(std::true_type());
     timing_after(st);
     return hipGetLastError();
 }
 
 }  // namespace
 
+// Which tile, from the rows a unit has on average (r) and the number of tiles; in
+// brackets us of the tile taken and of its neighbour, bf16 unless said.
+//   few.h      r <= 16, and tiles of 64 x 128 would not fill the GPU twice or rows
+//              have odd addresses (16 rows to 8 units of 2,048 x 2,048: 14, 64 x 64 19;
+//              100 to 100 of 333 x 250 f32: 12, 64 x 64 22; 32 to 64 of 2,048 x
+//              1,024: 64 x 128 25, few 27)
+//   256 x 256  r >= 512 and a tile for every CU (65,536 rows to 128 of 2,048 x 2,048:
+//              556, 128 x 128 628; r = 384, 64 of 1,024 x 1,024: 97, 128 x 128 86: the
+//              units' last tiles are half empty); 16-byte addresses only (20,000 rows
+//              to 60 of 1,027 x 1,027: 141, 128 x 128 117)
+//   128 x 128  r >= 96 and two for every CU (r = 128 of the 64: 47, 64 x 128 46;
+//              r = 256: 66 and 74)
+//   64 x 128   fewer rows (r = 32 of the 64: 32, 64 x 64 38, 128 x 128 43); 64 x 64
+//              at odd addresses (2,501 rows to 60 of 257 x 515 f16: 14, 64 x 128 19)
+//              and where tiles are few
+// fp32 has 64 x 64 only: bound by its matrix instructions, larger ones gain nothing
+// (16,384 rows to 16 of 2,048 x 2,048: 1,015, 128 x 128 1,043).
 hipError_t launch_unit_rows(const void *A, int64_t m, int32_t K, int dtype, const void *W,
                             const int32_t *offsets, int64_t G, int32_t cols, bool across, void *out,
                             hipStream_t st, int n_cu) {
-    (void)n_cu;
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
-        return unit_rows<T, 128, 128, 2, 2>(A, m, K, W, offsets, G, cols, across, out, st);
+        constexpr int ES = (int)sizeof(T);
+        const bool aligned = on(addr(A), K, ES, 16) && on(addr(W), across ? cols : K, ES, 16);
+        const int64_t units = G < m ? G : m;  // that have rows, at most
+        const int64_t r = m / units;
+        auto tiles = [&](int bm, int bn) { return (m / bm + units / 2) * tiles_of(cols, bn); };
+        if (!across && r <= 16 && (!aligned || units * tiles_of(cols, 128) < 2 * (int64_t)n_cu))
+            return unit_rows_few<T>(A, m, K, W, offsets, G, cols, out, st, n_cu);
+        if constexpr (ES == 2) {
+            if (aligned && r >= 512 && tiles(256, 256) >= n_cu && !wasteful(cols))
+                return unit_rows<T, 256, 256, 2, 4>(A, m, K, W, offsets, G, cols, across, aligned,
+                                                    out, st);
+            if (r >= 96 && tiles(128, 128) >= 2 * (int64_t)n_cu)
+                return unit_rows<T, 128, 128, 2, 2>(A, m, K, W, offsets, G, cols, across, aligned,
+                                                    out, st);
+            if (aligned && units * tiles_of(cols, 128) >= n_cu)
+                return unit_rows<T, 64, 128, 2, 2>(A, m, K, W, offsets, G, cols, across, aligned,
+                                                   out, st);
+        }
+        return unit_rows<T, 64, 64, 2, 2>(A, m, K, W, offsets, G, cols, across, aligned, out, st);
     });
 }
 
+// The same for the matrices' gradient, by the number of tiles: 256 x 256 if there are
+// two for every CU (4,096 rows of 64 units of 1,024 x 1,024, 1,024 tiles: 37, as 128
+// x 128; 65,536 of 128 of 2,048 x 2,048: 665, 128 x 128 784), 128 x 128 if there is
+// one (the 64 units with 64 rows: 34, 64 x 64 48).
 hipError_t launch_unit_mats(const void *dY, const void *X, int64_t m, int32_t d, int dtype,
                             const int32_t *offsets, int64_t G, int32_t cols, int grad_dtype,
                             void *dW, hipStream_t st, int n_cu) {
-    (void)n_cu;
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
+        constexpr int ES = (int)sizeof(T);
+        const bool aligned = on(addr(dY), cols, ES, 16) && on(addr(X), d, ES, 16);
+        auto tiles = [&](int b) { return G * tiles_of(cols, b) * tiles_of(d, b); };
         auto go = [&](auto o) {
             using O = decltype(o);
-            return unit_mats<T, O, 128, 128, 2, 2>(dY, X, m, d, offsets, G, cols, dW, st);
+            if constexpr (ES == 2) {
+                if (aligned && tiles(256) >= 2 * (int64_t)n_cu && !wasteful(cols) && !wasteful(d))
+                    return unit_mats<T, O, 256, 256, 2, 4>(dY, X, m, d, offsets, G, cols, aligned,
+                                                           dW, st);
+                if (tiles(128) >= n_cu)
+                    return unit_mats<T, O, 128, 128, 2, 2>(dY, X, m, d, offsets, G, cols, aligned,
+                                                           dW, st);
+            }
+            return unit_mats<T, O, 64, 64, 2, 2>(dY, X, m, d, offsets, G, cols, aligned, dW, st);
         };
         return grad_dtype == dtype ? go(T()) : go(float());
     });
