@@ -74,8 +74,8 @@ EXPORTS = ["vs_bmu_search_workspace", "vs_bmu_search", "vs_bmu_search_noalloc",
            "vs_row_lookup_backward_workspace", "vs_row_lookup_backward", "vs_route_rows",
            "vs_route_rows_backward", "vs_combine_rows", "vs_combine_rows_backward",
            "vs_q4_bytes", "vs_q4_quantize", "vs_q4_layout", "vs_q4_scores",
-           "vs_unit_products", "vs_unit_products_backward", "vs_norm_rows", "vs_norm_rows_q8",
-           "vs_norm_rows_backward_workspace", "vs_norm_rows_backward", "vs_q8_quantize",
+           "vs_unit_products", "vs_unit_products_backward_workspace", "vs_unit_products_backward",
+           "vs_norm_rows", "vs_norm_rows_q8", "vs_norm_rows_backward_workspace", "vs_norm_rows_backward", "vs_q8_quantize",
            "vs_q8_scores",
            "vs_candidate_norms", "vs_tile_rows", "vs_timing_enable", "vs_timing_read",
            "vs_timing_kernel_name", "vs_status_str", "vs_last_hip_error", "vs_version"]
@@ -164,7 +164,10 @@ def lib() -> ctypes.CDLL:
     L.vs_q4_layout.argtypes = [P, P, I64, I32, I32, P, P]
     L.vs_q4_scores.argtypes = [P, I64, I32, I32, P, I64, I32, I32, P, P]
     L.vs_unit_products.argtypes = [P, I64, I32, I32, P, P, I64, I32, P, P]
-    L.vs_unit_products_backward.argtypes = [P, P, I64, I32, I32, P, P, I64, I32, P, I32, P, P]
+    L.vs_unit_products_backward_workspace.argtypes = [I64, I32, I64, I32]
+    L.vs_unit_products_backward_workspace.restype = SZ
+    L.vs_unit_products_backward.argtypes = [P, P, I64, I32, I32, P, P, I64, I32, P, I32, P, P, SZ,
+                                            P]
     L.vs_norm_rows.argtypes = [P, P, P, I64, I32, I32, F, P, P, P, P]
     L.vs_norm_rows_q8.argtypes = [P, P, P, I64, I32, I32, F, P, P, P, P]
     L.vs_norm_rows_backward_workspace.argtypes = [I64, I32]
@@ -1371,12 +1374,12 @@ def vs_unit_products(Xs, W, offsets, out=None):
 
 
 def vs_unit_products_backward(dYs, Xs, W, offsets, grad_dtype=None, out=None, dW=None,
-                              want_dXs: bool = True, want_dW: bool = True):
+                              workspace=None, want_dXs: bool = True, want_dW: bool = True):
     """Gradients of vs_unit_products: (dXs, dW), dXs[p] = dYs[p] @ W[g] (zeros in
     the rows of no unit) and dW[g] = dYs[g's rows].T @ Xs[g's rows], of
     grad_dtype (dYs's type, the default, or torch.float32).  What is not wanted
     is None."""
-    lib()
+    L = lib()
     code = _rows_arg(dYs, "dYs")
     dev = dYs.device
     _rows_arg(Xs, "Xs", dev, dYs.dtype)
@@ -1394,8 +1397,10 @@ def vs_unit_products_backward(dYs, Xs, W, offsets, grad_dtype=None, out=None, dW
         raise ValueError("neither dXs nor dW is wanted")
     out = _new(out, "out", dYs.dtype, (m, d), dYs) if want_dXs else None
     dW = _new(dW, "dW", grad_dtype, (g, cols, d), dYs) if want_dW else None
+    need = L.vs_unit_products_backward_workspace(m, d, g, cols) if want_dW else 0
+    ws, size, _held = _scratch(need, dYs, workspace)
     _run("vs_unit_products_backward", dev, dYs.data_ptr(), Xs.data_ptr(), m, d, code, W.data_ptr(),
-         offsets_at, g, cols, _ptr(out), grad_code, _ptr(dW))
+         offsets_at, g, cols, _ptr(out), grad_code, _ptr(dW), ws, size)
     return out, dW
 
 
@@ -1403,23 +1408,33 @@ def _norm_args(X, weight, residual, name="X", rname="residual"):
     """The type, rows and columns of a norm's input; addresses of the weight and
     of the residual (None: none)."""
     code = _rows_arg(X, name)
-    n, d = X.shape
+    shape, dtype, dev = X.shape, X.dtype, X.device
+    n, d = shape
     if d > _MAX_I32:
         raise VsError(2, "d")
     w = r = None
     if weight is not None:
-        _dev(weight, "weight", X.dtype, 1)
-        if weight.device != X.device:
-            raise ValueError(f"weight is on {weight.device}, {name} on {X.device}")
-        if weight.numel() != d:
+        if not (getattr(weight, "dtype", None) is dtype and weight.device == dev and
+                weight.shape == shape[1:] and weight.is_contiguous()):
+            _dev(weight, "weight", dtype, 1)  # says what is wrong
+            if weight.device != dev:
+                raise ValueError(f"weight is on {weight.device}, {name} on {dev}")
             raise ValueError(f"weight holds {weight.numel()} values, the rows {d}")
         w = weight.data_ptr()
     if residual is not None:
-        _rows_arg(residual, rname, X.device, X.dtype)
-        if residual.shape != X.shape:
+        if not (getattr(residual, "dtype", None) is dtype and residual.device == dev and
+                residual.shape == shape and residual.is_contiguous()):
+            _rows_arg(residual, rname, dev, dtype)  # says what is wrong
             raise ValueError(f"{rname} must be {n} x {d}, as {name} is")
         r = residual.data_ptr()
     return code, n, d, w, r
+
+
+def _like(t, name, X, dtype=None):
+    """_new with the shape of the contiguous X, by the cheapest allocation."""
+    if t is not None:
+        return _out(t, name, dtype or X.dtype, tuple(X.shape), X.device)
+    return _torch().empty_like(X) if dtype is None else _torch().empty_like(X, dtype=dtype)
 
 
 def _norm_sum(X, H, residual):
@@ -1428,7 +1443,7 @@ def _norm_sum(X, H, residual):
         if H is not None:
             raise ValueError("H is written only with a residual")
         return X, None
-    H = _new(H, "H", X.dtype, tuple(X.shape), X)
+    H = _like(H, "H", X)
     return H, H.data_ptr()
 
 
@@ -1446,7 +1461,7 @@ def vs_norm_rows(X, weight=None, eps: float = 1e-6, residual=None, out=None, H=N
     code, n, d, w, r = _norm_args(X, weight, residual)
     if _grad_wanted(X, weight, residual):
         _outside_autograd("vs_norm_rows")
-    out = _new(out, "out", X.dtype, (n, d), X)
+    out = _like(out, "out", X)
     H, h = _norm_sum(X, H, residual)
     rstd = _new(rstd, "rstd", _torch().float32, (n,), X)
     _run("vs_norm_rows", X.device, X.data_ptr(), r, w, n, d, code, float(eps), h, out.data_ptr(),
@@ -1464,7 +1479,7 @@ def vs_norm_rows_q8(X, weight=None, eps: float = 1e-6, residual=None, codes=None
     code, n, d, w, r = _norm_args(X, weight, residual)
     if _grad_wanted(X, weight, residual):
         _outside_autograd("vs_norm_rows_q8")
-    codes = _new(codes, "codes", torch.int8, (n, d), X)
+    codes = _like(codes, "codes", X, torch.int8)
     scales = _new(scales, "scales", torch.float32, (n,), X)
     H, h = _norm_sum(X, H, residual)
     _run("vs_norm_rows_q8", X.device, X.data_ptr(), r, w, n, d, code, float(eps), h,
@@ -1494,7 +1509,7 @@ def vs_norm_rows_backward(dY, H, weight, rstd, dH=None, grad_dtype=None, out=Non
     if weight is None and dweight is not None:
         raise ValueError("dweight without a weight")
     want_dweight = weight is not None and (want_dweight or dweight is not None)
-    out = _new(out, "out", dY.dtype, (n, d), dY)
+    out = _like(out, "out", dY)
     dweight = _new(dweight, "dweight", grad_dtype, (d,), dY) if want_dweight else None
     need = L.vs_norm_rows_backward_workspace(n, d) if want_dweight else 0
     ws, size, _held = _scratch(need, dY, workspace)
@@ -1511,7 +1526,7 @@ def vs_q8_quantize(T, codes=None, scales=None):
     code, n, d, _, _ = _norm_args(T, None, None, "T")
     if T.requires_grad:
         _outside_autograd("vs_q8_quantize")
-    codes = _new(codes, "codes", torch.int8, (n, d), T)
+    codes = _like(codes, "codes", T, torch.int8)
     scales = _new(scales, "scales", torch.float32, (n,), T)
     _run("vs_q8_quantize", T.device, T.data_ptr(), n, d, code, codes.data_ptr(), scales.data_ptr())
     return codes, scales

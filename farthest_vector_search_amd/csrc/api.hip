@@ -1225,19 +1225,29 @@ VS_API int vs_unit_products(const void *Xs, int64_t m, int32_t d, int32_t dtype,
     return VS_OK;
 }
 
+VS_API size_t vs_unit_products_backward_workspace(int64_t m, int32_t d, int64_t n_groups,
+                                                  int32_t cols) {
+    if (unit_check(m, d, vs::kF32, n_groups, cols)) return 0;
+    return vs::unit_mats_workspace(m, n_groups, cols, d);
+}
+
 VS_API int vs_unit_products_backward(const void *dYs, const void *Xs, int64_t m, int32_t d,
                                      int32_t dtype, const void *W, const int32_t *offsets,
                                      int64_t n_groups, int32_t cols, void *dXs,
-                                     int32_t grad_dtype, void *dW, void *stream) {
+                                     int32_t grad_dtype, void *dW, void *workspace,
+                                     size_t workspace_bytes, void *stream) {
     if (bad_dtype(dtype) || bad_dtype(grad_dtype) ||
         (grad_dtype != dtype && grad_dtype != vs::kF32))
         return VS_ERR_DTYPE;
     if (const int s = unit_check(m, d, dtype, n_groups, cols)) return s;
-    if ((m > 0 && (!dYs || (dXs && !W) || (dW && !Xs))) || !offsets || (!dXs && !dW && m > 0))
+    const size_t need = dW ? vs::unit_mats_workspace(m, n_groups, cols, d) : 0;
+    if ((m > 0 && (!dYs || (dXs && !W) || (dW && !Xs))) || !offsets || (!dXs && !dW && m > 0) ||
+        (need > 0 && !workspace))
         return VS_ERR_NULL;
     if (!al_type(dYs, dtype) || !al_type(Xs, dtype) || !al_type(W, dtype) || !al4(offsets) ||
-        !al_type(dXs, dtype) || !al_type(dW, grad_dtype))
+        !al_type(dXs, dtype) || !al_type(dW, grad_dtype) || (need > 0 && !al256(workspace)))
         return VS_ERR_ALIGN;
+    if (workspace_bytes < need) return VS_ERR_WORKSPACE;
     int n_cu = 0;
     if (const int s = device_ready(&n_cu)) return s;
     const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
@@ -1246,7 +1256,7 @@ VS_API int vs_unit_products_backward(const void *dYs, const void *Xs, int64_t m,
                                         st, n_cu));
     if (dW)  // units without rows get zeros, so also where m is 0
         VS_TRY_HIP(vs::launch_unit_mats(dYs, Xs, m, d, dtype, offsets, n_groups, cols, grad_dtype,
-                                        dW, st, n_cu));
+                                        dW, workspace, st, n_cu));
     return VS_OK;
 }
 

@@ -107,28 +107,44 @@ __global__ __launch_bounds__(few::kWaves * 64) void k_unit_rows_few(
     }
 }
 
-// dW[g][j][k] = sum over g's rows p of dY[p][j] X[p][k]: both sides across
+// dW[g][j][k] = sum over g's rows p of dY[p][j] X[p][k]: both sides across.  With
+// `parts` > 1 each unit's rows are cut into so many equal runs, whose sums stand one
+// array of matrices behind the other.
 template <typename T, typename O, int BM, int BN, int WM, int WN, bool ALIGNED>
 __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_mats(
     const T *__restrict__ dY, const T *__restrict__ X, int64_t m, int32_t d,
-    const int32_t *__restrict__ offsets, int64_t G, int32_t cols, O *__restrict__ dW) {
+    const int32_t *__restrict__ offsets, int64_t G, int32_t cols, O *__restrict__ dW, int parts) {
     using C = tile::Core<T, BM, BN, WM, WN, true, true, ALIGNED>;
     __shared__ __attribute__((aligned(1024))) char bufs[2 * C::kBytes];
     const int64_t jt = (cols + BM - 1) / BM, kt = (d + BN - 1) / BN;
     tile::run_tiles<C, T, O>(
-        G * jt * kt, bufs,
+        G * parts * jt * kt, bufs,
         [&](int64_t at, tile::Job<T, O> &j) {
-            const int64_t g = at / (jt * kt);
-            const tile::Place pl = tile::place(at - g * jt * kt, jt, kt);
+            const int64_t run = at / (jt * kt), g = run / parts, part = run - g * parts;
+            const tile::Place pl = tile::place(at - run * jt * kt, jt, kt);
             const int64_t j0 = pl.row * BM, k0 = pl.col * BN;
-            const int64_t lo = offset_of(offsets, g, G, m), hi = offset_of(offsets, g + 1, G, m);
+            const int64_t first = offset_of(offsets, g, G, m), end = offset_of(offsets, g + 1, G, m);
+            const int64_t rows = end > first ? end - first : 0;
+            const int64_t lo = first + rows * part / parts, hi = first + rows * (part + 1) / parts;
             j.depth = hi - lo;
             j.m = {dY + lo * cols + j0, cols, (int)(cols - j0 < BM ? cols - j0 : BM)};
             j.n = {X + lo * d + k0, d, (int)(d - k0 < BN ? d - k0 : BN)};
-            j.out = dW + (g * cols + j0) * d + k0;
+            j.out = dW + ((part * G + g) * cols + j0) * d + k0;
             j.ld = d;
             return true;
         });
+}
+
+// the sums of a unit's runs of rows, in their order
+template <typename O>
+__global__ __launch_bounds__(256) void k_unit_join(const float *__restrict__ sums, int parts,
+                                                   int64_t n, O *__restrict__ dW) {
+    const int64_t step = (int64_t)gridDim.x * 256;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
+        float s = sums[i];
+        for (int p = 1; p < parts; ++p) s += sums[p * n + i];
+        dW[i] = narrow<O>(s);
+    }
 }
 
 template <typename F>
@@ -197,11 +213,12 @@ hipError_t unit_rows_few(const void *A, int64_t m, int32_t K, const void *W, con
 
 template <typename T, typename O, int BM, int BN, int WM, int WN>
 hipError_t unit_mats(const void *dY, const void *X, int64_t m, int32_t d, const int32_t *offsets,
-                     int64_t G, int32_t cols, bool aligned, void *dW, hipStream_t st) {
-    const dim3 grid(tile::grid_of(G * tiles_of(cols, BM) * tiles_of(d, BN))), block(WM * WN * 64);
+                     int64_t G, int32_t cols, bool aligned, void *dW, int parts, hipStream_t st) {
+    const dim3 grid(tile::grid_of(G * parts * tiles_of(cols, BM) * tiles_of(d, BN)));
+    const dim3 block(WM * WN * 64);
     auto go = [&](auto al) {
         hipLaunchKernelGGL((k_unit_mats<T, O, BM, BN, WM, WN, decltype(al)::value>), grid, block, 0,
-                           st, (const T *)dY, (const T *)X, m, d, offsets, G, cols, (O *)dW);
+                           st, (const T *)dY, (const T *)X, m, d, offsets, G, cols, (O *)dW, parts);
     };
     timing_before(st, "k_unit_mats");
     if constexpr (BM < 256) {  // the largest tile is for aligned rows only
@@ -258,29 +275,69 @@ hipError_t launch_unit_rows(const void *A, int64_t m, int32_t K, int dtype, cons
     });
 }
 
+// Runs that a unit's rows are cut into for the matrices' gradient: enough for two tiles
+// for every CU (of 128 x 128 if there are 64 of those and they pad little, else of 64 x
+// 64), of 128 rows on average at least, 32 at most.
+static int64_t mats_tiles(int64_t G, int32_t cols, int32_t d, int b) {
+    return G * tiles_of(cols, b) * tiles_of(d, b);
+}
+static bool mats_large(int64_t G, int32_t cols, int32_t d) {
+    const int64_t large = mats_tiles(G, cols, d, 128), small = mats_tiles(G, cols, d, 64);
+    return large >= 64 && large * 4 * 5 <= small * 6;
+}
+static int mats_parts(int64_t m, int64_t G, int32_t cols, int32_t d) {
+    const int64_t tiles = mats_tiles(G, cols, d, mats_large(G, cols, d) ? 128 : 64);
+    const int64_t want = (512 + tiles - 1) / tiles, most = m / G / 128;
+    const int64_t parts = want < most ? want : most;
+    return (int)(parts < 1 ? 1 : parts > 32 ? 32 : parts);
+}
+
+size_t unit_mats_workspace(int64_t m, int64_t G, int32_t cols, int32_t d) {
+    const int parts = mats_parts(m, G, cols, d);
+    return parts > 1 ? (size_t)parts * (size_t)G * (size_t)cols * (size_t)d * 4 : 0;
+}
+
 // The same for the matrices' gradient, by the number of tiles: 256 x 256 if there are
 // two for every CU (4,096 rows of 64 units of 1,024 x 1,024, 1,024 tiles: 37, as 128
 // x 128; 65,536 of 128 of 2,048 x 2,048: 665, 128 x 128 784), 128 x 128 if there is
-// one (the 64 units with 64 rows: 34, 64 x 64 48).
+// one (the 64 units with 64 rows: 34, 64 x 64 48).  Where tiles are few and units have
+// many rows, the rows are cut into runs, which a second kernel joins (65,536 rows to 4
+// units of 64 x 64: 19, in one run 111; of 512 x 512: 62 and 179).
 hipError_t launch_unit_mats(const void *dY, const void *X, int64_t m, int32_t d, int dtype,
                             const int32_t *offsets, int64_t G, int32_t cols, int grad_dtype,
-                            void *dW, hipStream_t st, int n_cu) {
+                            void *dW, void *ws, hipStream_t st, int n_cu) {
+    const int parts = mats_parts(m, G, cols, d);
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int ES = (int)sizeof(T);
         const bool aligned = on(addr(dY), cols, ES, 16) && on(addr(X), d, ES, 16);
-        auto tiles = [&](int b) { return G * tiles_of(cols, b) * tiles_of(d, b); };
+        auto tiles = [&](int b) { return mats_tiles(G, cols, d, b); };
         auto go = [&](auto o) {
             using O = decltype(o);
+            if (parts > 1) {
+                hipError_t e;
+                if (ES == 2 && mats_large(G, cols, d))
+                    e = unit_mats<T, float, 128, 128, 2, 2>(dY, X, m, d, offsets, G, cols, aligned,
+                                                            ws, parts, st);
+                else
+                    e = unit_mats<T, float, 64, 64, 2, 2>(dY, X, m, d, offsets, G, cols, aligned,
+                                                          ws, parts, st);
+                if (e != hipSuccess) return e;
+                const int64_t n = G * (int64_t)cols * d, want = (n + 255) / 256;
+                const int64_t most = (int64_t)n_cu * 32;
+                hipLaunchKernelGGL((k_unit_join<O>), dim3((unsigned)(want < most ? want : most)),
+                                   dim3(256), 0, st, (const float *)ws, parts, n, (O *)dW);
+                return hipGetLastError();
+            }
             if constexpr (ES == 2) {
                 if (aligned && tiles(256) >= 2 * (int64_t)n_cu && !wasteful(cols) && !wasteful(d))
                     return unit_mats<T, O, 256, 256, 2, 4>(dY, X, m, d, offsets, G, cols, aligned,
-                                                           dW, st);
+                                                           dW, 1, st);
                 if (tiles(128) >= n_cu)
                     return unit_mats<T, O, 128, 128, 2, 2>(dY, X, m, d, offsets, G, cols, aligned,
-                                                           dW, st);
+                                                           dW, 1, st);
             }
-            return unit_mats<T, O, 64, 64, 2, 2>(dY, X, m, d, offsets, G, cols, aligned, dW, st);
+            return unit_mats<T, O, 64, 64, 2, 2>(dY, X, m, d, offsets, G, cols, aligned, dW, 1, st);
         };
         return grad_dtype == dtype ? go(T()) : go(float());
     });

@@ -161,7 +161,8 @@ hipError_t launch_unit_rows(const void *A, int64_t m, int32_t K, int dtype, cons
                             void *out, hipStream_t st, int n_cu);
 hipError_t launch_unit_mats(const void *dY, const void *X, int64_t m, int32_t d, int dtype,
                             const int32_t *offsets, int64_t G, int32_t cols, int grad_dtype,
-                            void *dW, hipStream_t st, int n_cu);
+                            void *dW, void *ws, hipStream_t st, int n_cu);
+size_t unit_mats_workspace(int64_t m, int64_t G, int32_t cols, int32_t d);
 // Rows over their root mean square (norm.hip); R, w, H, rstd, dH, dw may be null
 hipError_t launch_norm_rows(const void *X, const void *R, const void *w, int64_t n, int32_t d,
                             int dtype, float eps, void *H, void *Y, float *rstd, hipStream_t st,

@@ -579,15 +579,17 @@ int vs_q4_scores(const void *x, int64_t nq, int32_t d, int32_t dtype, const void
  * outside [0, m] is held inside, and nothing outside the arrays is read.
  * m in [0, 2^31-1] (0: only dW is written), n_groups in [1, 2^31-2], d and cols
  * in [1, 2^20].  Addresses are aligned to their element.  Inputs and outputs
- * must not overlap.
+ * must not overlap.  The workspace is for dW: it may be NULL where dW is, or
+ * where the size query returns 0 (units of few rows, or many matrices).
  */
 int vs_unit_products(const void *Xs, int64_t m, int32_t d, int32_t dtype, const void *W,
                      const int32_t *offsets, int64_t n_groups, int32_t cols, void *Ys,
                      void *stream);
+size_t vs_unit_products_backward_workspace(int64_t m, int32_t d, int64_t n_groups, int32_t cols);
 int vs_unit_products_backward(const void *dYs, const void *Xs, int64_t m, int32_t d,
                               int32_t dtype, const void *W, const int32_t *offsets,
                               int64_t n_groups, int32_t cols, void *dXs, int32_t grad_dtype,
-                              void *dW, void *stream);
+                              void *dW, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
  * Rows divided by their root mean square (with weight d^-1/2 and eps 0: the

@@ -40,9 +40,9 @@ def test_unit_products(L):
 
 def test_unit_products_backward(L):
     def call(dYs=FAKE, Xs=FAKE, m=5, d=8, dtype=0, W=FAKE, off=FAKE, g=3, cols=4, dXs=FAKE, gd=0,
-             dW=FAKE):
+             dW=FAKE, ws=FAKE, size=BIG):
         return L.vs_unit_products_backward(_P(dYs), _P(Xs), m, d, dtype, _P(W), _P(off), g, cols,
-                                           _P(dXs), gd, _P(dW), None)
+                                           _P(dXs), gd, _P(dW), _P(ws), size, None)
     assert call(dtype=3) == DTYPE
     assert call(gd=1) == DTYPE and call(dtype=1, gd=2) == DTYPE and call(gd=-1) == DTYPE
     for bad in (dict(m=-1), dict(m=2 ** 31), dict(d=0), dict(d=WIDE), dict(cols=0),
@@ -57,6 +57,16 @@ def test_unit_products_backward(L):
     for name in ("dYs", "Xs", "W", "off", "dXs", "dW"):
         assert call(**{name: FAKE + 2}) == ALIGN
     assert call(dtype=1, gd=0, dW=FAKE + 2) == ALIGN
+    # units of many rows and few, small matrices are summed in runs of rows
+    need = L.vs_unit_products_backward_workspace(4096, 64, 4, 32)
+    assert need >= 2 * 4 * 64 * 32 * 4 and need % (4 * 64 * 32 * 4) == 0
+    many = dict(m=4096, d=64, g=4, cols=32)
+    assert call(**many, size=need - 1) == WORKSPACE
+    assert call(**many, ws=0) == NULL and call(**many, ws=FAKE + 64) == ALIGN
+    assert L.vs_unit_products_backward_workspace(100, 64, 4, 32) == 0
+    assert L.vs_unit_products_backward_workspace(1 << 20, 2048, 64, 2048) == 0
+    for bad in ((-1, 64, 4, 32), (100, 0, 4, 32), (100, 64, 0, 32), (100, 64, 4, 0)):
+        assert L.vs_unit_products_backward_workspace(*bad) == 0
 
 
 def test_norm_rows(L):

@@ -90,6 +90,18 @@ def test_unit_products(m, G, d, cols, kind, t):
 @pytest.mark.parametrize("t", [torch.float16, torch.bfloat16])
 def test_matrices_gradient_in_32_bits(t):
     check_all(rng(41), 210, 4, 48, 80, "skew", t, grad=torch.float32)
+    check_all(rng(41), 3000, 3, 48, 80, "skew", t, grad=torch.float32)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("m,G,d,cols,kind", [(3000, 2, 24, 40, "skew"), (6000, 3, 65, 33, "one"),
+                                             (2600, 2, 8, 8, "none"), (5001, 1, 130, 70, "even"),
+                                             (40000, 4, 16, 16, "skew")])
+def test_matrices_gradient_in_runs(m, G, d, cols, kind, t):
+    """Units of many rows with few, small matrices: their rows are summed in runs.
+    One addition more per run (32 at most), which the bound's K covers."""
+    assert vs.lib().vs_unit_products_backward_workspace(m, d, G, cols) > 0
+    check_all(rng(53, m, d), m, G, d, cols, kind, t)
 
 
 def whole(r, shape, t, top=3):
@@ -258,7 +270,9 @@ def test_refusals():
             (lambda: vs.vs_unit_products_backward(dY, X, W, off, grad_dtype=torch.float16),
              vs.VsError),
             (lambda: vs.vs_unit_products_backward(dY, X, W, off, want_dXs=False, want_dW=False),
-             ValueError)):
+             ValueError),
+            (lambda: vs.vs_unit_products_backward(f(4096, 4), f(4096, 8), W, off,
+                                                  workspace=f(8)), ValueError)):
         with pytest.raises(error):
             call()
     for call in (lambda: vs.vs_unit_products(X, W.clone().requires_grad_(), off),
