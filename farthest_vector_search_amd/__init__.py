@@ -1532,14 +1532,24 @@ def vs_q8_quantize(T, codes=None, scales=None):
     return codes, scales
 
 
+_int8 = _float32 = None
+
+
 def _q8_arg(t, name, scales, dev):
-    """8-bit codes with one float32 scale per row; their addresses."""
-    torch = _torch()
-    _dev(t, name, torch.int8, 2)
-    _dev(scales, f"{name}_scales", torch.float32)
-    if t.device != dev or scales.device != dev:
-        raise ValueError(f"{name} is on {t.device} and its scales on {scales.device}, x on {dev}")
-    if scales.numel() != t.shape[0]:
+    """8-bit codes with one float32 scale per row on the call's device; their
+    addresses."""
+    global _int8, _float32
+    if _int8 is None:
+        torch = _torch()
+        _int8, _float32 = torch.int8, torch.float32
+    if not (getattr(t, "dtype", None) is _int8 and getattr(scales, "dtype", None) is _float32 and
+            t.is_cuda and t.device == dev and scales.device == dev and t.dim() == 2 and
+            scales.numel() == t.shape[0] and t.is_contiguous() and scales.is_contiguous()):
+        _dev(t, name, _int8, 2)  # says what is wrong
+        _dev(scales, f"{name}_scales", _float32)
+        if t.device != dev or scales.device != dev:
+            raise ValueError(f"{name} is on {t.device} and its scales on {scales.device}, x on "
+                             f"{dev}")
         raise ValueError(f"{name}_scales holds {scales.numel()} values for {t.shape[0]} rows")
     return t.data_ptr(), scales.data_ptr()
 
@@ -1563,7 +1573,7 @@ def vs_q8_scores(x, x_scales, table, table_scales, out_dtype=None, out=None):
     out_code = _dtype(out_dtype, "out_dtype")
     if x_scales.requires_grad or table_scales.requires_grad:
         _outside_autograd("vs_q8_scores")
-    out = _new(out, "out", out_dtype, (nq, nc), x)
+    out = _new(out, "out", out_dtype, (nq, nc), x_scales)
     _run("vs_q8_scores", dev, x_at, xs_at, nq, d, t_at, ts_at, nc, out_code, out.data_ptr())
     return out
 

@@ -68,7 +68,7 @@ template <typename O>
 hipError_t q8_scores_few(const int8_t *x, const float *xs, int64_t nq, int32_t d, const int8_t *t,
                          const float *ts, int64_t nc, O *y, hipStream_t st, int n_cu) {
     const few::Deal e = few::deal(tiles_of(nc, 16), tiles_of(nq, 16), d, n_cu);
-    const int64_t total = tiles_of(nq, 16) * e.groups, most = 1 << 24;
+    const int64_t total = tiles_of(nq, 16) * e.groups, most = tile::kMostGroups;
     const dim3 grid((unsigned)(total < most ? total : most)), block(few::kWaves * 64);
     timing_before(st, "k_q8_scores_few");
     if (e.nb == 2)

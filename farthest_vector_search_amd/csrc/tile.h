@@ -103,18 +103,20 @@ struct Side {
 // One 16-byte piece a lane from memory into LDS: lane l's lands at lds + 16 l.  In
 // assembly because the compiler, which cannot tell the two buffers apart, would wait
 // for it before every LDS read; who uses it waits itself (wait_vmcnt) before the
-// barrier behind which the piece is read.
-// m0, which names the place in LDS, is put back for the compiler.
+// barrier behind which the piece is read.  m0, which names the place in LDS, is put
+// back for the compiler; the s_nop is what the load has to stay behind a vector
+// instruction's write of its scalar address (five states), which the compiler does
+// not see here.
 __device__ __forceinline__ void fetch(const void *base, uint32_t off, uint32_t lds) {
     uint32_t m0;
-    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\t"
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 4\n\t"
                  "global_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
                  : "=&s"(m0)
                  : "v"(off), "s"(base), "s"(lds));
 }
 __device__ __forceinline__ void fetch_from(const void *p, uint32_t lds) {
     uint32_t m0;
-    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\t"
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\ts_nop 4\n\t"
                  "global_load_lds_dwordx4 %1, off\n\ts_mov_b32 m0, %0"
                  : "=&s"(m0)
                  : "v"(p), "s"(lds));
@@ -561,8 +563,11 @@ __device__ __forceinline__ void run_tiles(int64_t total, char *bufs, FJ job) {
     }
 }
 
+// Workgroups for `total` tiles, a multiple of 8.  The most keeps the number of threads
+// below 2^32, which a launch counts in 32 bits.
+constexpr int64_t kMostGroups = 1 << 20;
 inline unsigned grid_of(int64_t total) {
-    const int64_t want = (total + 7) / 8 * 8, most = 1 << 24;
+    const int64_t want = (total + 7) / 8 * 8, most = kMostGroups;
     return (unsigned)(want < most ? want : most);
 }
 

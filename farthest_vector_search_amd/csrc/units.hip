@@ -4,14 +4,14 @@
 //   products   Y[p][j]  = sum_k X[p][k] W[g][j][k]    offsets[g] <= p < offsets[g + 1]
 //   rows       dX[p][k] = sum_j dY[p][j] W[g][j][k]
 //   matrices   dW[g][j][k] = sum over g's rows p of dY[p][j] X[p][k]
-// Rows of no unit (offsets[n_groups] .. m - 1) give zeros.
+// Rows of no unit (before offsets[0], or from offsets[n_groups] on) give zeros.
 //
-// The rows' tiles are found on the device: unit g owns the tiles T(g) ..
-// T(g + 1) - 1 with T(g) = offsets[g] / B + g for tiles of B rows, which is
-// never fewer than its rows need, so that the grid follows from m and the number
-// of units alone (a unit's spare tile ends at once).  T rises, and a wave finds
-// its tile's unit by looking at 64 of them at a time.  The rows of no unit count
-// as one unit more.
+// The rows' tiles are found on the device.  The rows form runs: those before the
+// first unit, each unit's, those behind the last.  Run u owns the tiles T(u) ..
+// T(u + 1) - 1 with T(u) = begin(u) / B + u for tiles of B rows, which is never fewer
+// than its rows need, so that the grid follows from m and the number of units alone
+// (a run's spare tile ends at once).  T rises, and a wave finds its tile's run by
+// looking at 64 of them at a time.
 #include <type_traits>
 
 #include "few.h"
@@ -23,40 +23,50 @@ namespace vs {
 
 namespace {
 
-__device__ __forceinline__ int64_t offset_of(const int32_t *__restrict__ offsets, int64_t g,
-                                             int64_t G, int64_t m) {
-    if (g > G) return m;
+// a place read from the offsets, held inside the rows
+__device__ __forceinline__ int64_t place_of(const int32_t *__restrict__ offsets, int64_t g,
+                                            int64_t m) {
     const int64_t o = offsets[g];
     return o < 0 ? 0 : o > m ? m : o;
 }
 
+// where run u of the rows begins: run 0 those before the first unit, run g + 1 unit g,
+// run G + 1 those behind the last unit
+__device__ __forceinline__ int64_t run_begin(const int32_t *__restrict__ offsets, int64_t u,
+                                             int64_t G, int64_t m) {
+    return u == 0 ? 0 : u > G + 1 ? m : place_of(offsets, u - 1, m);
+}
+
 struct RowTile {
-    int64_t unit, lo, hi;  // rows lo .. hi - 1 of the unit (G: no unit)
+    int64_t unit, lo, hi;  // rows lo .. hi - 1 of the unit
+    bool none;             // they belong to none (unit is 0)
 };
 
 // The rows of tile `slot`; the whole wave takes part.
 __device__ __forceinline__ RowTile row_tile(const int32_t *__restrict__ offsets, int64_t G,
                                             int64_t m, int rows, int64_t slot) {
     const int lane = threadIdx.x & 63;
-    // unit in [lo, hi): T(lo) <= slot, and T(hi) > slot or hi = G + 1
-    int64_t lo = 0, hi = G + 1;
+    // run in [lo, hi): T(lo) <= slot, and T(hi) > slot or hi = G + 2
+    int64_t lo = 0, hi = G + 2;
     while (hi - lo > 1) {
         const int64_t width = (hi - lo + 63) / 64;
-        const int64_t g = lo + lane * width;
-        const bool below = g < hi && offset_of(offsets, g, G, m) / rows + g <= slot;
+        const int64_t u = lo + lane * width;
+        const bool below = u < hi && run_begin(offsets, u, G, m) / rows + u <= slot;
         const unsigned long long set = __ballot(below) | 1;
         const int last = 63 - __clzll(set);
         lo += last * width;
         hi = lo + width < hi ? lo + width : hi;
     }
+    const int64_t o = run_begin(offsets, lo, G, m), e = run_begin(offsets, lo + 1, G, m);
     RowTile t;
-    t.unit = lo;
-    const int64_t o = offset_of(offsets, lo, G, m), e = offset_of(offsets, lo + 1, G, m);
-    const int64_t first = o / rows + lo;
-    t.lo = o + (slot - first) * rows;
+    t.none = lo == 0 || lo > G;
+    t.unit = t.none ? 0 : lo - 1;
+    t.lo = o + (slot - (o / rows + lo)) * rows;
     t.hi = t.lo + rows < e ? t.lo + rows : e;
     return t;
 }
+// tiles of `rows` rows that cover m rows of G units
+inline int64_t slots_of(int64_t m, int64_t G, int rows) { return m / rows + G + 2; }
 
 // out[p][j] = sum_k A[p][k] B(g)(j, k): B = W[g][j][k], or W[g][k][j] (ACROSS).
 template <typename T, int BM, int BN, int WM, int WN, bool ACROSS, bool ALIGNED>
@@ -74,10 +84,9 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_rows(
             const RowTile rt = row_tile(offsets, G, m, BM, pl.row);
             if (rt.lo >= rt.hi) return false;
             const int64_t j0 = pl.col * BN;
-            const bool none = rt.unit >= G;
-            const T *w = W + (none ? 0 : rt.unit) * (int64_t)K * cols;
+            const T *w = W + rt.unit * (int64_t)K * cols;
             const int jn = (int)(cols - j0 < BN ? cols - j0 : BN);
-            j.depth = none ? 0 : K;
+            j.depth = rt.none ? 0 : K;
             j.m = {A + rt.lo * K, K, (int)(rt.hi - rt.lo)};
             j.n = {ACROSS ? w + j0 : w + j0 * K, ACROSS ? cols : K, jn};
             j.out = out + rt.lo * cols + j0;
@@ -97,10 +106,9 @@ __global__ __launch_bounds__(few::kWaves * 64) void k_unit_rows_few(
         const RowTile rt = row_tile(offsets, G, m, 16, id / groups);
         if (rt.lo >= rt.hi) continue;
         const int64_t j0 = id % groups * per;
-        const bool none = rt.unit >= G;
-        const T *w = W + (none ? 0 : rt.unit) * (int64_t)K * cols;
+        const T *w = W + rt.unit * (int64_t)K * cols;
         __syncthreads();  // the last turn's sums have been read
-        few::products<T, 1, NB>(A + rt.lo * K, (int)(rt.hi - rt.lo), w, j0, cols, none ? 0 : K,
+        few::products<T, 1, NB>(A + rt.lo * K, (int)(rt.hi - rt.lo), w, j0, cols, rt.none ? 0 : K,
                                 share, [&](int i, int64_t j, const tile::f32x4 &v) {
                                     few::store4(out + (rt.lo + i) * cols, j, cols, v);
                                 });
@@ -123,7 +131,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_mats(
             const int64_t run = at / (jt * kt), g = run / parts, part = run - g * parts;
             const tile::Place pl = tile::place(at - run * jt * kt, jt, kt);
             const int64_t j0 = pl.row * BM, k0 = pl.col * BN;
-            const int64_t first = offset_of(offsets, g, G, m), end = offset_of(offsets, g + 1, G, m);
+            const int64_t first = place_of(offsets, g, m), end = place_of(offsets, g + 1, m);
             const int64_t rows = end > first ? end - first : 0;
             const int64_t lo = first + rows * part / parts, hi = first + rows * (part + 1) / parts;
             j.depth = hi - lo;
@@ -171,7 +179,7 @@ template <typename T, int BM, int BN, int WM, int WN>
 hipError_t unit_rows(const void *A, int64_t m, int32_t K, const void *W, const int32_t *offsets,
                      int64_t G, int32_t cols, bool across, bool aligned, void *out,
                      hipStream_t st) {
-    const int64_t slots = m / BM + G + 1;
+    const int64_t slots = slots_of(m, G, BM);
     const dim3 grid(tile::grid_of(slots * tiles_of(cols, BN))), block(WM * WN * 64);
     auto go = [&](auto ac, auto al) {
         hipLaunchKernelGGL((k_unit_rows<T, BM, BN, WM, WN, decltype(ac)::value, decltype(al)::value>),
@@ -196,9 +204,9 @@ hipError_t unit_rows(const void *A, int64_t m, int32_t K, const void *W, const i
 template <typename T>
 hipError_t unit_rows_few(const void *A, int64_t m, int32_t K, const void *W, const int32_t *offsets,
                          int64_t G, int32_t cols, void *out, hipStream_t st, int n_cu) {
-    const int64_t slots = m / 16 + G + 1, units = G < m ? G : m;
+    const int64_t slots = slots_of(m, G, 16), units = G < m ? G : m;
     const few::Deal d = few::deal(tiles_of(cols, 16), units, (int64_t)K * sizeof(T), n_cu);
-    const int64_t total = slots * d.groups, most = 1 << 24;
+    const int64_t total = slots * d.groups, most = tile::kMostGroups;
     const dim3 grid((unsigned)(total < most ? total : most)), block(few::kWaves * 64);
     timing_before(st, "k_unit_rows_few");
     if (d.nb == 2)

@@ -571,8 +571,8 @@ int vs_q4_scores(const void *x, int64_t nq, int32_t d, int32_t dtype, const void
  *                     VS_F32, else VS_ERR_DTYPE); zeros for a unit without
  *                     rows.  dXs or dW may be NULL, then it is not computed;
  *                     Xs may be NULL where dW is, W where dXs is.
- * Rows of no unit (offsets[n_groups] .. m - 1) give rows of zeros, and what they
- * hold is never used.  Xs, dXs are m x d, Ys, dYs m x cols, all of `dtype`, as
+ * Rows of no unit (offsets[n_groups] .. m - 1, and any before offsets[0]) give rows
+ * of zeros, and what they hold is never used.  Xs, dXs are m x d, Ys, dYs m x cols, all of `dtype`, as
  * is W (n_groups x cols x d).  Sums are fp32 (products of VS_F16 and VS_BF16
  * values are exact) and rounded once.  offsets is taken as
  * vs_group_rows makes it, int32[n_groups + 1]; a place read from it that lies

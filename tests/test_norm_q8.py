@@ -123,7 +123,8 @@ def backward_tol(dY, h, rstd, w, dX, dw, t, gt):
 @pytest.mark.parametrize("t", TYPES)
 @pytest.mark.parametrize("more", [False, True])
 @pytest.mark.parametrize("n,d", [(1, 1), (3, 7), (9, 64), (700, 100), (5, 513), (1100, 768), (1023, 257),
-                                 (6, 4099), (1300, 2048), (40, 8192), (7, 20001), (600, 9000)])
+                                 (6, 4099), (1300, 2048), (40, 8192), (7, 20001), (600, 9000),
+                                 (2, 1 << 20)])
 def test_norm_rows_backward(n, d, more, t):
     r = rng(62, n, d, more)
     x, x64, res, r64, w, w64 = inputs(r, n, d, t, more)
@@ -513,6 +514,21 @@ def test_rows_scored_and_sent_to_units():
     # every value is a few hundred fp32 roundings from its inputs, which are of size 1 to 10
     close(H2, h2, 400 * V * 10)
     close(out, y2, 800 * V * 10)
+
+
+def test_more_tiles_than_a_launch_takes():
+    """A table of very many short rows, for one query and for some."""
+    nc, d = 150000000, 2
+    gen = torch.Generator(device=dev()).manual_seed(8)
+    t = torch.empty(nc, d, dtype=torch.int8, device=dev()).random_(-100, 101, generator=gen)
+    one = torch.ones(nc, device=dev())
+    at = torch.tensor([0, 1, 2 ** 27 - 1, 2 ** 27, 2 ** 27 + 129, nc - 1], device=dev())
+    for nq in (1, 9):
+        q = t[nc // 2:nc // 2 + nq].contiguous()
+        got = vs.vs_q8_scores(q, one[:nq], t, one)
+        assert np.array_equal(host(got[:, at]), host(q) @ host(t[at]).T)
+        assert int(torch.count_nonzero(got)) > nq * nc // 2  # every part was written
+        del got
 
 
 def test_past_32_bit_offsets():

@@ -230,6 +230,60 @@ def test_places_outside_the_rows():
             close(out, Y, bound(d, mag, Y, torch.bfloat16))
 
 
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("m,first,d,cols", [(20, 3, 24, 16), (400, 150, 64, 72), (3000, 1000, 33, 40)])
+def test_rows_before_the_first_unit(m, first, d, cols, t):
+    """Places that begin behind row 0: the rows before belong to no unit."""
+    r = rng(54, m)
+    G = 3
+    off = first + make_offsets(r, m - first, G, "skew")
+    X, X64 = rows(r, (m, d), t)
+    W, W64 = rows(r, (G, cols, d), t)
+    dY, dY64 = rows(r, (m, cols), t)
+    X[:first], dY[:first] = float("nan"), float("inf")
+    (Y, dX, dW), (mY, mX, mW) = reference(X64, W64, off, dY64)
+    close(vs.vs_unit_products(X, W, i32(off)), Y, bound(d, mY, Y, t))
+    gX, gW = vs.vs_unit_products_backward(dY, X, W, i32(off))
+    close(gX, dX, bound(cols, mX, dX, t))
+    close(gW, dW, bound(np.diff(off)[:, None, None], mW, dW, t))
+
+
+def test_very_many_units():
+    """More tiles than a launch takes at a time."""
+    m, G, d, cols = 500, 2500000, 2, 3
+    r = rng(55)
+    units = np.sort(r.choice(G, m // 2, replace=False))
+    units = np.sort(np.concatenate([units, units[:m - m // 2]]))
+    off = np.searchsorted(units, np.arange(G + 1)).astype(np.int32)
+    (X, X64), (W, W64), (dY, dY64) = (whole(r, s, torch.float32)
+                                      for s in ((m, d), (G, cols, d), (m, cols)))
+    Y = vs.vs_unit_products(X, W, i32(off))
+    dX, dW = vs.vs_unit_products_backward(dY, X, W, i32(off))
+    assert np.array_equal(host(Y), np.einsum("mk,mjk->mj", X64, W64[units]))
+    assert np.array_equal(host(dX), np.einsum("mj,mjk->mk", dY64, W64[units]))
+    want = np.zeros((G, cols, d))
+    np.add.at(want, units, dY64[:, :, None] * X64[:, None, :])
+    assert np.array_equal(host(dW), want)
+
+
+@pytest.mark.parametrize("t,step", [(torch.float32, 2.0 ** -149), (torch.float16, 2.0 ** -24),
+                                    (torch.bfloat16, 2.0 ** -133)])
+@pytest.mark.parametrize("m", [6, 100, 700])
+def test_subnormal_factors(m, t, step):
+    """Subnormal values are multiplied, not flushed: small multiples of the smallest
+    one times small whole numbers."""
+    r = rng(56, m)
+    d, cols = 24, 32
+    off = np.array([0, m // 2, m], np.int32)
+    X64 = r.integers(-3, 4, (m, d)) * step
+    X = torch.from_numpy(X64).to(t).to(dev())
+    (W, W64), (dY, dY64) = whole(r, (2, cols, d), t, 2), whole(r, (m, cols), t, 2)
+    (Y, _, dW), _ = reference(X64, W64, off, dY64)
+    assert np.array_equal(host(vs.vs_unit_products(X, W, i32(off))), host(torch.from_numpy(Y).to(t)))
+    _, gW = vs.vs_unit_products_backward(dY, X, W, i32(off))
+    assert np.array_equal(host(gW), host(torch.from_numpy(dW).to(t)))
+
+
 def test_no_rows():
     W = torch.ones(3, 5, 8, device=dev())
     off = i32([0, 0, 0, 0])
