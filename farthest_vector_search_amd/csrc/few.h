@@ -3,7 +3,7 @@
 //
 // Bound by reading the matrix, so there are no tiles in LDS: a wave takes NB blocks of
 // 16 of its rows and loads them straight into the matrix instruction's layout, 16 bytes
-// a lane at any address, 256 bytes of k at a time (16 KiB in flight with NB = 2); the
+// a lane at any address, 256 bytes of k at a time (8 KiB of the matrix with NB = 2); the
 // few rows' own, 16 MB at most, come from the caches the same way.  Where there are too
 // few blocks to fill the GPU, the waves of a workgroup share a block along k, and the
 // first of them adds their sums in order.

@@ -438,10 +438,10 @@ struct Core {
 
     // Results into rows of `out` (`ld` elements apart), rows 0 .. rows - 1 and
     // columns 0 .. cols - 1 of the tile.  convert(a, b, sums of block row a and block
-    // column b) gives their floats.  A wave's blocks go through its part of the buffers, which no wave
-    // reads any more: stored from the matrix instruction's layout, 32 bytes
+    // column b) gives their floats.  A wave's blocks go through its part of the buffers,
+    // which no wave reads any more: stored from the matrix instruction's layout, 32 bytes
     // of a row at a time, 8,192 x 8,192 bf16 results of 128 products each took 71 us,
-    // whole lines at a time OUT_TIME.
+    // whole lines at a time 51.
     template <typename O, typename F>
     __device__ __forceinline__ void put(char *bufs, O *out, int64_t ld, int rows, int cols,
                                         F convert) const {

@@ -1,5 +1,5 @@
 // vs_types.h -- element types and short vectors of the table operators
-// (group.hip, rows.hip, q4.hip).
+// (group.hip, rows.hip, q4.hip) and of units.hip, norm.hip and q8.hip.
 //
 // Arithmetic is fp32 throughout: values are widened on load (exactly) and
 // rounded once, to nearest even, when they are stored.

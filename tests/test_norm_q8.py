@@ -230,6 +230,46 @@ def test_rows_that_are_not_finite(d, t):
 
 
 @pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("n,d", [(1030, 1024), (700, 1600), (1030, 2800), (40, 6000), (1030, 6000),
+                                 (1030, 6008), (9, 12001), (1030, 12000), (5, 24000), (1025, 17000),
+                                 (3, 40003)])
+def test_norm_rows_wide(n, d, t):
+    """Wide rows, few and many: one row a workgroup of each size, held or read twice."""
+    r = rng(71, n, d)
+    x, x64, res, r64, w, w64 = inputs(r, n, d, t, True)
+    h, rstd, y = norm_ref(x64, r64, w64, EPS, t)
+    Y, H, rs = vs.vs_norm_rows(x, w, EPS, residual=res)
+    assert np.array_equal(host(H), h)
+    close(Y, y, 1.01 * (r_of(d) + 2 * V + U(t)) * np.abs(y) + SUB[t])
+    codes, scales, _ = vs.vs_norm_rows_q8(H, w, EPS)
+    c, top = codes_ref(h, w64)
+    assert np.array_equal(host(codes), c)
+    scale = (top * rstd / 127)[:, 0]
+    close(scales, scale, 1.01 * (r_of(d) + 3 * V) * scale)
+    assert np.array_equal(host(vs.vs_q8_quantize(H)[0]), codes_ref(h, np.ones(d))[0])
+    dY, dY64 = rows(r, (n, d), t)
+    dX, dw = backward_ref(dY64, h, rstd, w64, None)
+    gX, gw = vs.vs_norm_rows_backward(dY, H, w, rs)
+    tx, tw = backward_tol(dY64, h, rstd, w64, dX, dw, t, t)
+    close(gX, dX, tx)
+    close(gw, dw, tw)
+
+
+def test_codes_beside_borders():
+    """Values next to the borders of rows with any largest magnitude: the float
+    nearest to each border, and the two beside it on both sides."""
+    r = rng(72)
+    top = np.concatenate([r.uniform(1, 2, 300), 2.0 ** -130 * r.uniform(1, 2, 20),
+                          2.0 ** 126 * r.uniform(1, 2, 20)]).astype(np.float32)[:, None]
+    border = np.concatenate([np.arange(0.5, 127), -np.arange(0.5, 127)])
+    v = (border * top.astype(np.float64) / 127).astype(np.float32)
+    bits = v.view(np.int32)
+    x = np.concatenate([top] + [(bits + k).view(np.float32) for k in (-2, -1, 0, 1, 2)], 1)
+    got = host(vs.vs_q8_quantize(torch.from_numpy(x).to(dev()))[0])
+    assert np.array_equal(got, codes_ref(x, np.ones(x.shape[1]))[0])
+
+
+@pytest.mark.parametrize("t", TYPES)
 def test_codes_at_borders(t):
     """Quotients exactly halfway between whole numbers go to the even one, and
     those one step of the type beside them to their side."""
