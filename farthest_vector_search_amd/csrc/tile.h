@@ -100,26 +100,40 @@ struct Side {
     int rows;
 };
 
-// One 16-byte piece a lane from memory into LDS: lane l's lands at lds + 16 l.  In
-// assembly because the compiler, which cannot tell the two buffers apart, would wait
+// A piece of 16 or 4 bytes a lane from memory into LDS: lane l's lands at lds + l pieces.
+// In assembly because the compiler, which cannot tell the two buffers apart, would wait
 // for it before every LDS read; who uses it waits itself (wait_vmcnt) before the
 // barrier behind which the piece is read.  m0, which names the place in LDS, is put
 // back for the compiler; the s_nop is what the load has to stay behind a vector
 // instruction's write of its scalar address (five states), which the compiler does
 // not see here.
+template <int PIECE>
 __device__ __forceinline__ void fetch(const void *base, uint32_t off, uint32_t lds) {
     uint32_t m0;
-    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 4\n\t"
-                 "global_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
-                 : "=&s"(m0)
-                 : "v"(off), "s"(base), "s"(lds));
+    if constexpr (PIECE == 16)
+        asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 4\n\t"
+                     "global_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
+                     : "=&s"(m0)
+                     : "v"(off), "s"(base), "s"(lds));
+    else
+        asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 4\n\t"
+                     "global_load_lds_dword %1, %2\n\ts_mov_b32 m0, %0"
+                     : "=&s"(m0)
+                     : "v"(off), "s"(base), "s"(lds));
 }
+template <int PIECE>
 __device__ __forceinline__ void fetch_from(const void *p, uint32_t lds) {
     uint32_t m0;
-    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\ts_nop 4\n\t"
-                 "global_load_lds_dwordx4 %1, off\n\ts_mov_b32 m0, %0"
-                 : "=&s"(m0)
-                 : "v"(p), "s"(lds));
+    if constexpr (PIECE == 16)
+        asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\ts_nop 4\n\t"
+                     "global_load_lds_dwordx4 %1, off\n\ts_mov_b32 m0, %0"
+                     : "=&s"(m0)
+                     : "v"(p), "s"(lds));
+    else
+        asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\ts_nop 4\n\t"
+                     "global_load_lds_dword %1, off\n\ts_mov_b32 m0, %0"
+                     : "=&s"(m0)
+                     : "v"(p), "s"(lds));
 }
 
 // a value that is the same in all lanes, in scalar registers
@@ -133,26 +147,31 @@ __device__ __forceinline__ P *uniform(P *p) {
 }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// R rows of a side, moved by W waves.  ALIGNED: 16-byte loads straight into LDS; all
-// addresses, ld and (along) the number of k's are multiples of 16 bytes.  Else
-// through registers, 16 bytes a load at any address.
-template <typename T, int R, int W, bool ACROSS, bool ALIGNED>
+// R rows of a side, moved by W waves.  PIECE of 16 or 4: loads of so many bytes straight
+// into LDS; all addresses, ld and (along) the number of k's are multiples of them.
+// PIECE of 0: through registers, 16 bytes a load at any address.  us in pieces of 4 and
+// through registers: 16,384 rows to 16 units of 2,049 x 2,049 fp32 1,160 and 1,334;
+// 20,000 to 60 of 1,026 x 1,026 bf16 121 and 133; 1,000 codes' rows of 1,004 over 20,000
+// 41 and 45.  In pieces of 16: 1,024 x 1,024 67, 1,008 codes 38.
+template <typename T, int R, int W, bool ACROSS, int PIECE>
 struct Mover {
     static constexpr int ES = (int)sizeof(T);
     static constexpr int N = 16 / ES;               // elements a chunk
     static constexpr int K = kStep / ES;            // k's a step
     static constexpr int kChunks = R * ES / 16;     // chunks of a k's row (across)
-    static constexpr int kLoads = R / 8 / W;        // loads a wave
+    static constexpr int kBytes = PIECE ? PIECE : 16;  // a lane's of a load
+    static constexpr int kLoads = R * kStep / (64 * kBytes * W);  // loads a wave
+    static constexpr int kIn = 16 / kBytes;         // loads' parts of a chunk
     static_assert(R % (8 * W) == 0, "every wave moves the same number of pieces");
     typedef unsigned __int128 Bits;
     typedef typename std::conditional<
         ES == 1, uint8_t, typename std::conditional<ES == 2, uint16_t, uint32_t>::type>::type Whole;
     const T *base;
     int64_t ld;
-    uint32_t off[kLoads];  // bytes from a step's first k to the lane's chunk
-    int part[kLoads];      // the chunk's first k inside the step (along), its k (across)
+    uint32_t off[kLoads];  // bytes from a step's first k to the lane's
+    int part[kLoads];      // the lane's first k inside the step (along), its k (across)
     int left[kLoads];      // across, unaligned: elements from the chunk's first to the row's end
-    u32x4 held[ALIGNED ? 1 : kLoads];
+    u32x4 held[PIECE ? 1 : kLoads];
     int held_have;  // k's of the step in `held`
     bool tiny;
     bool whole;     // along: all of the step's chunks are there
@@ -162,20 +181,21 @@ struct Mover {
         ld = s.ld;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int piece = wave * kLoads + i;  // 64 chunks, 1 KiB of LDS
+            const int piece = (wave * kLoads + i) * 64 + lane;  // its place in LDS
+            const int chunk = piece / kIn, e = piece % kIn * (kBytes / ES);  // element of it
             if constexpr (!ACROSS) {
-                const int r = piece * 8 + lane / 8;
-                const int c = (lane & 7) ^ (r >> 1 & 7);
+                const int r = chunk / 8;
+                const int c = (chunk & 7) ^ (r >> 1 & 7);
                 const int row = r < s.rows ? r : s.rows - 1;
-                off[i] = (uint32_t)row * (uint32_t)(s.ld * ES) + c * 16;
-                part[i] = c * N;
+                off[i] = (uint32_t)row * (uint32_t)(s.ld * ES) + (c * N + e) * ES;
+                part[i] = c * N + e;
             } else {
-                const int k = (piece * 64 + lane) / kChunks, at = (piece * 64 + lane) % kChunks;
-                const int c = at ^ (ES == 2 ? (k & 3) << 1 : k & 4);
-                const bool in = c * N < s.rows;
-                off[i] = (uint32_t)k * (uint32_t)(s.ld * ES) + (in ? c * 16 : 0);
+                const int k = chunk / kChunks, at = chunk % kChunks;
+                const int c = (at ^ (ES == 2 ? (k & 3) << 1 : k & 4)) * N + e;
+                const bool in = c < s.rows;
+                off[i] = (uint32_t)k * (uint32_t)(s.ld * ES) + (in ? c * ES : 0);
                 part[i] = k;
-                left[i] = in ? s.rows - c * N : s.rows;
+                left[i] = in ? s.rows - c : s.rows;
             }
         }
     }
@@ -185,19 +205,19 @@ struct Mover {
         return reinterpret_cast<const char *>(base + (ACROSS ? k0 * ld : k0));
     }
 
-    // ALIGNED: load i of the step at `step`; lds: where the side's buffer begins
+    // PIECE: load i of the step at `step`; lds: where the side's buffer begins
     __device__ __forceinline__ void load(int i, const char *step, uint32_t lds, int wave) const {
-        fetch(step, off[i], lds + (wave * kLoads + i) * 1024);
+        fetch<PIECE>(step, off[i], lds + (wave * kLoads + i) * 64 * kBytes);
     }
     // the same for a step of which only `have` k's are there
     __device__ __forceinline__ void load_part(int i, const char *step, uint32_t lds, int wave,
                                               int have) const {
         const char *p = step + off[i];
         if (part[i] >= have) p = reinterpret_cast<const char *>(&g_zeros);
-        fetch_from(p, lds + (wave * kLoads + i) * 1024);
+        fetch_from<PIECE>(p, lds + (wave * kLoads + i) * 64 * kBytes);
     }
 
-    // Not ALIGNED: the step at k0, of which `have` k's are there, into registers ...
+    // No PIECE: the step at k0, of which `have` k's are there, into registers ...
     // Of a chunk that ends behind its row, the row's last 16 bytes are loaded, and
     // shifted into place when they are written, so that all loads are whole and none
     // waits for another.  Rows of fewer than 16 bytes go by elements.
@@ -282,7 +302,7 @@ __device__ __forceinline__ u32x4 fragment(const char *lds, int b, int h, int lan
     }
 }
 
-template <typename T, int BM, int BN, int WM, int WN, bool M_ACROSS, bool N_ACROSS, bool ALIGNED>
+template <typename T, int BM, int BN, int WM, int WN, bool M_ACROSS, bool N_ACROSS, int PIECE>
 struct Core {
     static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
     static constexpr int MB = BM / WM / 16, NB = BN / WN / 16;  // blocks of a wave
@@ -290,8 +310,8 @@ struct Core {
     static constexpr int kBytes = (BM + BN) * kStep;            // of a buffer
     static constexpr int K = kStep / (int)sizeof(T);
     typedef typename Sum<T>::type Acc;
-    typedef Mover<T, BM, kWaves, M_ACROSS, ALIGNED> MMover;
-    typedef Mover<T, BN, kWaves, N_ACROSS, ALIGNED> NMover;
+    typedef Mover<T, BM, kWaves, M_ACROSS, PIECE> MMover;
+    typedef Mover<T, BN, kWaves, N_ACROSS, PIECE> NMover;
     struct Frags {
         u32x4 m[MB], n[NB];
     };
@@ -363,7 +383,7 @@ struct Core {
         const int l = fresh(lane);
         mm.set(ms, wave, l);
         nm.set(ns, wave, l);
-        if constexpr (ALIGNED) {
+        if constexpr (PIECE > 0) {
             const int first = (int)((depth - 1) % K) + 1;
             count_to<MMover::kLoads>(
                 [&](auto i) { mm.load_part(i, mm.from(0), lds_at(bufs), wave, first); });
@@ -392,7 +412,7 @@ struct Core {
         count_to<MB * NB>([&](auto q) { acc[q / NB][q % NB] = Acc{0, 0, 0, 0}; });
         if (depth <= 0) return;
         const int64_t steps = (depth + K - 1) / K;
-        if constexpr (ALIGNED) {
+        if constexpr (PIECE > 0) {
             const int first = (int)((depth - 1) % K) + 1;
             const uint32_t lds = lds_at(bufs);
             const char *mstep = uniform(mm.from(first)), *nstep = uniform(nm.from(first));  // step 1's

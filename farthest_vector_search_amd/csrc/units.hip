@@ -68,13 +68,18 @@ __device__ __forceinline__ RowTile row_tile(const int32_t *__restrict__ offsets,
 // tiles of `rows` rows that cover m rows of G units
 inline int64_t slots_of(int64_t m, int64_t G, int rows) { return m / rows + G + 2; }
 
-// out[p][j] = sum_k A[p][k] B(g)(j, k): B = W[g][j][k], or W[g][k][j] (ACROSS).
-template <typename T, int BM, int BN, int WM, int WN, bool ACROSS, bool ALIGNED>
+// out[p][j] = sum_k A[p][k] B(g)(j, k): B = W[g][j][k], or W[g][k][j] (ACROSS).  Bound
+// by the matrix cores where units have many rows (8,192 rows to one unit of 8,192 x 8,192
+// bf16: 979 us, 1,123 TFLOP/s, across 891 us, 1,235 TFLOP/s), with 65,536 rows to 128 of
+// 2,048 x 2,048 547 us (1,005 TFLOP/s: a unit's last tile is half empty on average); fp32
+// 1,012 us for 16,384 to 16 of 2,048 x 2,048 (136 TFLOP/s).  By reading W where they have
+// few: 1,024 rows to 64 of 1,024 x 1,024 30 us (4.6 TB/s).
+template <typename T, int BM, int BN, int WM, int WN, bool ACROSS, int PIECE>
 __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_rows(
     const T *__restrict__ A, int64_t m, int32_t K, const T *__restrict__ W,
     const int32_t *__restrict__ offsets, int64_t G, int32_t cols, T *__restrict__ out,
     int64_t slots) {
-    using C = tile::Core<T, BM, BN, WM, WN, false, ACROSS, ALIGNED>;
+    using C = tile::Core<T, BM, BN, WM, WN, false, ACROSS, PIECE>;
     __shared__ __attribute__((aligned(1024))) char bufs[2 * C::kBytes];
     const int64_t ctiles = (cols + BN - 1) / BN;
     tile::run_tiles<C, T, T>(
@@ -96,6 +101,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_rows(
 }
 
 // The same along k for units of few rows: 16 rows a tile, `groups` workgroups for each.
+// Bound by reading W: 32 rows to 64 units of 2,048 x 1,024 bf16 24 us (4.5 TB/s).
 template <typename T, int NB>
 __global__ __launch_bounds__(few::kWaves * 64) void k_unit_rows_few(
     const T *__restrict__ A, int64_t m, int32_t K, const T *__restrict__ W,
@@ -117,12 +123,14 @@ __global__ __launch_bounds__(few::kWaves * 64) void k_unit_rows_few(
 
 // dW[g][j][k] = sum over g's rows p of dY[p][j] X[p][k]: both sides across.  With
 // `parts` > 1 each unit's rows are cut into so many equal runs, whose sums stand one
-// array of matrices behind the other.
-template <typename T, typename O, int BM, int BN, int WM, int WN, bool ALIGNED>
+// array of matrices behind the other.  Bound by the matrix cores where units have many
+// rows (8,192 of one, 8,192 x 8,192 bf16: 770 us, 1,429 TFLOP/s), by writing dW where they
+// have few (64 rows to 64 of 1,024 x 1,024: 35 us, 3.8 TB/s).
+template <typename T, typename O, int BM, int BN, int WM, int WN, int PIECE>
 __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_mats(
     const T *__restrict__ dY, const T *__restrict__ X, int64_t m, int32_t d,
     const int32_t *__restrict__ offsets, int64_t G, int32_t cols, O *__restrict__ dW, int parts) {
-    using C = tile::Core<T, BM, BN, WM, WN, true, true, ALIGNED>;
+    using C = tile::Core<T, BM, BN, WM, WN, true, true, PIECE>;
     __shared__ __attribute__((aligned(1024))) char bufs[2 * C::kBytes];
     const int64_t jt = (cols + BM - 1) / BM, kt = (d + BN - 1) / BN;
     tile::run_tiles<C, T, O>(
@@ -174,29 +182,41 @@ inline int64_t tiles_of(int64_t n, int tile) { return (n + tile - 1) / tile; }
 // a width that tiles of 256 pad by more than a fifth beyond those of 128
 inline bool wasteful(int64_t n) { return tiles_of(n, 256) * 256 * 5 > tiles_of(n, 128) * 128 * 6; }
 
-// `aligned`: rows of A, and of W as the product takes them, lie on 16-byte boundaries
+// the bytes that rows at p and q move in, by the boundaries they lie on: 16, 4 or (0) any
+inline int piece_of(uintptr_t p, int64_t pcols, uintptr_t q, int64_t qcols, int esize) {
+    auto both = [&](uintptr_t b) { return on(p, pcols, esize, b) && on(q, qcols, esize, b); };
+    return both(16) ? 16 : both(4) ? 4 : 0;
+}
+
+// f(piece as a constant); tiles of 256 are for pieces of 16, and fp32 has none of 0
+template <typename T, int BM, typename F>
+void by_piece(int piece, F f) {
+    if constexpr (BM < 256) {
+        if (piece == 4) f(std::integral_constant<int, 4>());
+        if constexpr (sizeof(T) < 4)
+            if (piece == 0) f(std::integral_constant<int, 0>());
+    }
+    if (piece == 16) f(std::integral_constant<int, 16>());
+}
+
+// `piece`: of the rows of A, and of W as the product takes them
 template <typename T, int BM, int BN, int WM, int WN>
 hipError_t unit_rows(const void *A, int64_t m, int32_t K, const void *W, const int32_t *offsets,
-                     int64_t G, int32_t cols, bool across, bool aligned, void *out,
+                     int64_t G, int32_t cols, bool across, int piece, void *out,
                      hipStream_t st) {
     const int64_t slots = slots_of(m, G, BM);
     const dim3 grid(tile::grid_of(slots * tiles_of(cols, BN))), block(WM * WN * 64);
-    auto go = [&](auto ac, auto al) {
-        hipLaunchKernelGGL((k_unit_rows<T, BM, BN, WM, WN, decltype(ac)::value, decltype(al)::value>),
+    auto go = [&](auto ac, auto pc) {
+        hipLaunchKernelGGL((k_unit_rows<T, BM, BN, WM, WN, decltype(ac)::value, decltype(pc)::value>),
                            grid, block, 0, st, (const T *)A, m, K, (const T *)W, offsets, G, cols,
                            (T *)out, slots);
     };
+    auto way = [&](auto pc) {
+        if (across) go(std::true_type(), pc);
+        else go(std::false_type(), pc);
+    };
     timing_before(st, "k_unit_rows");
-    if constexpr (BM < 256) {  // the largest tile is for aligned rows only
-        if (!aligned) {
-            if (across) go(std::true_type(), std::false_type());
-            else go(std::false_type(), std::false_type());
-        }
-    }
-    if (aligned) {
-        if (across) go(std::true_type(), std::true_type());
-        else go(std::false_type(), std::true_type());
-    }
+    by_piece<T, BM>(piece, way);
     timing_after(st);
     return hipGetLastError();
 }
@@ -221,18 +241,15 @@ hipError_t unit_rows_few(const void *A, int64_t m, int32_t K, const void *W, con
 
 template <typename T, typename O, int BM, int BN, int WM, int WN>
 hipError_t unit_mats(const void *dY, const void *X, int64_t m, int32_t d, const int32_t *offsets,
-                     int64_t G, int32_t cols, bool aligned, void *dW, int parts, hipStream_t st) {
+                     int64_t G, int32_t cols, int piece, void *dW, int parts, hipStream_t st) {
     const dim3 grid(tile::grid_of(G * parts * tiles_of(cols, BM) * tiles_of(d, BN)));
     const dim3 block(WM * WN * 64);
-    auto go = [&](auto al) {
-        hipLaunchKernelGGL((k_unit_mats<T, O, BM, BN, WM, WN, decltype(al)::value>), grid, block, 0,
+    auto go = [&](auto pc) {
+        hipLaunchKernelGGL((k_unit_mats<T, O, BM, BN, WM, WN, decltype(pc)::value>), grid, block, 0,
                            st, (const T *)dY, (const T *)X, m, d, offsets, G, cols, (O *)dW, parts);
     };
     timing_before(st, "k_unit_mats");
-    if constexpr (BM < 256) {  // the largest tile is for aligned rows only
-        if (!aligned) go(std::false_type());
-    }
-    if (aligned) go(std::true_type());
+    by_piece<T, BM>(piece, go);
     timing_after(st);
     return hipGetLastError();
 }
@@ -247,8 +264,8 @@ hipError_t unit_mats(const void *dY, const void *X, int64_t m, int32_t d, const 
 //              1,024: 64 x 128 25, few 27)
 //   256 x 256  r >= 512 and a tile for every CU (65,536 rows to 128 of 2,048 x 2,048:
 //              556, 128 x 128 628; r = 384, 64 of 1,024 x 1,024: 97, 128 x 128 86: the
-//              units' last tiles are half empty); 16-byte addresses only (20,000 rows
-//              to 60 of 1,027 x 1,027: 141, 128 x 128 117)
+//              units' last tiles are half empty); 16-byte addresses only (through
+//              registers, 20,000 rows to 60 of 1,027 x 1,027: 141, 128 x 128 117)
 //   128 x 128  r >= 96 and two for every CU (r = 128 of the 64: 47, 64 x 128 46;
 //              r = 256: 66 and 74)
 //   64 x 128   fewer rows (r = 32 of the 64: 32, 64 x 64 38, 128 x 128 43); 64 x 64
@@ -262,7 +279,8 @@ hipError_t launch_unit_rows(const void *A, int64_t m, int32_t K, int dtype, cons
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int ES = (int)sizeof(T);
-        const bool aligned = on(addr(A), K, ES, 16) && on(addr(W), across ? cols : K, ES, 16);
+        const int piece = piece_of(addr(A), K, addr(W), across ? cols : K, ES);
+        const bool aligned = piece == 16;
         const int64_t units = G < m ? G : m;  // that have rows, at most
         const int64_t r = m / units;
         auto tiles = [&](int bm, int bn) { return (m / bm + units / 2) * tiles_of(cols, bn); };
@@ -270,16 +288,16 @@ hipError_t launch_unit_rows(const void *A, int64_t m, int32_t K, int dtype, cons
             return unit_rows_few<T>(A, m, K, W, offsets, G, cols, out, st, n_cu);
         if constexpr (ES == 2) {
             if (aligned && r >= 512 && tiles(256, 256) >= n_cu && !wasteful(cols))
-                return unit_rows<T, 256, 256, 2, 4>(A, m, K, W, offsets, G, cols, across, aligned,
+                return unit_rows<T, 256, 256, 2, 4>(A, m, K, W, offsets, G, cols, across, piece,
                                                     out, st);
             if (r >= 96 && tiles(128, 128) >= 2 * (int64_t)n_cu)
-                return unit_rows<T, 128, 128, 2, 2>(A, m, K, W, offsets, G, cols, across, aligned,
+                return unit_rows<T, 128, 128, 2, 2>(A, m, K, W, offsets, G, cols, across, piece,
                                                     out, st);
             if (aligned && units * tiles_of(cols, 128) >= n_cu)
-                return unit_rows<T, 64, 128, 2, 2>(A, m, K, W, offsets, G, cols, across, aligned,
+                return unit_rows<T, 64, 128, 2, 2>(A, m, K, W, offsets, G, cols, across, piece,
                                                    out, st);
         }
-        return unit_rows<T, 64, 64, 2, 2>(A, m, K, W, offsets, G, cols, across, aligned, out, st);
+        return unit_rows<T, 64, 64, 2, 2>(A, m, K, W, offsets, G, cols, across, piece, out, st);
     });
 }
 
@@ -318,18 +336,20 @@ hipError_t launch_unit_mats(const void *dY, const void *X, int64_t m, int32_t d,
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int ES = (int)sizeof(T);
-        const bool aligned = on(addr(dY), cols, ES, 16) && on(addr(X), d, ES, 16);
+        const int piece = piece_of(addr(dY), cols, addr(X), d, ES);
         auto tiles = [&](int b) { return mats_tiles(G, cols, d, b); };
         auto go = [&](auto o) {
             using O = decltype(o);
             if (parts > 1) {
-                hipError_t e;
-                if (ES == 2 && mats_large(G, cols, d))
-                    e = unit_mats<T, float, 128, 128, 2, 2>(dY, X, m, d, offsets, G, cols, aligned,
-                                                            ws, parts, st);
-                else
-                    e = unit_mats<T, float, 64, 64, 2, 2>(dY, X, m, d, offsets, G, cols, aligned,
-                                                          ws, parts, st);
+                auto sums = [&] {
+                    if constexpr (ES == 2)
+                        if (mats_large(G, cols, d))
+                            return unit_mats<T, float, 128, 128, 2, 2>(dY, X, m, d, offsets, G, cols,
+                                                                       piece, ws, parts, st);
+                    return unit_mats<T, float, 64, 64, 2, 2>(dY, X, m, d, offsets, G, cols, piece,
+                                                             ws, parts, st);
+                };
+                const hipError_t e = sums();
                 if (e != hipSuccess) return e;
                 const int64_t n = G * (int64_t)cols * d, want = (n + 255) / 256;
                 const int64_t most = (int64_t)n_cu * 32;
@@ -338,14 +358,14 @@ hipError_t launch_unit_mats(const void *dY, const void *X, int64_t m, int32_t d,
                 return hipGetLastError();
             }
             if constexpr (ES == 2) {
-                if (aligned && tiles(256) >= 2 * (int64_t)n_cu && !wasteful(cols) && !wasteful(d))
-                    return unit_mats<T, O, 256, 256, 2, 4>(dY, X, m, d, offsets, G, cols, aligned,
+                if (piece == 16 && tiles(256) >= 2 * (int64_t)n_cu && !wasteful(cols) && !wasteful(d))
+                    return unit_mats<T, O, 256, 256, 2, 4>(dY, X, m, d, offsets, G, cols, piece,
                                                            dW, 1, st);
                 if (tiles(128) >= n_cu)
-                    return unit_mats<T, O, 128, 128, 2, 2>(dY, X, m, d, offsets, G, cols, aligned,
+                    return unit_mats<T, O, 128, 128, 2, 2>(dY, X, m, d, offsets, G, cols, piece,
                                                            dW, 1, st);
             }
-            return unit_mats<T, O, 64, 64, 2, 2>(dY, X, m, d, offsets, G, cols, aligned, dW, 1, st);
+            return unit_mats<T, O, 64, 64, 2, 2>(dY, X, m, d, offsets, G, cols, piece, dW, 1, st);
         };
         return grad_dtype == dtype ? go(T()) : go(float());
     });
