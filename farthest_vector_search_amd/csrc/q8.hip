@@ -24,7 +24,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_q8_scores(
     using C = tile::Core<int8_t, BM, BN, WM, WN, false, false, PIECE>;
     __shared__ __attribute__((aligned(1024))) char bufs[2 * C::kBytes];
     const int64_t qt = (nq + BM - 1) / BM, it = (nc + BN - 1) / BN;
-    tile::run_tiles<C, int8_t, O>(
+    tile::run_tiles<int8_t, O, C>(
         qt * it, bufs,
         [&](int64_t at, tile::Job<int8_t, O> &j) {
             const tile::Place pl = tile::place(at, qt, it);

@@ -309,6 +309,7 @@ struct Core {
     static constexpr int kSide = BM * kStep;                    // where the N side begins
     static constexpr int kBytes = (BM + BN) * kStep;            // of a buffer
     static constexpr int K = kStep / (int)sizeof(T);
+    static constexpr int kRows = BM;
     typedef typename Sum<T>::type Acc;
     typedef Mover<T, BM, kWaves, M_ACROSS, PIECE> MMover;
     typedef Mover<T, BN, kWaves, N_ACROSS, PIECE> NMover;
@@ -572,23 +573,29 @@ struct Job {
 // they stored this one's results, and so saved its start, were no faster (65,536 x
 // 2,048 rows into 128 units of 2,048 columns, bf16, 557 us so, 589 us then), since
 // all of them store at the same time and the loads behind wait for the stores.
-template <typename C, typename T, typename O, typename FJ>
+// A tile of few rows is taken by the first of the lower cores `Low` that holds them.
+template <typename T, typename O, typename C, typename... Low, typename FJ>
 __device__ __forceinline__ void run_tiles(int64_t total, char *bufs, FJ job) {
     for (int64_t id = blockIdx.x; id < (total + 7) / 8 * 8; id += gridDim.x) {
         const int64_t at = xcd_order(id, total);
         Job<T, O> j;
         if (at >= total || !job(at, j)) continue;
-        C core;
         lds_barrier();  // the last tile's results have left the buffers
-        core.begin(j.m, j.n, j.depth, bufs);
-        core.sum(bufs);
-        lds_barrier();  // no wave reads the buffers any more
-        if constexpr (std::is_same<T, int8_t>::value) {
-            core.put_scaled(bufs, j.out, j.ld, j.m.rows, j.n.rows, j.mscale, j.nscale);
-        } else {
-            core.put(bufs, j.out, j.ld, j.m.rows, j.n.rows,
-                     [](int, int, const f32x4 &v) { return v; });
-        }
+        auto work = [&](auto core) {
+            core.begin(j.m, j.n, j.depth, bufs);
+            core.sum(bufs);
+            lds_barrier();  // no wave reads the buffers any more
+            if constexpr (std::is_same<T, int8_t>::value) {
+                core.put_scaled(bufs, j.out, j.ld, j.m.rows, j.n.rows, j.mscale, j.nscale);
+            } else {
+                core.put(bufs, j.out, j.ld, j.m.rows, j.n.rows,
+                         [](int, int, const f32x4 &v) { return v; });
+            }
+            return true;
+        };
+        const int rows = uniform(j.m.rows);
+        if ((... || (rows <= Low::kRows && work(Low())))) continue;
+        work(C());
     }
 }
 

@@ -71,8 +71,7 @@ inline int64_t slots_of(int64_t m, int64_t G, int rows) { return m / rows + G + 
 // out[p][j] = sum_k A[p][k] B(g)(j, k): B = W[g][j][k], or W[g][k][j] (ACROSS).  Bound
 // by the matrix cores where units have many rows (8,192 rows to one unit of 8,192 x 8,192
 // bf16: 979 us, 1,123 TFLOP/s, across 891 us, 1,235 TFLOP/s), with 65,536 rows to 128 of
-// 2,048 x 2,048 547 us (1,005 TFLOP/s: a unit's last tile is half empty on average); fp32
-// 1,012 us for 16,384 to 16 of 2,048 x 2,048 (136 TFLOP/s).  By reading W where they have
+// 2,048 x 2,048 at random 609 us (902 TFLOP/s: units' last tiles); fp32 1,012 us for 16,384 to 16 of 2,048 x 2,048 (136 TFLOP/s).  By reading W where they have
 // few: 1,024 rows to 64 of 1,024 x 1,024 30 us (4.6 TB/s).
 template <typename T, int BM, int BN, int WM, int WN, bool ACROSS, int PIECE>
 __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_rows(
@@ -82,9 +81,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_rows(
     using C = tile::Core<T, BM, BN, WM, WN, false, ACROSS, PIECE>;
     __shared__ __attribute__((aligned(1024))) char bufs[2 * C::kBytes];
     const int64_t ctiles = (cols + BN - 1) / BN;
-    tile::run_tiles<C, T, T>(
-        slots * ctiles, bufs,
-        [&](int64_t at, tile::Job<T, T> &j) {
+    auto job = [&](int64_t at, tile::Job<T, T> &j) {
             const tile::Place pl = tile::place(at, slots, ctiles);
             const RowTile rt = row_tile(offsets, G, m, BM, pl.row);
             if (rt.lo >= rt.hi) return false;
@@ -97,7 +94,15 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_rows(
             j.out = out + rt.lo * cols + j0;
             j.ld = cols;
             return true;
-        });
+        };
+    // A unit's last tile is half empty on average: with tiles of 256 rows it is taken as
+    // one of 64 or 128 where that is enough.  65,536 rows to 128 units of 2,048 x 2,048,
+    // skewed: 609 us, with 128 alone 617, without 641.  (Tiles of 128 as 64: no gain.)
+    if constexpr (BM == 256)
+        tile::run_tiles<T, T, C, tile::Core<T, 64, BN, 1, 8, false, ACROSS, PIECE>,
+                        tile::Core<T, 128, BN, 2, 4, false, ACROSS, PIECE>>(slots * ctiles, bufs, job);
+    else
+        tile::run_tiles<T, T, C>(slots * ctiles, bufs, job);
 }
 
 // The same along k for units of few rows: 16 rows a tile, `groups` workgroups for each.
@@ -133,7 +138,7 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_mats(
     using C = tile::Core<T, BM, BN, WM, WN, true, true, PIECE>;
     __shared__ __attribute__((aligned(1024))) char bufs[2 * C::kBytes];
     const int64_t jt = (cols + BM - 1) / BM, kt = (d + BN - 1) / BN;
-    tile::run_tiles<C, T, O>(
+    tile::run_tiles<T, O, C>(
         G * parts * jt * kt, bufs,
         [&](int64_t at, tile::Job<T, O> &j) {
             const int64_t run = at / (jt * kt), g = run / parts, part = run - g * parts;
@@ -262,12 +267,12 @@ hipError_t unit_mats(const void *dY, const void *X, int64_t m, int32_t d, const 
 //              have odd addresses (16 rows to 8 units of 2,048 x 2,048: 14, 64 x 64 19;
 //              100 to 100 of 333 x 250 f32: 12, 64 x 64 22; 32 to 64 of 2,048 x
 //              1,024: 64 x 128 25, few 27)
-//   256 x 256  r >= 512 and a tile for every CU (65,536 rows to 128 of 2,048 x 2,048:
-//              556, 128 x 128 628; r = 384, 64 of 1,024 x 1,024: 97, 128 x 128 86: the
-//              units' last tiles are half empty); 16-byte addresses only (through
-//              registers, 20,000 rows to 60 of 1,027 x 1,027: 141, 128 x 128 117)
+//   256 x 256  r >= 200 and a tile for every CU (65,536 rows to 300 of 2,048 x 2,048,
+//              r = 218: 713, 128 x 128 820; r = 192, 64 of 2,048 x 1,024: 130 and 122);
+//              16-byte addresses only (through registers, 20,000 rows to 60 of 1,027
+//              x 1,027: 141, 128 x 128 117)
 //   128 x 128  r >= 96 and two for every CU (r = 128 of the 64: 47, 64 x 128 46;
-//              r = 256: 66 and 74)
+//              64 of 2,048 x 1,024, r = 192: 122, 256 x 256 130)
 //   64 x 128   fewer rows (r = 32 of the 64: 32, 64 x 64 38, 128 x 128 43); 64 x 64
 //              at odd addresses (2,501 rows to 60 of 257 x 515 f16: 14, 64 x 128 19)
 //              and where tiles are few
@@ -287,7 +292,7 @@ hipError_t launch_unit_rows(const void *A, int64_t m, int32_t K, int dtype, cons
         if (!across && r <= 16 && (!aligned || units * tiles_of(cols, 128) < 2 * (int64_t)n_cu))
             return unit_rows_few<T>(A, m, K, W, offsets, G, cols, out, st, n_cu);
         if constexpr (ES == 2) {
-            if (aligned && r >= 512 && tiles(256, 256) >= n_cu && !wasteful(cols))
+            if (aligned && r >= 200 && tiles(256, 256) >= n_cu && !wasteful(cols))
                 return unit_rows<T, 256, 256, 2, 4>(A, m, K, W, offsets, G, cols, across, piece,
                                                     out, st);
             if (r >= 96 && tiles(128, 128) >= 2 * (int64_t)n_cu)
