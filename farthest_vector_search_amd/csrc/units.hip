@@ -71,8 +71,9 @@ inline int64_t slots_of(int64_t m, int64_t G, int rows) { return m / rows + G + 
 // out[p][j] = sum_k A[p][k] B(g)(j, k): B = W[g][j][k], or W[g][k][j] (ACROSS).  Bound
 // by the matrix cores where units have many rows (8,192 rows to one unit of 8,192 x 8,192
 // bf16: 979 us, 1,123 TFLOP/s, across 891 us, 1,235 TFLOP/s), with 65,536 rows to 128 of
-// 2,048 x 2,048 at random 609 us (902 TFLOP/s: units' last tiles); fp32 1,012 us for 16,384 to 16 of 2,048 x 2,048 (136 TFLOP/s).  By reading W where they have
-// few: 1,024 rows to 64 of 1,024 x 1,024 30 us (4.6 TB/s).
+// 2,048 x 2,048 at random 609 us (902 TFLOP/s: units' last tiles); fp32 1,012 us for
+// 16,384 to 16 of 2,048 x 2,048 (136 TFLOP/s).  By reading W where they have few: 1,024
+// rows to 64 of 1,024 x 1,024 30 us (4.6 TB/s).
 template <typename T, int BM, int BN, int WM, int WN, bool ACROSS, int PIECE>
 __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_rows(
     const T *__restrict__ A, int64_t m, int32_t K, const T *__restrict__ W,
@@ -82,22 +83,22 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_rows(
     __shared__ __attribute__((aligned(1024))) char bufs[2 * C::kBytes];
     const int64_t ctiles = (cols + BN - 1) / BN;
     auto job = [&](int64_t at, tile::Job<T, T> &j) {
-            const tile::Place pl = tile::place(at, slots, ctiles);
-            const RowTile rt = row_tile(offsets, G, m, BM, pl.row);
-            if (rt.lo >= rt.hi) return false;
-            const int64_t j0 = pl.col * BN;
-            const T *w = W + rt.unit * (int64_t)K * cols;
-            const int jn = (int)(cols - j0 < BN ? cols - j0 : BN);
-            j.depth = rt.none ? 0 : K;
-            j.m = {A + rt.lo * K, K, (int)(rt.hi - rt.lo)};
-            j.n = {ACROSS ? w + j0 : w + j0 * K, ACROSS ? cols : K, jn};
-            j.out = out + rt.lo * cols + j0;
-            j.ld = cols;
-            return true;
-        };
+        const tile::Place pl = tile::place(at, slots, ctiles);
+        const RowTile rt = row_tile(offsets, G, m, BM, pl.row);
+        if (rt.lo >= rt.hi) return false;
+        const int64_t j0 = pl.col * BN;
+        const T *w = W + rt.unit * (int64_t)K * cols;
+        const int jn = (int)(cols - j0 < BN ? cols - j0 : BN);
+        j.depth = rt.none ? 0 : K;
+        j.m = {A + rt.lo * K, K, (int)(rt.hi - rt.lo)};
+        j.n = {ACROSS ? w + j0 : w + j0 * K, ACROSS ? cols : K, jn};
+        j.out = out + rt.lo * cols + j0;
+        j.ld = cols;
+        return true;
+    };
     // A unit's last tile is half empty on average: with tiles of 256 rows it is taken as
-    // one of 64 or 128 where that is enough.  65,536 rows to 128 units of 2,048 x 2,048,
-    // skewed: 609 us, with 128 alone 617, without 641.  (Tiles of 128 as 64: no gain.)
+    // one of 64 or 128 where that is enough.  65,536 rows to 128 units of 2,048 x 2,048 at
+    // random: 609 us, with 128 alone 617, without 641.  (Tiles of 128 as 64: no gain.)
     if constexpr (BM == 256)
         tile::run_tiles<T, T, C, tile::Core<T, 64, BN, 1, 8, false, ACROSS, PIECE>,
                         tile::Core<T, 128, BN, 2, 4, false, ACROSS, PIECE>>(slots * ctiles, bufs, job);

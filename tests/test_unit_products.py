@@ -126,6 +126,45 @@ def test_whole_numbers_are_exact(m, G, d, cols, t):
 
 
 @pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("m,G,d,cols", [(300, 5, 66, 130), (700, 2, 258, 514), (900, 4, 30, 6),
+                                        (2000, 3, 10, 700), (70, 9, 1030, 36), (5000, 20, 390, 262)])
+def test_rows_on_four_bytes(m, G, d, cols, t):
+    """Even widths that no multiple of 8 divides: rows of 16 bits on 4-byte addresses,
+    and the same a half-word off them."""
+    check_all(rng(54, m, d), m, G, d, cols, "skew", t)
+    r = rng(55, m, d)
+    off = i32(make_offsets(r, m, G, "skew"))
+    X, W = rows(r, (m, d), t)[0], rows(r, (G, cols, d), t)[0]
+    want = vs.vs_unit_products(X, W, off)
+    for s in (1, 2):
+        at = torch.empty(X.numel() + 8, dtype=t, device=dev())[s:s + X.numel()].view(X.shape)
+        close(vs.vs_unit_products(at.copy_(X), W, off), host(want),
+              2 * bound(d, host(X.float().abs()) @ np.ones((d, cols)) * float(W.abs().max()),
+                        host(want), t))
+
+
+@pytest.mark.parametrize("t", [torch.float16, torch.bfloat16])
+def test_last_tiles_of_every_height(t):
+    """Units of some hundred rows, whose last tiles have few rows, many, or all."""
+    r = rng(56)
+    G, d, cols = 120, 512, 1024
+    count = 256 * r.integers(0, 3, G) + np.resize(
+        [0, 1, 15, 63, 64, 65, 100, 127, 128, 129, 192, 255], G)
+    off = np.concatenate([[0], np.cumsum(count)]).astype(np.int32)
+    m = int(off[-1])
+    assert m // G >= 200
+    (X, X64), (W, W64), (dY, dY64) = (whole(r, s, t, 1) for s in ((m, d), (G, cols, d), (m, cols)))
+    Y = vs.vs_unit_products(X, W, i32(off))
+    dX, _ = vs.vs_unit_products_backward(dY, X, W, i32(off), want_dW=False)
+    for g in range(G):
+        a, b = off[g], off[g + 1]
+        w = W64[g].astype(np.float32)  # sums below 2^24: exact
+        for got, want in ((Y, X64[a:b].astype(np.float32) @ w.T),
+                          (dX, dY64[a:b].astype(np.float32) @ w)):
+            assert torch.equal(got[a:b].cpu(), torch.from_numpy(want).to(t))
+
+
+@pytest.mark.parametrize("t", TYPES)
 def test_differences(t):
     """The loss sum(R * Y) is linear in X and in W, and exact for small whole
     numbers: moving one element by 1 moves it by that element's gradient."""
