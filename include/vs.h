@@ -6,8 +6,9 @@
  * similar by cosine on unit-norm rows -- optionally skipping candidates a
  * per-query bit mask excludes, with the lowest candidate index winning ties.
  * The table operators (vs_group_rows and below) take the indices and the
- * table further: rows by index and by unit, their gradients, and scores over
- * a table held in 4 bits.
+ * table further: rows by index and by unit, products of units' rows, the
+ * rows' norm, the gradients of these, and scores over a table held in 4 or 8
+ * bits.
  *
  * Sources (web pages, cited by title and section):
  *  [BMU] "From 80x to 385x: A Best-Matching-Unit Search at the L2 Roof,
