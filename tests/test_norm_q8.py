@@ -314,6 +314,48 @@ def test_in_place(d, t):
         assert torch.equal(a[which], dX) and torch.equal(gw, dw)
 
 
+@pytest.mark.parametrize("n,d", [(3, 40003), (1030, 9001), (1030, 17000)])
+def test_wide_in_place(n, d):
+    """The same for rows that are read twice."""
+    r = rng(73, n)
+    x, _, res, _, w, _ = inputs(r, n, d, torch.bfloat16, True)
+    dY = rows(r, (n, d), torch.bfloat16)[0]
+    Y, H, rs = vs.vs_norm_rows(x, w, residual=res)
+    codes, scales, _ = vs.vs_norm_rows_q8(x, w, residual=res)
+    dX, dw = vs.vs_norm_rows_backward(dY, H, w, rs, dH=x)
+    for which in (0, 1):
+        a, b = x.clone(), res.clone()
+        assert torch.equal(vs.vs_norm_rows(a, w, residual=b, H=(a, b)[which])[0], Y)
+        assert torch.equal((a, b)[which], H)
+        a, b = x.clone(), res.clone()
+        c, s, _ = vs.vs_norm_rows_q8(a, w, residual=b, H=(a, b)[which])
+        assert torch.equal(c, codes) and torch.equal(s, scales) and torch.equal((a, b)[which], H)
+    a = H.clone()
+    assert torch.equal(vs.vs_norm_rows(a, w, out=a)[0], Y)
+    for which in (0, 1, 2):
+        a = [dY.clone(), H.clone(), x.clone()]
+        g, gw = vs.vs_norm_rows_backward(a[0], a[1], w, rs, dH=a[2], out=a[which])
+        assert torch.equal(g, dX) and torch.equal(gw, dw)
+
+
+@pytest.mark.parametrize("d", [64, 8000])
+def test_largest_magnitudes(d):
+    """fp32 rows up to the largest number: rstd and the scale as in 64 bits, one
+    rounding to a subnormal rstd more."""
+    x = torch.from_numpy(rng(74, d).uniform(-1, 1, (3, d)) * 3.4e38).float().to(dev())
+    x64 = host(x)
+    h, rstd, y = norm_ref(x64, None, np.ones(d), 0.0, torch.float32)
+    Y, _, rs = vs.vs_norm_rows(x, None, 0.0)
+    sub = 2.0 ** -150 / rstd  # of a subnormal rstd, relative
+    close(rs, rstd[:, 0], 1.01 * ((r_of(d) + 8 * V + sub) * rstd)[:, 0])
+    close(Y, y, 1.01 * (r_of(d) + 10 * V + sub) * np.abs(y))
+    codes, scales, _ = vs.vs_norm_rows_q8(x, None, 0.0)
+    c, top = codes_ref(h, np.ones(d))
+    assert np.array_equal(host(codes), c)
+    scale = top * rstd / 127
+    close(scales, scale[:, 0], 1.01 * ((r_of(d) + 10 * V + sub) * scale)[:, 0])
+
+
 @pytest.mark.parametrize("t", TYPES)
 def test_outputs_and_addresses(t):
     """Odd addresses; nothing beside the outputs is written."""
@@ -422,6 +464,24 @@ def test_q8_scores(nq, nc, d, out):
     want = (xc @ tc.T).astype(np.float64) * xs64[:, None] * ts64
     tol = 1.01 * (3 * V + U(out)) * np.abs(want) + SUB[out]
     close(vs.vs_q8_scores(x, xs, t, ts, out_dtype=out), want, tol)
+
+
+@pytest.mark.parametrize("shift", [0, 4, 2])
+@pytest.mark.parametrize("nq,nc,d", [(37, 209, 764), (130, 515, 100), (300, 700, 268), (6, 33, 4),
+                                     (300, 17000, 132)])
+def test_q8_scores_on_four_bytes(nq, nc, d, shift):
+    """Widths that 4 divides and 16 does not, on addresses of 4 bytes and of 2."""
+    r = rng(75, nq, d)
+    (x, xc), (t, tc) = codes8(r, (nq, d)), codes8(r, (nc, d))
+    (xs, xs64), (ts, ts64) = scales8(r, nq), scales8(r, nc)
+
+    def at(a):
+        return torch.empty(a.numel() + 8, dtype=a.dtype, device=dev())[shift:shift + a.numel()].view(
+            a.shape).copy_(a)
+
+    want = (xc @ tc.T).astype(np.float64) * xs64[:, None] * ts64
+    close(vs.vs_q8_scores(at(x), xs, at(t), ts), want,
+          1.01 * (3 * V + U(torch.float32)) * np.abs(want) + SUB[torch.float32])
 
 
 @pytest.mark.parametrize("nq,d", [(1, 131071), (40, 131071), (200, 131056), (3, 100000)])
