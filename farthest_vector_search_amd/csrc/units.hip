@@ -313,9 +313,12 @@ hipError_t launch_unit_rows(const void *A, int64_t m, int32_t K, int dtype, cons
 static int64_t mats_tiles(int64_t G, int32_t cols, int32_t d, int b) {
     return G * tiles_of(cols, b) * tiles_of(d, b);
 }
+// tiles of 128 x 128 pad a matrix by a fifth more than those of 64 x 64 at most
+static bool mats_filled(int64_t G, int32_t cols, int32_t d) {
+    return mats_tiles(G, cols, d, 128) * 4 * 5 <= mats_tiles(G, cols, d, 64) * 6;
+}
 static bool mats_large(int64_t G, int32_t cols, int32_t d) {
-    const int64_t large = mats_tiles(G, cols, d, 128), small = mats_tiles(G, cols, d, 64);
-    return large >= 64 && large * 4 * 5 <= small * 6;
+    return mats_tiles(G, cols, d, 128) >= 64 && mats_filled(G, cols, d);
 }
 static int mats_parts(int64_t m, int64_t G, int32_t cols, int32_t d) {
     const int64_t tiles = mats_tiles(G, cols, d, mats_large(G, cols, d) ? 128 : 64);
@@ -332,9 +335,11 @@ size_t unit_mats_workspace(int64_t m, int64_t G, int32_t cols, int32_t d) {
 // The same for the matrices' gradient, by the number of tiles: 256 x 256 if there are
 // two for every CU (4,096 rows of 64 units of 1,024 x 1,024, 1,024 tiles: 37, as 128
 // x 128; 65,536 of 128 of 2,048 x 2,048: 665, 128 x 128 784), 128 x 128 if there is
-// one (the 64 units with 64 rows: 34, 64 x 64 48).  Where tiles are few and units have
-// many rows, the rows are cut into runs, which a second kernel joins (65,536 rows to 4
-// units of 64 x 64: 19, in one run 111; of 512 x 512: 62 and 179).
+// one and it pads little (20,000 rows to 60 of 1,027 x 1,027 f16: 151, 64 x 64 200; 9,000
+// to 100 of 260 x 130: 16.5, so 64 x 64 11.9; of 384 x 384: 15.4, 64 x 64 18.8).  Where
+// tiles are few and units have many rows, the rows are cut into runs, which a second
+// kernel joins (65,536 rows to 4 units of 64 x 64: 19, in one run 111; of 512 x 512: 62
+// and 179).
 hipError_t launch_unit_mats(const void *dY, const void *X, int64_t m, int32_t d, int dtype,
                             const int32_t *offsets, int64_t G, int32_t cols, int grad_dtype,
                             void *dW, void *ws, hipStream_t st, int n_cu) {
@@ -367,7 +372,7 @@ hipError_t launch_unit_mats(const void *dY, const void *X, int64_t m, int32_t d,
                 if (piece == 16 && tiles(256) >= 2 * (int64_t)n_cu && !wasteful(cols) && !wasteful(d))
                     return unit_mats<T, O, 256, 256, 2, 4>(dY, X, m, d, offsets, G, cols, piece,
                                                            dW, 1, st);
-                if (tiles(128) >= n_cu)
+                if (tiles(128) >= n_cu && mats_filled(G, cols, d))
                     return unit_mats<T, O, 128, 128, 2, 2>(dY, X, m, d, offsets, G, cols, piece,
                                                            dW, 1, st);
             }
