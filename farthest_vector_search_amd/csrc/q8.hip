@@ -26,7 +26,9 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_q8_scores(
     const int64_t qt = (nq + BM - 1) / BM, it = (nc + BN - 1) / BN;
     tile::run_tiles<int8_t, O, C>(
         qt * it, bufs,
-        [&](int64_t at, tile::Job<int8_t, O> &j) {
+        [&](int64_t id, tile::Job<int8_t, O> &j) {
+            const int64_t at = tile::xcd_order(id, qt * it);
+            if (at >= qt * it) return false;
             const tile::Place pl = tile::place(at, qt, it);
             const int64_t q0 = pl.row * BM, i0 = pl.col * BN;
             j.depth = d;

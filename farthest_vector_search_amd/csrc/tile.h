@@ -567,8 +567,8 @@ struct Job {
     const float *mscale, *nscale;  // int8: the rows' scales of either side
 };
 
-// A workgroup's tiles.  job(at, j) says what tile `at` of `total` is, or that there is
-// nothing to do.  As a rule a workgroup
+// A workgroup's tiles.  job(id, j) says what tile `id` of `total` is (numbered as
+// workgroups are, see xcd_order), or that there is nothing to do.  As a rule a workgroup
 // has one tile: workgroups that stayed, took the next tile's first loads up before
 // they stored this one's results, and so saved its start, were no faster (65,536 x
 // 2,048 rows into 128 units of 2,048 columns, bf16, 557 us so, 589 us then), since
@@ -577,9 +577,8 @@ struct Job {
 template <typename T, typename O, typename C, typename... Low, typename FJ>
 __device__ __forceinline__ void run_tiles(int64_t total, char *bufs, FJ job) {
     for (int64_t id = blockIdx.x; id < (total + 7) / 8 * 8; id += gridDim.x) {
-        const int64_t at = xcd_order(id, total);
         Job<T, O> j;
-        if (at >= total || !job(at, j)) continue;
+        if (!job(id, j)) continue;
         lds_barrier();  // the last tile's results have left the buffers
         auto work = [&](auto core) {
             core.begin(j.m, j.n, j.depth, bufs);

@@ -11,7 +11,8 @@
 // T(u + 1) - 1 with T(u) = begin(u) / B + u for tiles of B rows, which is never fewer
 // than its rows need, so that the grid follows from m and the number of units alone
 // (a run's spare tile ends at once).  T rises, and a wave finds its tile's run by
-// looking at 64 of them at a time.
+// looking at 64 of them at a time.  Up to some hundred runs are counted through
+// instead (counted_tile).
 #include <type_traits>
 
 #include "few.h"
@@ -68,12 +69,82 @@ __device__ __forceinline__ RowTile row_tile(const int32_t *__restrict__ offsets,
 // tiles of `rows` rows that cover m rows of G units
 inline int64_t slots_of(int64_t m, int64_t G, int rows) { return m / rows + G + 2; }
 
+// inclusive sums over the wave's lanes: within rows of 16, then across them
+__device__ __forceinline__ int scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // from 1 lane below
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);  // 2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);  // 4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);  // 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row 0's to 1, 2's to 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // the lower half's
+    return v;
+}
+
+// The same for up to kCounted units, in an order that keeps the XCDs even: the tiles of
+// the units are counted and dealt out in 8 equal stretches, one an XCD, and after them
+// those of no unit, which cost little, the same way.  By slots, empty ones fall to some
+// XCDs more than to others (bf16, us by slots and counted: 8,192 rows to one unit of
+// 8,192 x 8,192 913 and 790; 10,240 to 64 of 1,024 x 1,024 58 and 50; 32 to 64 of 2,048 x
+// 1,024 24.9 and 21.2).  Counting takes every lane more loads the more units there are:
+// 65,536 rows to 300 of 2,048 x 2,048 712 and 718; 60,000 to 1,000 of 512 x 512 132 and
+// 161.  Whole tiles first and units' last tiles behind them was slower (65,536 rows to
+// 128 of 2,048 x 2,048: 609, so 669), since W is then read twice.
+constexpr int64_t kCounted = 256;
+__device__ __forceinline__ bool counted_tile(const int32_t *__restrict__ offsets, int64_t G,
+                                             int64_t m, int rows, int64_t ctiles, int64_t id,
+                                             RowTile &t, int64_t &col) {
+    const int lane = threadIdx.x & 63;
+    const int per = (int)((G + 63) / 64);  // a lane's units
+    auto count = [&](int64_t g) {
+        if (g >= G) return 0;
+        const int64_t n = place_of(offsets, g + 1, m) - place_of(offsets, g, m);
+        return n > 0 ? ((int)n + rows - 1) / rows : 0;
+    };
+    int mine = 0;
+    for (int i = 0; i < per; ++i) mine += count((int64_t)lane * per + i);
+    int sum = scan(mine);
+    const int64_t begin = place_of(offsets, 0, m), end = place_of(offsets, G, m);
+    const int before_units = (int)((begin + rows - 1) / rows);
+    const int64_t all = __builtin_amdgcn_readlane(sum, 63);
+    const int64_t others = before_units + (m - end + rows - 1) / rows;
+    const int64_t turn = id >> 3, xcd = id & 7;
+    const int64_t first = (all * ctiles + 7) >> 3, then = (others * ctiles + 7) >> 3;
+    t.none = turn >= first;
+    const int64_t at = t.none ? xcd * then + turn - first : xcd * first + turn;
+    if (t.none ? turn - first >= then || at >= others * ctiles : at >= all * ctiles) return false;
+    const tile::Place pl = tile::place(at, t.none ? others : all, ctiles);
+    const int row = tile::uniform((int)pl.row);
+    col = pl.col;
+    int64_t e;
+    if (t.none) {
+        const bool front = row < before_units;
+        t.unit = 0;
+        t.lo = front ? (int64_t)row * rows : end + (int64_t)(row - before_units) * rows;
+        e = front ? begin : m;
+    } else {
+        int holder = __ffsll((unsigned long long)__ballot(sum > row)) - 1;
+        int before = __builtin_amdgcn_readlane(sum - mine, holder);
+        t.unit = (int64_t)holder * per;
+        if (per > 1) {  // which of the lane's units
+            mine = lane < per ? count(t.unit + lane) : 0;
+            sum = before + scan(mine);
+            holder = __ffsll((unsigned long long)__ballot(sum > row)) - 1;
+            before = __builtin_amdgcn_readlane(sum - mine, holder);
+            t.unit += holder;
+        }
+        t.lo = place_of(offsets, t.unit, m) + (int64_t)(row - before) * rows;
+        e = place_of(offsets, t.unit + 1, m);
+    }
+    t.hi = t.lo + rows < e ? t.lo + rows : e;
+    return true;
+}
+
 // out[p][j] = sum_k A[p][k] B(g)(j, k): B = W[g][j][k], or W[g][k][j] (ACROSS).  Bound
 // by the matrix cores where units have many rows (8,192 rows to one unit of 8,192 x 8,192
-// bf16: 979 us, 1,123 TFLOP/s, across 891 us, 1,235 TFLOP/s), with 65,536 rows to 128 of
-// 2,048 x 2,048 at random 609 us (902 TFLOP/s: units' last tiles); fp32 1,012 us for
+// bf16: 790 us, 1,392 TFLOP/s, across 780 us, 1,410 TFLOP/s), with 65,536 rows to 128 of
+// 2,048 x 2,048 at random 600 us (916 TFLOP/s: units' last tiles); fp32 1,012 us for
 // 16,384 to 16 of 2,048 x 2,048 (136 TFLOP/s).  By reading W where they have few: 1,024
-// rows to 64 of 1,024 x 1,024 30 us (4.6 TB/s).
+// rows to 64 of 1,024 x 1,024 28 us (4.9 TB/s).
 template <typename T, int BM, int BN, int WM, int WN, bool ACROSS, int PIECE>
 __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_rows(
     const T *__restrict__ A, int64_t m, int32_t K, const T *__restrict__ W,
@@ -82,11 +153,20 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_rows(
     using C = tile::Core<T, BM, BN, WM, WN, false, ACROSS, PIECE>;
     __shared__ __attribute__((aligned(1024))) char bufs[2 * C::kBytes];
     const int64_t ctiles = (cols + BN - 1) / BN;
-    auto job = [&](int64_t at, tile::Job<T, T> &j) {
-        const tile::Place pl = tile::place(at, slots, ctiles);
-        const RowTile rt = row_tile(offsets, G, m, BM, pl.row);
+    auto job = [&](int64_t id, tile::Job<T, T> &j) {
+        RowTile rt;
+        int64_t col;
+        if (G <= kCounted) {
+            if (!counted_tile(offsets, G, m, BM, ctiles, id, rt, col)) return false;
+        } else {
+            const int64_t at = tile::xcd_order(id, slots * ctiles);
+            if (at >= slots * ctiles) return false;
+            const tile::Place pl = tile::place(at, slots, ctiles);
+            rt = row_tile(offsets, G, m, BM, pl.row);
+            col = pl.col;
+        }
         if (rt.lo >= rt.hi) return false;
-        const int64_t j0 = pl.col * BN;
+        const int64_t j0 = col * BN;
         const T *w = W + rt.unit * (int64_t)K * cols;
         const int jn = (int)(cols - j0 < BN ? cols - j0 : BN);
         j.depth = rt.none ? 0 : K;
@@ -101,9 +181,9 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_rows(
     // random: 609 us, with 128 alone 617, without 641.  (Tiles of 128 as 64: no gain.)
     if constexpr (BM == 256)
         tile::run_tiles<T, T, C, tile::Core<T, 64, BN, 1, 8, false, ACROSS, PIECE>,
-                        tile::Core<T, 128, BN, 2, 4, false, ACROSS, PIECE>>(slots * ctiles, bufs, job);
+                        tile::Core<T, 128, BN, 2, 4, false, ACROSS, PIECE>>(slots * ctiles + 16, bufs, job);
     else
-        tile::run_tiles<T, T, C>(slots * ctiles, bufs, job);
+        tile::run_tiles<T, T, C>(slots * ctiles + 16, bufs, job);
 }
 
 // The same along k for units of few rows: 16 rows a tile, `groups` workgroups for each.
@@ -138,10 +218,12 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_mats(
     const int32_t *__restrict__ offsets, int64_t G, int32_t cols, O *__restrict__ dW, int parts) {
     using C = tile::Core<T, BM, BN, WM, WN, true, true, PIECE>;
     __shared__ __attribute__((aligned(1024))) char bufs[2 * C::kBytes];
-    const int64_t jt = (cols + BM - 1) / BM, kt = (d + BN - 1) / BN;
+    const int64_t jt = (cols + BM - 1) / BM, kt = (d + BN - 1) / BN, total = G * parts * jt * kt;
     tile::run_tiles<T, O, C>(
-        G * parts * jt * kt, bufs,
-        [&](int64_t at, tile::Job<T, O> &j) {
+        total, bufs,
+        [&](int64_t id, tile::Job<T, O> &j) {
+            const int64_t at = tile::xcd_order(id, total);
+            if (at >= total) return false;
             const int64_t run = at / (jt * kt), g = run / parts, part = run - g * parts;
             const tile::Place pl = tile::place(at - run * jt * kt, jt, kt);
             const int64_t j0 = pl.row * BM, k0 = pl.col * BN;
@@ -211,7 +293,8 @@ hipError_t unit_rows(const void *A, int64_t m, int32_t K, const void *W, const i
                      int64_t G, int32_t cols, bool across, int piece, void *out,
                      hipStream_t st) {
     const int64_t slots = slots_of(m, G, BM);
-    const dim3 grid(tile::grid_of(slots * tiles_of(cols, BN))), block(WM * WN * 64);
+    // 16 more: each of the 8 stretches of either kind is rounded up
+    const dim3 grid(tile::grid_of(slots * tiles_of(cols, BN) + 16)), block(WM * WN * 64);
     auto go = [&](auto ac, auto pc) {
         hipLaunchKernelGGL((k_unit_rows<T, BM, BN, WM, WN, decltype(ac)::value, decltype(pc)::value>),
                            grid, block, 0, st, (const T *)A, m, K, (const T *)W, offsets, G, cols,

@@ -165,6 +165,25 @@ def test_last_tiles_of_every_height(t):
 
 
 @pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("G", [1, 2, 63, 64, 65, 129, 200, 255, 256, 257, 400])
+def test_every_row_is_taken_once(G, t):
+    """Few and many units, some empty, with rows before the first and behind the last:
+    each row is its unit's alone."""
+    r = rng(57, G)
+    d, cols = 24, 200
+    count = r.integers(0, 150, G) * (r.random(G) < 0.8)
+    count[r.integers(0, G)] += 70
+    off = (37 + np.concatenate([[0], np.cumsum(count)])).astype(np.int32)
+    m = int(off[-1]) + 333
+    (X, X64), (W, W64), (dY, dY64) = (whole(r, s, t, 1) for s in ((m, d), (G, cols, d), (m, cols)))
+    (Y, dX, _), _ = reference(X64, W64, off, dY64)
+    X[:37], X[off[-1]:], dY[:37], dY[off[-1]:] = (float("nan"),) * 4
+    assert np.array_equal(host(vs.vs_unit_products(X, W, i32(off))), Y)
+    gX, _ = vs.vs_unit_products_backward(dY, X, W, i32(off), want_dW=False)
+    assert np.array_equal(host(gX), host(torch.from_numpy(dX).to(t)))
+
+
+@pytest.mark.parametrize("t", TYPES)
 def test_differences(t):
     """The loss sum(R * Y) is linear in X and in W, and exact for small whole
     numbers: moving one element by 1 moves it by that element's gradient."""
