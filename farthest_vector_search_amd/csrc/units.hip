@@ -347,10 +347,10 @@ hipError_t unit_mats(const void *dY, const void *X, int64_t m, int32_t d, const 
 
 // Which tile, from the rows a unit has on average (r) and the number of tiles; in
 // brackets us of the tile taken and of its neighbour, bf16 unless said.
-//   few.h      r <= 16, and tiles of 64 x 128 would not fill the GPU twice or rows
-//              have odd addresses (16 rows to 8 units of 2,048 x 2,048: 14, 64 x 64 19;
+//   few.h      r <= 16, and tiles of 64 x 128 would not fill the GPU twice or rows are
+//              not on 16-byte addresses (16 rows to 8 units of 2,048 x 2,048: 14, 64 x 64 19;
 //              100 to 100 of 333 x 250 f32: 12, 64 x 64 22; 32 to 64 of 2,048 x
-//              1,024: 64 x 128 25, few 27)
+//              1,024: 64 x 128 21, few 27)
 //   256 x 256  r >= 200 and a tile for every CU (65,536 rows to 300 of 2,048 x 2,048,
 //              r = 218: 713, 128 x 128 820; r = 192, 64 of 2,048 x 1,024: 130 and 122);
 //              16-byte addresses only (through registers, 20,000 rows to 60 of 1,027
@@ -358,7 +358,7 @@ hipError_t unit_mats(const void *dY, const void *X, int64_t m, int32_t d, const 
 //   128 x 128  r >= 96 and two for every CU (r = 128 of the 64: 47, 64 x 128 46;
 //              64 of 2,048 x 1,024, r = 192: 122, 256 x 256 130)
 //   64 x 128   fewer rows (r = 32 of the 64: 32, 64 x 64 38, 128 x 128 43); 64 x 64
-//              at odd addresses (2,501 rows to 60 of 257 x 515 f16: 14, 64 x 128 19)
+//              at other addresses (2,501 rows to 60 of 257 x 515 f16: 14, 64 x 128 19)
 //              and where tiles are few
 // fp32 has 64 x 64 only: bound by its matrix instructions, larger ones gain nothing
 // (16,384 rows to 16 of 2,048 x 2,048: 1,015, 128 x 128 1,043).
