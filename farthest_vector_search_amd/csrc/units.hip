@@ -98,7 +98,7 @@ __device__ __forceinline__ bool counted_tile(const int32_t *__restrict__ offsets
     auto count = [&](int64_t g) {
         if (g >= G) return 0;
         const int64_t n = place_of(offsets, g + 1, m) - place_of(offsets, g, m);
-        return n > 0 ? ((int)n + rows - 1) / rows : 0;
+        return n > 0 ? (int)(((uint32_t)n + rows - 1) / rows) : 0;
     };
     int mine = 0;
     for (int i = 0; i < per; ++i) mine += count((int64_t)lane * per + i);
@@ -132,6 +132,7 @@ __device__ __forceinline__ bool counted_tile(const int32_t *__restrict__ offsets
             before = __builtin_amdgcn_readlane(sum - mine, holder);
             t.unit += holder;
         }
+        if (holder < 0 || row < before) return false;  // places that fall, and sums past 31 bits
         t.lo = place_of(offsets, t.unit, m) + (int64_t)(row - before) * rows;
         e = place_of(offsets, t.unit + 1, m);
     }

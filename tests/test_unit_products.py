@@ -502,3 +502,33 @@ def test_matrices_past_32_bit_offsets():
     assert bool((Y[28:] == 0).all()) and bool((dX[28:] == 0).all())
     for g in (1, 300, 513, G - 2):
         assert bool((dW[g] == 0).all())
+
+
+def test_largest_number_of_rows():
+    """2^31 - 1 rows of one element: every row its unit's factor times itself."""
+    m = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[1] < 64 << 30:
+        pytest.skip("needs 64 GiB")
+    X = torch.ones((m, 1), dtype=torch.bfloat16, device=dev())
+    W = torch.tensor([2.0, 3.0, 5.0], dtype=torch.bfloat16, device=dev()).view(3, 1, 1)
+    for cuts in ((0, 0, 0, m), (0, 1, m - 1, m), (7, 2 ** 30 + 5, 2 ** 30 + 5, m - 9)):
+        off = i32(np.array(cuts))
+        for Y in (vs.vs_unit_products(X, W, off),
+                  vs.vs_unit_products_backward(X, X, W, off, want_dW=False)[0]):
+            ends = (0, *cuts, m)
+            for f, a, b in zip((0.0, 2.0, 3.0, 5.0, 0.0), ends, ends[1:]):
+                assert bool((Y[a:b] == f).all()), (cuts, f)
+            del Y
+
+
+@pytest.mark.parametrize("G", [2, 64, 130, 300])
+def test_places_that_fall(G):
+    """Offsets that go up and down: results are nobody's, but nothing beside the
+    output is written, and the call ends."""
+    m, d, cols = 700, 40, 72
+    r = rng(58, G)
+    X, W = rows(r, (m, d), torch.bfloat16)[0], rows(r, (G, cols, d), torch.bfloat16)[0]
+    buf = torch.full((m + 2, cols), 7.0, dtype=torch.bfloat16, device=dev())
+    for off in (np.arange(G + 1) % 2 * m, (np.arange(G + 1) + 1) % 2 * m, r.integers(-9, m + 9, G + 1)):
+        vs.vs_unit_products(X, W, i32(off.astype(np.int32)), out=buf[1:-1])
+        assert bool((buf[0] == 7).all()) and bool((buf[-1] == 7).all())
