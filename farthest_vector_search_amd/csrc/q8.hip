@@ -90,16 +90,17 @@ hipError_t q8_scores(const int8_t *x, const float *xs, int64_t nq, int32_t d, co
                      const float *ts, int64_t nc, int piece, O *y, hipStream_t st) {
     const dim3 grid(tile::grid_of(tiles_of(nq, BM) * tiles_of(nc, BN))), block(WM * WN * 64);
     auto go = [&](auto pc) {
+        static const tile::FormName name("k_q8_scores", BM, BN, decltype(pc)::value);
+        timing_before(st, name.text);
         hipLaunchKernelGGL((k_q8_scores<O, BM, BN, WM, WN, decltype(pc)::value>), grid, block, 0, st,
                            x, xs, nq, d, t, ts, nc, y);
+        timing_after(st);
     };
-    timing_before(st, "k_q8_scores");
     if constexpr (BM < 256) {  // the largest tile is for pieces of 16 only
         if (piece == 4) go(std::integral_constant<int, 4>());
         if (piece == 0) go(std::integral_constant<int, 0>());
     }
     if (piece == 16) go(std::integral_constant<int, 16>());
-    timing_after(st);
     return hipGetLastError();
 }
 

@@ -29,6 +29,8 @@
 // in as copies of rows that are there, and their results not stored.
 #pragma once
 
+#include <stdio.h>
+
 #include <type_traits>
 #include <utility>
 
@@ -597,6 +599,14 @@ __device__ __forceinline__ void run_tiles(int64_t total, char *bufs, FJ job) {
         work(C());
     }
 }
+
+// What the timing hook calls a kernel: its tile, the bytes that rows move in, and more
+struct FormName {
+    char text[48];
+    FormName(const char *kernel, int bm, int bn, int piece, const char *more = "") {
+        snprintf(text, sizeof(text), "%s<%dx%d,%d%s>", kernel, bm, bn, piece, more);
+    }
+};
 
 // Workgroups for `total` tiles, a multiple of 8.  The most keeps the number of threads
 // below 2^32, which a launch counts in 32 bits.

@@ -297,17 +297,19 @@ hipError_t unit_rows(const void *A, int64_t m, int32_t K, const void *W, const i
     // 16 more: each of the 8 stretches of either kind is rounded up
     const dim3 grid(tile::grid_of(slots * tiles_of(cols, BN) + 16)), block(WM * WN * 64);
     auto go = [&](auto ac, auto pc) {
+        static const tile::FormName name("k_unit_rows", BM, BN, decltype(pc)::value,
+                                         decltype(ac)::value ? ",across" : "");
+        timing_before(st, name.text);
         hipLaunchKernelGGL((k_unit_rows<T, BM, BN, WM, WN, decltype(ac)::value, decltype(pc)::value>),
                            grid, block, 0, st, (const T *)A, m, K, (const T *)W, offsets, G, cols,
                            (T *)out, slots);
+        timing_after(st);
     };
     auto way = [&](auto pc) {
         if (across) go(std::true_type(), pc);
         else go(std::false_type(), pc);
     };
-    timing_before(st, "k_unit_rows");
     by_piece<T, BM>(piece, way);
-    timing_after(st);
     return hipGetLastError();
 }
 
@@ -335,12 +337,13 @@ hipError_t unit_mats(const void *dY, const void *X, int64_t m, int32_t d, const 
     const dim3 grid(tile::grid_of(G * parts * tiles_of(cols, BM) * tiles_of(d, BN)));
     const dim3 block(WM * WN * 64);
     auto go = [&](auto pc) {
+        static const tile::FormName name("k_unit_mats", BM, BN, decltype(pc)::value);
+        timing_before(st, name.text);
         hipLaunchKernelGGL((k_unit_mats<T, O, BM, BN, WM, WN, decltype(pc)::value>), grid, block, 0,
                            st, (const T *)dY, (const T *)X, m, d, offsets, G, cols, (O *)dW, parts);
+        timing_after(st);
     };
-    timing_before(st, "k_unit_mats");
     by_piece<T, BM>(piece, go);
-    timing_after(st);
     return hipGetLastError();
 }
 

@@ -679,8 +679,10 @@ int64_t vs_tile_rows(int64_t cache_bytes, int32_t d, int32_t bytes_per_value);
  * the call's stream.  vs_timing_enable(max_launches) (re)starts recording
  * for up to max_launches launches (0 disables); vs_timing_read() waits for
  * the recorded events, returns the summed kernel time in milliseconds and the
- * number of launches, and stops recording.  Kernel names: see
- * vs_timing_kernel_name().
+ * number of launches, and stops recording.  vs_timing_kernel_name() names the
+ * last of them, the tiled products with their tile and the bytes that rows
+ * move in (k_unit_rows<128x128,16>, across W k_unit_rows<128x128,16,across>;
+ * 0: through registers).
  */
 int vs_timing_enable(int32_t max_launches);
 int vs_timing_read(double *total_ms, int64_t *launches);

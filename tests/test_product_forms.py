@@ -1,0 +1,150 @@
+"""Every form of the tiled products over several steps of k, on the GPU: the timing
+hook's name says which form a call took.  Inputs are small whole numbers, so that
+every sum is exact in fp32 (below 2^24) and equality is asked for: a step that is
+left out, taken twice or read from the other buffer, and a short first step, change
+the result.  The choices are those of a GPU of 256 CUs."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import farthest_vector_search_amd as vs  # noqa: E402
+from test_table_ops import dev, i32, rng  # noqa: E402
+
+HALF = [torch.float16, torch.bfloat16]
+
+
+def whole(r, shape, top):
+    """Whole numbers -top .. top as fp32 on the CPU."""
+    return torch.from_numpy(r.integers(-top, top + 1, shape).astype(np.float32))
+
+
+def places(r, G, lo, hi, empty):
+    """Places of G units of lo .. hi rows, `empty` of them without, and 9 rows of no unit
+    before and 70 behind."""
+    count = r.integers(lo, hi + 1, G)
+    count[r.choice(G, empty, replace=False)] = 0
+    off = 9 + np.concatenate([[0], np.cumsum(count)])
+    return off, int(off[-1]) + 70
+
+
+def named(call):
+    with vs.KernelTimer(8) as kt:
+        out = call()
+    assert kt.launches == 1
+    return out, kt.name
+
+
+def same(got, want, t):
+    got = got.cpu()
+    want = want.to(t)
+    assert torch.equal(got, want), int((got != want).sum())
+
+
+ROWS = [
+    # form, across's form, units, rows a unit (least, most, empty units), d, cols
+    ("256x256,16", "256x256,16", 64, 200, 300, 2, 1032, 1024),
+    ("256x256,16", "256x256,16", 300, 190, 260, 5, 520, 512),      # found by slots
+    ("128x128,16", "128x128,16", 64, 100, 180, 3, 1032, 1048),
+    ("128x128,16", "128x128,16", 300, 90, 130, 5, 264, 272),       # found by slots
+    ("128x128,4", "128x128,4", 64, 100, 180, 3, 1030, 1042),
+    ("128x128,0", "128x128,0", 64, 100, 180, 3, 1027, 1033),
+    ("64x128,16", "64x128,16", 64, 20, 64, 3, 1032, 1048),
+    ("64x128,16", "64x128,16", 400, 20, 64, 9, 520, 264),          # found by slots
+    ("64x64,16", "64x64,16", 5, 20, 300, 1, 1032, 264),
+    ("64x64,4", "64x64,4", 20, 20, 90, 1, 1030, 262),
+    ("64x64,0", "64x64,0", 20, 20, 90, 1, 1027, 261),
+    ("64x64,4", "64x64,4", 300, 20, 60, 5, 262, 70),               # found by slots
+    ("64x64,0", "64x64,0", 300, 20, 60, 5, 263, 71),               # found by slots
+]
+
+
+@pytest.mark.parametrize("form,across,G,lo,hi,empty,d,cols", ROWS)
+def test_rows(form, across, G, lo, hi, empty, d, cols):
+    r = rng(80, G, d, cols)
+    off, m = places(r, G, lo, hi, empty)
+    X, W, dY = whole(r, (m, d), 3), whole(r, (G, cols, d), 3), whole(r, (m, cols), 3)
+    Y, dX = torch.zeros(m, cols), torch.zeros(m, d)
+    for g in range(G):
+        s = slice(off[g], off[g + 1])
+        Y[s], dX[s] = X[s] @ W[g].T, dY[s] @ W[g]
+    for t in HALF:
+        x, w, dy, o = X.to(t).to(dev()), W.to(t).to(dev()), dY.to(t).to(dev()), i32(off)
+        got, name = named(lambda: vs.vs_unit_products(x, w, o))
+        assert name == f"k_unit_rows<{form}>"
+        same(got, Y, t)
+        (got, _), name = named(lambda: vs.vs_unit_products_backward(dy, x, w, o, want_dW=False))
+        assert name == f"k_unit_rows<{across},across>"
+        same(got, dX, t)
+
+
+@pytest.mark.parametrize("G,lo,hi,empty,d,cols,piece", [
+    (64, 20, 200, 3, 264, 328, 16), (64, 20, 200, 3, 257, 333, 4), (300, 20, 70, 3, 136, 132, 16),
+    (300, 20, 70, 3, 133, 135, 4)])
+def test_rows_in_full_precision(G, lo, hi, empty, d, cols, piece):
+    r = rng(81, G, d, cols)
+    off, m = places(r, G, lo, hi, empty)
+    X, W, dY = whole(r, (m, d), 9), whole(r, (G, cols, d), 9), whole(r, (m, cols), 9)
+    Y, dX = torch.zeros(m, cols), torch.zeros(m, d)
+    for g in range(G):
+        s = slice(off[g], off[g + 1])
+        Y[s], dX[s] = X[s] @ W[g].T, dY[s] @ W[g]
+    x, w, dy, o = X.to(dev()), W.to(dev()), dY.to(dev()), i32(off)
+    got, name = named(lambda: vs.vs_unit_products(x, w, o))
+    assert name == f"k_unit_rows<64x64,{piece}>"
+    same(got, Y, torch.float32)
+    (got, _), name = named(lambda: vs.vs_unit_products_backward(dy, x, w, o, want_dW=False))
+    assert name == f"k_unit_rows<64x64,{piece},across>"
+    same(got, dX, torch.float32)
+
+
+MATS = [
+    # form, units, rows a unit (least, most, empty units), d, cols, in runs
+    ("256x256,16", 64, 130, 300, 3, 1024, 1024, False),
+    ("128x128,16", 20, 130, 250, 2, 512, 520, False),
+    ("128x128,4", 20, 130, 250, 2, 510, 506, False),
+    ("128x128,0", 20, 130, 250, 2, 509, 507, False),
+    ("128x128,16", 4, 1000, 2100, 0, 512, 504, True),
+    ("128x128,4", 4, 1000, 2100, 0, 506, 510, True),
+    ("128x128,0", 4, 1000, 2100, 0, 507, 509, True),
+    ("64x64,16", 20, 130, 250, 2, 264, 72, False),
+    ("64x64,4", 20, 130, 250, 2, 262, 70, False),
+    ("64x64,0", 20, 130, 250, 2, 261, 71, False),
+]
+
+
+@pytest.mark.parametrize("form,G,lo,hi,empty,d,cols,runs", MATS)
+def test_matrices(form, G, lo, hi, empty, d, cols, runs):
+    r = rng(82, G, d, cols)
+    off, m = places(r, G, lo, hi, empty)
+    assert (vs.lib().vs_unit_products_backward_workspace(m, d, G, cols) > 0) == runs
+    X, dY = whole(r, (m, d), 3), whole(r, (m, cols), 3)
+    dW = torch.stack([dY[a:b].T @ X[a:b] for a, b in zip(off, off[1:])])
+    X[:9], X[off[-1]:], dY[:9], dY[off[-1]:] = (float("nan"),) * 4  # rows of no unit
+    for t in HALF:
+        x, dy, o = X.to(t).to(dev()), dY.to(t).to(dev()), i32(off)
+        w = torch.zeros(G, cols, d, dtype=t, device=dev())
+        for gt in (t, torch.float32):
+            (_, got), name = named(lambda: vs.vs_unit_products_backward(
+                dy, x, w, o, grad_dtype=gt, want_dXs=False))
+            assert name == f"k_unit_mats<{form}>"
+            same(got, dW, gt)
+
+
+SCORES = [
+    # form, queries, table rows, d
+    ("256x256,16", 300, 65500, 400), ("128x128,16", 130, 40000, 400), ("128x128,4", 130, 40000, 404),
+    ("128x128,0", 130, 40000, 403), ("64x64,16", 40, 5000, 912), ("64x64,4", 40, 5000, 908),
+    ("64x64,0", 40, 5000, 911),
+]
+
+
+@pytest.mark.parametrize("form,nq,nc,d", SCORES)
+def test_scores(form, nq, nc, d):
+    r = rng(83, nq, nc, d)
+    x, t = (torch.from_numpy(r.integers(-128, 128, s).astype(np.int8)) for s in ((nq, d), (nc, d)))
+    one = torch.ones(nc, device=dev())
+    got, name = named(lambda: vs.vs_q8_scores(x.to(dev()), one[:nq], t.to(dev()), one))
+    assert name == f"k_q8_scores<{form}>"
+    same(got, x.float() @ t.float().T, torch.float32)  # below 2^24
