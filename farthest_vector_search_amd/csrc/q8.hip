@@ -27,8 +27,8 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_q8_scores(
     tile::run_tiles<int8_t, O, C>(
         qt * it, bufs,
         [&](int64_t id, tile::Job<int8_t, O> &j) {
-            const int64_t at = tile::xcd_order(id, qt * it);
-            if (at >= qt * it) return false;
+            int64_t at;
+            if (!tile::xcd_tile(id, qt * it, at)) return false;
             const tile::Place pl = tile::place(at, qt, it);
             const int64_t q0 = pl.row * BM, i0 = pl.col * BN;
             j.depth = d;

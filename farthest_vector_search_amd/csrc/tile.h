@@ -551,10 +551,14 @@ struct Core {
 struct Place {
     int64_t row, col;
 };
-__device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t total) {
-    return (id & 7) * ((total + 7) >> 3) + (id >> 3);
+// The tile of workgroup `id`; false where it has none.  Each of the 8 has a stretch
+// of the tiles, and an id behind its XCD's stretch must not run into the next one.
+__host__ __device__ inline bool xcd_tile(int64_t id, int64_t total, int64_t &at) {
+    const int64_t stretch = (total + 7) >> 3, turn = id >> 3;
+    at = (id & 7) * stretch + turn;
+    return turn < stretch && at < total;
 }
-__device__ __forceinline__ Place place(int64_t tile, int64_t rows, int64_t cols) {
+__host__ __device__ inline Place place(int64_t tile, int64_t rows, int64_t cols) {
     const int64_t group = tile / (rows * 8), in = tile - group * rows * 8;
     const int64_t left = cols - group * 8, width = left < 8 ? left : 8;
     return Place{in / width, group * 8 + in % width};
@@ -570,7 +574,7 @@ struct Job {
 };
 
 // A workgroup's tiles.  job(id, j) says what tile `id` of `total` is (numbered as
-// workgroups are, see xcd_order), or that there is nothing to do.  As a rule a workgroup
+// workgroups are, see xcd_tile), or that there is nothing to do.  As a rule a workgroup
 // has one tile: workgroups that stayed, took the next tile's first loads up before
 // they stored this one's results, and so saved its start, were no faster (65,536 x
 // 2,048 rows into 128 units of 2,048 columns, bf16, 557 us so, 589 us then), since

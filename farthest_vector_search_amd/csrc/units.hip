@@ -86,8 +86,8 @@ __device__ __forceinline__ int scan(int v) {
 // XCDs more than to others (bf16, us by slots and counted: 8,192 rows to one unit of
 // 8,192 x 8,192 913 and 790; 10,240 to 64 of 1,024 x 1,024 58 and 50; 32 to 64 of 2,048 x
 // 1,024 24.9 and 21.2).  Counting takes every lane more loads the more units there are:
-// 65,536 rows to 300 of 2,048 x 2,048 712 and 718; 60,000 to 1,000 of 512 x 512 132 and
-// 161.  Whole tiles first and units' last tiles behind them was slower (65,536 rows to
+// 65,536 rows to 300 of 2,048 x 2,048 707 and 707; 60,000 to 300 of 512 x 512 71 and 74,
+// to 1,000 137 and 165; 2,500 to 2,500 of 512 x 256 94 and 199.  Whole tiles first and units' last tiles behind them was slower (65,536 rows to
 // 128 of 2,048 x 2,048: 609, so 669), since W is then read twice.
 constexpr int64_t kCounted = 256;
 __device__ __forceinline__ bool counted_tile(const int32_t *__restrict__ offsets, int64_t G,
@@ -160,8 +160,8 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_rows(
         if (G <= kCounted) {
             if (!counted_tile(offsets, G, m, BM, ctiles, id, rt, col)) return false;
         } else {
-            const int64_t at = tile::xcd_order(id, slots * ctiles);
-            if (at >= slots * ctiles) return false;
+            int64_t at;
+            if (!tile::xcd_tile(id, slots * ctiles, at)) return false;
             const tile::Place pl = tile::place(at, slots, ctiles);
             rt = row_tile(offsets, G, m, BM, pl.row);
             col = pl.col;
@@ -223,8 +223,8 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_mats(
     tile::run_tiles<T, O, C>(
         total, bufs,
         [&](int64_t id, tile::Job<T, O> &j) {
-            const int64_t at = tile::xcd_order(id, total);
-            if (at >= total) return false;
+            int64_t at;
+            if (!tile::xcd_tile(id, total, at)) return false;
             const int64_t run = at / (jt * kt), g = run / parts, part = run - g * parts;
             const tile::Place pl = tile::place(at - run * jt * kt, jt, kt);
             const int64_t j0 = pl.row * BM, k0 = pl.col * BN;
