@@ -149,8 +149,8 @@ __device__ __forceinline__ void store4(O *row, int64_t c, int64_t cols, const f3
 // How `blocks` blocks of 16 rows of `bytes` each, taken `times` times, are dealt out: nb
 // of them a wave, `share` waves a block, so that there are 16 waves a CU if they can be
 // had; a wave's part of k is not cut below 128 bytes.  Half and twice the waves, 16 of
-// 65,536 rows of 4,096 bytes for 1 query: 66 and 53 us, so 51; 32 rows of 2,048 bytes
-// for 64 units of 2,048 columns 40 and 28, so 28.
+// 65,536 rows of 4,096 bytes for 1 query: 86 and 53 us, so 51; 128 rows to 16 units of
+// 2,048 x 2,048 bf16 48 and 32, so 30.
 struct Deal {
     int nb, share;
     int64_t groups;  // workgroups

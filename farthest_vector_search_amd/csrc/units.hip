@@ -188,7 +188,8 @@ __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_rows(
 }
 
 // The same along k for units of few rows: 16 rows a tile, `groups` workgroups for each.
-// Bound by reading W: 32 rows to 64 units of 2,048 x 1,024 bf16 24 us (4.5 TB/s).
+// Bound by reading W: 16 rows to 8 units of 2,048 x 2,048 bf16 16.6 us (4.0 TB/s), to 4 of
+// 8,192 x 8,192 121 us (4.4 TB/s).
 template <typename T, int NB>
 __global__ __launch_bounds__(few::kWaves * 64) void k_unit_rows_few(
     const T *__restrict__ A, int64_t m, int32_t K, const T *__restrict__ W,
@@ -315,10 +316,8 @@ hipError_t unit_rows(const void *A, int64_t m, int32_t K, const void *W, const i
 
 template <typename T>
 hipError_t unit_rows_few(const void *A, int64_t m, int32_t K, const void *W, const int32_t *offsets,
-                         int64_t G, int32_t cols, void *out, hipStream_t st, int n_cu) {
-    const int64_t slots = slots_of(m, G, 16), units = G < m ? G : m;
-    const few::Deal d = few::deal(tiles_of(cols, 16), units, (int64_t)K * sizeof(T), n_cu);
-    const int64_t total = slots * d.groups, most = tile::kMostGroups;
+                         int64_t G, int32_t cols, const few::Deal &d, void *out, hipStream_t st) {
+    const int64_t slots = slots_of(m, G, 16), total = slots * d.groups, most = tile::kMostGroups;
     const dim3 grid((unsigned)(total < most ? total : most)), block(few::kWaves * 64);
     timing_before(st, "k_unit_rows_few");
     if (d.nb == 2)
@@ -351,10 +350,18 @@ hipError_t unit_mats(const void *dY, const void *X, int64_t m, int32_t d, const 
 
 // Which tile, from the rows a unit has on average (r) and the number of tiles; in
 // brackets us of the tile taken and of its neighbour, bf16 unless said.
-//   few.h      r <= 16, and tiles of 64 x 128 would not fill the GPU twice or rows are
-//              not on 16-byte addresses (16 rows to 8 units of 2,048 x 2,048: 14, 64 x 64 19;
-//              100 to 100 of 333 x 250 f32: 12, 64 x 64 22; 32 to 64 of 2,048 x
-//              1,024: 64 x 128 21, few 27)
+//   few.h      r <= 16, and
+//              - tiles of 64 x 64 are two for a CU at most (16 rows to 8 units of 2,048 x
+//                2,048: 16.6, 64 x 64 28.7; to 16 of them 128 rows 31, 36, 256 47, 36; to
+//                64 of them 128 rows 112, 113, 256 147, 131; at odd addresses 64 to 16 of
+//                1,027 x 1,025 24, 25), or fp32 has r <= 8, since its tiles' matrix
+//                instructions are mostly padding (256 to 64 of 1,024 x 1,024: 53, 64 x 64
+//                75; 512 67, 75; 1,024 103, 74);
+//              - and its empty workgroups cost less than the tiles' steps along k.  It
+//                launches `groups` of them for every unit, at 3.1 us for a thousand that
+//                find no rows; a step, 128 bytes of k, takes a tile 0.5 us in 16 bits and 1
+//                in fp32 (1 row to 64 of 2,048 x 1,024: 27, 64 x 64 8; 1 to 64 of 1,024 x
+//                4,096: 16.5 and 32, f32 19 and 72)
 //   256 x 256  r >= 200 and a tile for every CU (65,536 rows to 300 of 2,048 x 2,048,
 //              r = 218: 713, 128 x 128 820; r = 192, 64 of 2,048 x 1,024: 130 and 122);
 //              16-byte addresses only (through registers, 20,000 rows to 60 of 1,027
@@ -377,8 +384,13 @@ hipError_t launch_unit_rows(const void *A, int64_t m, int32_t K, int dtype, cons
         const int64_t units = G < m ? G : m;  // that have rows, at most
         const int64_t r = m / units;
         auto tiles = [&](int bm, int bn) { return (m / bm + units / 2) * tiles_of(cols, bn); };
-        if (!across && r <= 16 && (!aligned || units * tiles_of(cols, 128) < 2 * (int64_t)n_cu))
-            return unit_rows_few<T>(A, m, K, W, offsets, G, cols, out, st, n_cu);
+        if (!across && r <= 16) {
+            const few::Deal deal = few::deal(tiles_of(cols, 16), units, (int64_t)K * ES, n_cu);
+            const int64_t empty = slots_of(m, G, 16) * deal.groups;
+            if (empty * 4 <= (int64_t)K * ES * (ES == 4 ? 10 : 5) &&
+                ((ES == 4 && r <= 8) || units * tiles_of(cols, 64) <= 2 * (int64_t)n_cu))
+                return unit_rows_few<T>(A, m, K, W, offsets, G, cols, deal, out, st);
+        }
         if constexpr (ES == 2) {
             if (aligned && r >= 200 && tiles(256, 256) >= n_cu && !wasteful(cols))
                 return unit_rows<T, 256, 256, 2, 4>(A, m, K, W, offsets, G, cols, across, piece,

@@ -148,3 +148,38 @@ def test_scores(form, nq, nc, d):
     got, name = named(lambda: vs.vs_q8_scores(x.to(dev()), one[:nq], t.to(dev()), one))
     assert name == f"k_q8_scores<{form}>"
     same(got, x.float() @ t.float().T, torch.float32)  # below 2^24
+
+
+FEW = [
+    # type, rows, units, d, cols, the form the call takes
+    (torch.bfloat16, 1, 64, 1024, 2048, "<64x64,16>"),     # empty workgroups would be the most
+    (torch.bfloat16, 1, 64, 4096, 1024, "_few"),
+    (torch.bfloat16, 31, 64, 1024, 2048, "<64x128,16>"),   # as for 32
+    (torch.bfloat16, 32, 64, 1024, 2048, "<64x128,16>"),
+    (torch.bfloat16, 16, 8, 2048, 2048, "_few"),
+    (torch.bfloat16, 512, 32, 2048, 2048, "<64x128,16>"),
+    (torch.float16, 64, 16, 1027, 1025, "_few"),
+    (torch.float16, 4096, 256, 515, 131, "<64x64,0>"),     # 16 rows a unit at odd addresses
+    (torch.float32, 1, 64, 1024, 8192, "<64x64,16>"),
+    (torch.float32, 1, 64, 1024, 1024, "_few"),
+    (torch.float32, 31, 64, 1024, 2048, "_few"),
+    (torch.float32, 32, 64, 1024, 2048, "_few"),
+    (torch.float32, 256, 64, 1024, 1024, "_few"),
+    (torch.float32, 1024, 64, 1024, 1024, "<64x64,16>"),
+]
+
+
+@pytest.mark.parametrize("t,m,G,d,cols,form", FEW)
+def test_few_rows(t, m, G, d, cols, form):
+    """The form for units of few rows, on both sides of each border."""
+    gen = torch.Generator(device=dev()).manual_seed(m + cols)
+    X, W = (torch.randint(-3, 4, s, generator=gen, device=dev()).to(t) for s in ((m, d), (G, cols, d)))
+    unit = torch.sort(torch.randint(0, G, (m,), generator=gen, device=dev()))[0]
+    off = torch.searchsorted(unit, torch.arange(G + 1, device=dev())).int()
+    got, name = named(lambda: vs.vs_unit_products(X, W, off))
+    assert name == "k_unit_rows" + form
+    want = torch.empty(m, cols)
+    for g in unit.unique().tolist():
+        a, b = int(off[g]), int(off[g + 1])
+        want[a:b] = X[a:b].float().cpu() @ W[g].float().cpu().T
+    same(got, want, t)
