@@ -323,8 +323,9 @@ __global__ __launch_bounds__(block_of(TPR)) void k_norm_rows(NormArgs<T> a) {
             if constexpr (OUT == kRows) {
                 a.scalar[i] = rstd;
             } else {
-                // a row that holds a NaN or an infinity: NaN, with codes of 0
-                const float s = top / 127.0f * rstd;
+                // a row that holds a NaN or an infinity: NaN, with codes of 0.  top / 127
+                // must not become a subnormal number, nor top * rstd an infinity
+                const float s = top < 0x1p-100f ? top * rstd / 127.0f : top / 127.0f * rstd;
                 a.scalar[i] = coded ? s : top == 0.0f && rstd == rstd ? 0.0f : __builtin_nanf("");
             }
         }

@@ -1,0 +1,33 @@
+"""The row norm at the ends of fp32's range, on the GPU against 64 bits.
+
+Tolerances, in v = 2^-24, the rounding of one fp32 operation: rstd is within
+(d / 2 + 4) v by the sum of d positive terms (test_norm_q8.py), and 4 v more where the
+row is scaled to keep its squares in range and back.  A scale is top * rstd / 127: two
+roundings more, and half a unit of the subnormal numbers where it is one of them."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+import farthest_vector_search_amd as vs  # noqa: E402
+from test_norm_q8 import codes_ref, norm_ref, r_of  # noqa: E402
+from test_table_ops import SUB, V, close, dev, host, rng  # noqa: E402
+
+
+@pytest.mark.parametrize("e", [-90, -99, -100, -101, -118, -125])
+@pytest.mark.parametrize("d", [3, 8, 64, 777])
+def test_scales_of_tiny_rows(d, e):
+    """Rows whose largest magnitude over 127 is below the normal numbers, while the
+    scale itself, over the row's root mean square, is about 1 / 127."""
+    x64 = rng(90, d).uniform(0.5, 1, (200, d)) * 2.0 ** e
+    x = torch.from_numpy(x64).float().to(dev())
+    x64 = host(x)
+    for weight in (None, torch.full((d,), 0.75, device=dev())):
+        w64 = np.ones(d) if weight is None else host(weight)
+        h, rstd, _ = norm_ref(x64, None, w64, 0.0, torch.float32)
+        codes, scales, _ = vs.vs_norm_rows_q8(x, weight, 0.0)
+        c, top = codes_ref(h, w64)
+        assert np.array_equal(host(codes), c)
+        scale = (top * rstd / 127)[:, 0]
+        close(scales, scale, 1.01 * (r_of(d) + 10 * V) * scale + SUB[torch.float32])
