@@ -6,6 +6,7 @@
 // memory: every buffer is the caller's.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
@@ -1264,7 +1265,7 @@ VS_API int vs_unit_products_backward(const void *dYs, const void *Xs, int64_t m,
 
 static int norm_check(int64_t n, int32_t d, int32_t dtype, float eps) {
     if (bad_dtype(dtype)) return VS_ERR_DTYPE;
-    if (n < 0 || n > kMaxIndex || d < 1 || d > kMaxDim || !(eps >= 0.0f && eps <= 3.0e38f))
+    if (n < 0 || n > kMaxIndex || d < 1 || d > kMaxDim || !(eps >= 0.0f && eps <= FLT_MAX))
         return VS_ERR_SHAPE;
     return VS_OK;
 }

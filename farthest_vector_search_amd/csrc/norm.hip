@@ -159,7 +159,9 @@ template <typename F>
 __device__ __forceinline__ float rstd_of(float ss, float top, int64_t d, float eps, F again) {
     float rms;
     if (ss >= 0x1p-90f && ss <= 0x1p126f) {
-        rms = sqrtf(ss / (float)d + eps);
+        const float ms = ss / (float)d + eps;
+        // an eps near the largest number: the sum of quarters is finite
+        rms = ms < __builtin_inff() ? sqrtf(ms) : 2.0f * sqrtf(ss / (float)d * 0.25f + eps * 0.25f);
     } else {
         if (!(top < __builtin_inff())) return __builtin_nanf("");
         int e = top > 0.0f ? __builtin_amdgcn_frexp_expf(top) : 0;

@@ -31,3 +31,18 @@ def test_scales_of_tiny_rows(d, e):
         assert np.array_equal(host(codes), c)
         scale = (top * rstd / 127)[:, 0]
         close(scales, scale, 1.01 * (r_of(d) + 10 * V) * scale + SUB[torch.float32])
+
+
+@pytest.mark.parametrize("eps", [1e38, 2.9e38, 3.4e38])
+@pytest.mark.parametrize("d", [1, 3, 64])
+def test_largest_eps(d, eps):
+    """Every finite eps is taken, also where its sum with the mean square is none."""
+    x64 = rng(91, d).uniform(0.5, 1, (50, d)) * np.sqrt(2.0 ** 126 / d)
+    x64[1::3] *= 2.0 ** -70
+    x64[2::3] *= 1.5  # squares beyond 2^126
+    x = torch.from_numpy(x64).float().to(dev())
+    x64, eps = host(x), float(np.float32(eps))
+    _, rstd, y = norm_ref(x64, None, np.ones(d), eps, torch.float32)
+    Y, _, rs = vs.vs_norm_rows(x, None, eps)
+    close(rs, rstd[:, 0], 1.01 * (r_of(d) + 8 * V) * rstd[:, 0])
+    close(Y, y, 1.01 * (r_of(d) + 10 * V) * np.abs(y))
