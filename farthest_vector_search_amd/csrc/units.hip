@@ -406,9 +406,20 @@ hipError_t launch_unit_rows(const void *A, int64_t m, int32_t K, int dtype, cons
     });
 }
 
-// Runs that a unit's rows are cut into for the matrices' gradient: enough for two tiles
-// for every CU (of 128 x 128 if there are 64 of those and they pad little, else of 64 x
-// 64), of 128 rows on average at least, 32 at most.
+// Runs that a unit's rows are cut into for the matrices' gradient, 32 at most: enough for
+// two tiles for every CU, of 128 x 128 if there are 64 of those and they pad little, else
+// of 64 x 64 (fp32 has those alone, but is no slower with the runs that the large ones
+// ask for: 65,536 rows to one unit of 1,024 x 1,024, 8 runs 1,018 us, 2 1,092), and so
+// many rows on average that a run saves more than its sums cost to store and join (us in
+// one run and in runs):
+//   16 bits  1,024 rows (1 unit of 64 x 64, 2,048 rows: 13, 2 runs 11; 4,096: 21, 4 runs
+//            11), and four runs where matrices hold more than 2^18 elements together and
+//            rows move in pieces of 16 (16 units of 256 x 256, 1,024 rows each: 9.6, 8 runs
+//            24; 2,048: 16, 2 runs 22; 4,096: 34, 4 runs 26; 4 of 515 x 263, 2,048 rows
+//            through registers: 33, 2 runs 26)
+//   fp32     128 rows and four runs up to 2^18 elements (4 units of 64 x 64, 512 rows each:
+//            15.1, 4 runs 10.1; 256 rows 10.2, 2 runs 9.7), 1,024 rows beyond (16 of 256 x
+//            256, 1,024 rows: 27, 2 runs 30; 4,096: 87, 4 runs 77)
 static int64_t mats_tiles(int64_t G, int32_t cols, int32_t d, int b) {
     return G * tiles_of(cols, b) * tiles_of(d, b);
 }
@@ -419,15 +430,23 @@ static bool mats_filled(int64_t G, int32_t cols, int32_t d) {
 static bool mats_large(int64_t G, int32_t cols, int32_t d) {
     return mats_tiles(G, cols, d, 128) >= 64 && mats_filled(G, cols, d);
 }
-static int mats_parts(int64_t m, int64_t G, int32_t cols, int32_t d) {
+static int mats_parts(int64_t m, int64_t G, int32_t cols, int32_t d, int esize, int piece) {
     const int64_t tiles = mats_tiles(G, cols, d, mats_large(G, cols, d) ? 128 : 64);
-    const int64_t want = (512 + tiles - 1) / tiles, most = m / G / 128;
+    const bool small = G * (int64_t)cols * d <= (1 << 18);
+    const int64_t rows = small && esize == 4 ? 128 : 1024;
+    const int64_t least = esize == 4 ? (small ? 4 : 2) : (small || piece != 16 ? 2 : 4);
+    const int64_t want = (512 + tiles - 1) / tiles, most = m / G / rows;
     const int64_t parts = want < most ? want : most;
-    return (int)(parts < 1 ? 1 : parts > 32 ? 32 : parts);
+    return (int)(most < least || parts < 1 ? 1 : parts > 32 ? 32 : parts);
 }
 
+// for rows of any type and boundary
 size_t unit_mats_workspace(int64_t m, int64_t G, int32_t cols, int32_t d) {
-    const int parts = mats_parts(m, G, cols, d);
+    int parts = mats_parts(m, G, cols, d, 4, 16);
+    for (const int piece : {16, 0}) {
+        const int p = mats_parts(m, G, cols, d, 2, piece);
+        if (p > parts) parts = p;
+    }
     return parts > 1 ? (size_t)parts * (size_t)G * (size_t)cols * (size_t)d * 4 : 0;
 }
 
@@ -437,16 +456,16 @@ size_t unit_mats_workspace(int64_t m, int64_t G, int32_t cols, int32_t d) {
 // one and it pads little (20,000 rows to 60 of 1,027 x 1,027 f16: 151, 64 x 64 200; 9,000
 // to 100 of 260 x 130: 16.5, so 64 x 64 11.9; of 384 x 384: 15.4, 64 x 64 18.8).  Where
 // tiles are few and units have many rows, the rows are cut into runs, which a second
-// kernel joins (65,536 rows to 4 units of 64 x 64: 19, in one run 111; of 512 x 512: 62
-// and 179).
+// kernel joins (65,536 rows to 4 units of 64 x 64: 15, in one run 73; of 512 x 512: 47
+// and 119).
 hipError_t launch_unit_mats(const void *dY, const void *X, int64_t m, int32_t d, int dtype,
                             const int32_t *offsets, int64_t G, int32_t cols, int grad_dtype,
                             void *dW, void *ws, hipStream_t st, int n_cu) {
-    const int parts = mats_parts(m, G, cols, d);
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int ES = (int)sizeof(T);
         const int piece = piece_of(addr(dY), cols, addr(X), d, ES);
+        const int parts = mats_parts(m, G, cols, d, ES, piece);
         auto tiles = [&](int b) { return mats_tiles(G, cols, d, b); };
         auto go = [&](auto o) {
             using O = decltype(o);

@@ -105,12 +105,17 @@ MATS = [
     ("128x128,16", 20, 130, 250, 2, 512, 520, False),
     ("128x128,4", 20, 130, 250, 2, 510, 506, False),
     ("128x128,0", 20, 130, 250, 2, 509, 507, False),
-    ("128x128,16", 4, 1000, 2100, 0, 512, 504, True),
-    ("128x128,4", 4, 1000, 2100, 0, 506, 510, True),
-    ("128x128,0", 4, 1000, 2100, 0, 507, 509, True),
+    ("128x128,16", 4, 4200, 5300, 0, 512, 504, True),
+    ("128x128,4", 4, 4200, 5300, 0, 506, 510, True),
+    ("128x128,0", 4, 4200, 5300, 0, 507, 509, True),
     ("64x64,16", 20, 130, 250, 2, 264, 72, False),
     ("64x64,4", 20, 130, 250, 2, 262, 70, False),
     ("64x64,0", 20, 130, 250, 2, 261, 71, False),
+    ("64x64,16", 4, 1100, 1500, 0, 512, 504, False),   # rows too few for runs
+    ("64x64,16", 4, 2200, 2500, 0, 512, 504, False),
+    ("128x128,0", 4, 2200, 2500, 0, 511, 503, True),
+    ("64x64,16", 3, 2200, 2500, 0, 128, 72, True),
+    ("64x64,16", 3, 800, 1000, 0, 128, 72, False),
 ]
 
 
@@ -118,7 +123,8 @@ MATS = [
 def test_matrices(form, G, lo, hi, empty, d, cols, runs):
     r = rng(82, G, d, cols)
     off, m = places(r, G, lo, hi, empty)
-    assert (vs.lib().vs_unit_products_backward_workspace(m, d, G, cols) > 0) == runs
+    need = vs.lib().vs_unit_products_backward_workspace(m, d, G, cols)
+    ws = torch.empty(need + 256, dtype=torch.uint8, device=dev())
     X, dY = whole(r, (m, d), 3), whole(r, (m, cols), 3)
     dW = torch.stack([dY[a:b].T @ X[a:b] for a, b in zip(off, off[1:])])
     X[:9], X[off[-1]:], dY[:9], dY[off[-1]:] = (float("nan"),) * 4  # rows of no unit
@@ -126,10 +132,29 @@ def test_matrices(form, G, lo, hi, empty, d, cols, runs):
         x, dy, o = X.to(t).to(dev()), dY.to(t).to(dev()), i32(off)
         w = torch.zeros(G, cols, d, dtype=t, device=dev())
         for gt in (t, torch.float32):
+            ws.fill_(0xA5)
             (_, got), name = named(lambda: vs.vs_unit_products_backward(
-                dy, x, w, o, grad_dtype=gt, want_dXs=False))
+                dy, x, w, o, grad_dtype=gt, want_dXs=False, workspace=ws))
             assert name == f"k_unit_mats<{form}>"
+            assert bool((ws[:need] != 0xA5).any()) == runs  # runs leave their sums there
             same(got, dW, gt)
+
+
+@pytest.mark.parametrize("G,r,d,cols,runs", [(4, 600, 64, 64, True), (4, 400, 64, 64, False),
+                                             (16, 1100, 256, 256, False), (16, 2100, 256, 257, True)])
+def test_matrices_in_full_precision(G, r, d, cols, runs):
+    m = G * r
+    gen = rng(84, G, r)
+    X, dY = whole(gen, (m, d), 9), whole(gen, (m, cols), 9)
+    off = np.arange(G + 1) * r
+    dW = torch.stack([dY[a:b].T @ X[a:b] for a, b in zip(off, off[1:])])
+    need = vs.lib().vs_unit_products_backward_workspace(m, d, G, cols)
+    ws = torch.full((need + 256,), 0xA5, dtype=torch.uint8, device=dev())
+    w = torch.zeros(G, cols, d, device=dev())
+    _, got = vs.vs_unit_products_backward(dY.to(dev()), X.to(dev()), w, i32(off), want_dXs=False,
+                                          workspace=ws)
+    assert bool((ws[:need] != 0xA5).any()) == runs
+    same(got, dW, torch.float32)
 
 
 SCORES = [
