@@ -586,10 +586,14 @@ hipError_t norm_rows(const NormArgs<T> &a, hipStream_t st, int n_cu) {
 }
 
 // Partial sums of the weight's gradient: one per workgroup of the backward pass.  Fewer
-// leave CUs idle, more cost the join: 16,384 x 2,048 bf16 at 256, 512, 1,024 parts 39, 33,
-// 37 us, 65,536 x 512 63, 41, 34, 4,096 x 4,096 32, 25, 29.
-constexpr int64_t kMostParts = 512;
-inline int64_t bwd_groups(int64_t n) { return n < kMostParts ? n : kMostParts; }
+// leave CUs idle, more cost the join.  A workgroup with one vector a thread has half as
+// many bytes on their way as one with two, so twice as many of them run (us at 512 and
+// 1,024 parts, bf16 unless said: 65,536 x 512 47 and 40, 524,288 x 128 275 and 171, 262,144
+// x 64 116 and 80, 16,384 x 2,047 67 and 51, 16,384 x 1,023 fp32 53 and 42, 16,384 x 128
+// 12.7 and 13.2; with more vectors: 16,384 x 2,048 40 and 44, 4,096 x 4,096 28 and 32, 65,536
+// x 1,024 78 and 84, 16,384 x 1,023 27 and 29).
+constexpr int64_t most_parts(int vpt) { return vpt == 1 ? 1024 : 512; }
+inline int64_t bwd_groups(int64_t n, int vpt) { return n < most_parts(vpt) ? n : most_parts(vpt); }
 
 }  // namespace
 
@@ -626,7 +630,8 @@ hipError_t launch_q8_quantize(const void *X, int64_t n, int32_t d, int dtype, in
 }
 
 size_t norm_bwd_workspace(int64_t n, int32_t d) {
-    return (size_t)bwd_groups(n) * (size_t)d * 4;
+    // rows of more than 256 vectors of 16 bits have more than one a thread in every type
+    return (size_t)bwd_groups(n, d <= 2048 ? 1 : 2) * (size_t)d * 4;
 }
 
 hipError_t launch_norm_rows_bwd(const void *dY, const void *H, const void *w, const void *dH,
@@ -641,7 +646,7 @@ hipError_t launch_norm_rows_bwd(const void *dY, const void *H, const void *w, co
         return with_row<T, kBackward>(n, d, n_cu, [&](auto tpr, auto vpt, auto fit) {
             constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
             constexpr int kPer = block_of(TPR) / TPR;
-            const int64_t want = (n + kPer - 1) / kPer, most = bwd_groups(n);
+            const int64_t want = (n + kPer - 1) / kPer, most = bwd_groups(n, VPT);
             parts = (int)(want < most ? want : most);
             timing_before(st, "k_norm_rows_bwd");
             hipLaunchKernelGGL((k_norm_rows_bwd<T, TPR, VPT, decltype(fit)::value>), dim3(parts),

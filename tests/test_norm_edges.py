@@ -46,3 +46,23 @@ def test_largest_eps(d, eps):
     Y, _, rs = vs.vs_norm_rows(x, None, eps)
     close(rs, rstd[:, 0], 1.01 * (r_of(d) + 8 * V) * rstd[:, 0])
     close(Y, y, 1.01 * (r_of(d) + 10 * V) * np.abs(y))
+
+
+@pytest.mark.parametrize("t", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("n,d", [(511, 64), (513, 257), (1023, 128), (1025, 512), (4100, 7), (4101, 64),
+                                 (9000, 2047), (1500, 2048), (600, 2056)])
+def test_weights_gradient_of_many_rows(n, d, t):
+    """The weight's gradient on both sides of each number of partial sums: whole numbers
+    over rows of rms 1 (+-1), so that every sum is exact.  The workspace holds just what
+    the size query says, and nothing behind it is written."""
+    r = rng(92, n, d)
+    h = torch.from_numpy(r.choice([-1.0, 1.0], (n, d)).astype(np.float32))
+    dY = torch.from_numpy(r.integers(-3, 4, (n, d)).astype(np.float32))
+    want = (h * dY).sum(0)
+    w, rs = torch.ones(d, device=dev()).to(t), torch.ones(n, device=dev())
+    need = vs.lib().vs_norm_rows_backward_workspace(n, d)
+    buf = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device=dev())
+    _, dw = vs.vs_norm_rows_backward(dY.to(t).to(dev()), h.to(t).to(dev()), w, rs,
+                                     grad_dtype=torch.float32, workspace=buf[:need])
+    assert torch.equal(dw.cpu(), want)
+    assert bool((buf[need:] == 0x5A).all())
