@@ -362,13 +362,13 @@ hipError_t unit_mats(const void *dY, const void *X, int64_t m, int32_t d, const 
 //                find no rows; a step, 128 bytes of k, takes a tile 0.5 us in 16 bits and 1
 //                in fp32 (1 row to 64 of 2,048 x 1,024: 27, 64 x 64 8; 1 to 64 of 1,024 x
 //                4,096: 16.5 and 32, f32 19 and 72)
-//   256 x 256  r >= 200 and a tile for every CU (65,536 rows to 300 of 2,048 x 2,048,
-//              r = 218: 713, 128 x 128 820; r = 192, 64 of 2,048 x 1,024: 130 and 122);
-//              16-byte addresses only (through registers, 20,000 rows to 60 of 1,027
-//              x 1,027: 141, 128 x 128 117)
-//   128 x 128  r >= 96 and two for every CU (r = 128 of the 64: 47, 64 x 128 46;
-//              64 of 2,048 x 1,024, r = 192: 122, 256 x 256 130)
-//   64 x 128   fewer rows (r = 32 of the 64: 32, 64 x 64 38, 128 x 128 43); 64 x 64
+//   256 x 256  r >= 128 and a tile for every CU (64 units of 1,024 x 1,024, r = 150: 39,
+//              128 x 128 48; 256 of 2,048 x 2,048: 546 and 668, r = 200 573 and 696; r = 96:
+//              454 and 438, of 1,024 x 1,024 145 and 141); 16-byte addresses only (through
+//              registers, 20,000 rows to 60 of 1,027 x 1,027: 141, 128 x 128 117)
+//   128 x 128  r >= 96 and two for every CU (256 of 2,048 x 2,048, r = 96: 438, 64 x 128
+//              512; r = 48: 426 and 424)
+//   64 x 128   fewer rows (of the same, r = 48: 424, 64 x 64 490); 64 x 64
 //              at other addresses (2,501 rows to 60 of 257 x 515 f16: 14, 64 x 128 19)
 //              and where tiles are few
 // fp32 has 64 x 64 only: bound by its matrix instructions, larger ones gain nothing
@@ -392,7 +392,7 @@ hipError_t launch_unit_rows(const void *A, int64_t m, int32_t K, int dtype, cons
                 return unit_rows_few<T>(A, m, K, W, offsets, G, cols, deal, out, st);
         }
         if constexpr (ES == 2) {
-            if (aligned && r >= 200 && tiles(256, 256) >= n_cu && !wasteful(cols))
+            if (aligned && r >= 128 && tiles(256, 256) >= n_cu && !wasteful(cols))
                 return unit_rows<T, 256, 256, 2, 4>(A, m, K, W, offsets, G, cols, across, piece,
                                                     out, st);
             if (r >= 96 && tiles(128, 128) >= 2 * (int64_t)n_cu)

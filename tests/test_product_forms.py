@@ -45,8 +45,9 @@ def same(got, want, t):
 ROWS = [
     # form, across's form, units, rows a unit (least, most, empty units), d, cols
     ("256x256,16", "256x256,16", 64, 200, 300, 2, 1032, 1024),
+    ("256x256,16", "256x256,16", 64, 130, 170, 0, 1032, 1048),
     ("256x256,16", "256x256,16", 300, 190, 260, 5, 520, 512),      # found by slots
-    ("128x128,16", "128x128,16", 64, 100, 180, 3, 1032, 1048),
+    ("128x128,16", "128x128,16", 64, 100, 140, 3, 1032, 1048),
     ("128x128,16", "128x128,16", 300, 90, 130, 5, 264, 272),       # found by slots
     ("128x128,4", "128x128,4", 64, 100, 180, 3, 1030, 1042),
     ("128x128,0", "128x128,0", 64, 100, 180, 3, 1027, 1033),
