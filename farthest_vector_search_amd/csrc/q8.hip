@@ -107,10 +107,16 @@ hipError_t q8_scores(const int8_t *x, const float *xs, int64_t nq, int32_t d, co
 }  // namespace
 
 // Which kernel, in brackets us of it and of its neighbour:
-//   few.h      up to 4 queries (1 over 262,144 x 256: 15, 64 x 64 17), up to 16 where
-//              rows are long (16 over 65,536 x 4,096: 59 and 67; 16 over 8,359 x 767:
-//              14 and 10), and more where tiles of 64 x 64 leave half the CUs idle (64
-//              over 4,096 x 4,096: 17.5 with tiles)
+//   few.h      reads the table once for every 16 queries.  Rows on 4-byte boundaries: up
+//              to 4 queries (1 over 262,144 x 256: 15, 64 x 64 17); with rows of 1,024 codes
+//              or more up to 16 (16 over 65,536 x 4,096: 59 and 67), and any number while
+//              12,288 rows are read in all, since tiles leave most CUs idle there (256 over
+//              300 x 2,048: 7.9, 64 x 64 8.4, over 1,000 x 8,192 27 and 33; 1,024 over 300 x
+//              2,048: 17 and 8.4).  At other addresses its loads are the slower ones: while
+//              8,192 rows are read in all, of 512 codes or more for up to 4 queries, of
+//              1,024 for more (4 over 4,096 x 767: 8.0, 64 x 64 8.8, over 32,768 18 and 11.5,
+//              over 4,096 x 255 9.0 and 5.7; 16 over 4,096 x 2,047: 12 and 18, over 32,768 48
+//              and 24)
 //   64 x 64    up to 64 queries (37 over 8,359 x 767: 10, 128 x 128 13), or too few
 //              tiles of 128 x 128 for the GPU
 //   128 x 128  96 over 65,536 x 4,096: 74, 64 x 64 85; 1,000 over 20,000 x 1,000: 53,
@@ -127,7 +133,9 @@ hipError_t launch_q8_scores(const int8_t *x, const float *xs, int64_t nq, int32_
     auto tiles = [&](int b) { return tiles_of(nq, b) * tiles_of(nc, b); };
     auto go = [&](auto o) {
         using O = decltype(o);
-        if (nq <= 4 || (d >= 1024 && (nq <= 16 || tiles(64) * 2 < n_cu)))
+        const int64_t reads = tiles_of(nq, 16) * nc;  // rows of the table, with few.h
+        if (piece ? nq <= 4 || (d >= 1024 && (nq <= 16 || reads <= 12288))
+                  : d >= (nq <= 4 ? 512 : 1024) && reads <= 8192)
             return q8_scores_few<O>(x, xs, nq, d, table, ts, nc, (O *)y, st, n_cu);
         if (piece == 16 && nq >= 192 && tiles(256) >= 2 * (int64_t)n_cu)
             return q8_scores<O, 256, 256, 2, 4>(x, xs, nq, d, table, ts, nc, piece, (O *)y, st);

@@ -209,3 +209,32 @@ def test_few_rows(t, m, G, d, cols, form):
         a, b = int(off[g]), int(off[g + 1])
         want[a:b] = X[a:b].float().cpu() @ W[g].float().cpu().T
     same(got, want, t)
+
+
+@pytest.mark.parametrize("nq,nc,d,form", [
+    (4, 4096, 256, "_few"), (4, 4096, 255, "<64x64,0>"), (4, 4096, 767, "_few"),
+    (4, 32768, 767, "<64x64,0>"), (5, 4096, 256, "<64x64,16>"), (16, 9000, 1024, "_few"),
+    (17, 9000, 1024, "<64x64,16>"), (16, 4096, 1027, "_few"), (16, 9000, 1027, "<64x64,0>"),
+    (256, 300, 1024, "_few"), (1024, 300, 1024, "<64x64,16>"), (16, 9000, 1020, "<64x64,4>"),
+    (16, 9000, 1028, "_few")])
+def test_few_queries(nq, nc, d, form):
+    """The form for few queries, on both sides of each border."""
+    r = rng(85, nq, nc, d)
+    x, t = (torch.from_numpy(r.integers(-120, 121, s).astype(np.int8)) for s in ((nq, d), (nc, d)))
+    one = torch.ones(max(nq, nc), device=dev())
+    got, name = named(lambda: vs.vs_q8_scores(x.to(dev()), one[:nq], t.to(dev()), one[:nc]))
+    assert name == "k_q8_scores" + form
+    same(got, x.float() @ t.float().T, torch.float32)  # below 2^24
+
+
+def test_few_queries_over_very_many_rows():
+    """More workgroups than a launch takes at a time, in the form for few queries."""
+    nc, d = 150000000, 4
+    gen = torch.Generator(device=dev()).manual_seed(9)
+    t = torch.empty(nc, d, dtype=torch.int8, device=dev()).random_(-100, 101, generator=gen)
+    one = torch.ones(nc, device=dev())
+    q = t[nc // 2:nc // 2 + 1].contiguous()
+    got, name = named(lambda: vs.vs_q8_scores(q, one[:1], t, one))
+    assert name == "k_q8_scores_few"
+    for lo in range(0, nc, 1 << 25):
+        assert torch.equal(got[0, lo:lo + (1 << 25)], (t[lo:lo + (1 << 25)].float() * q.float()).sum(1))
