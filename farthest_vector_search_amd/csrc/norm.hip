@@ -577,7 +577,9 @@ hipError_t norm_rows(const NormArgs<T> &a, hipStream_t st, int n_cu) {
         constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
         constexpr int kPer = block_of(TPR) / TPR;
         const int64_t want = (a.n + kPer - 1) / kPer, most = (int64_t)n_cu * 64;
-        timing_before(st, OUT == kRows ? "k_norm_rows" : "k_norm_rows_q8");
+        timing_before(st, OUT == kRows    ? "k_norm_rows"
+                          : OUT == kCodes ? "k_norm_rows_q8"
+                                          : "k_q8_quantize");
         hipLaunchKernelGGL((k_norm_rows<T, TPR, VPT, decltype(fit)::value, OUT>),
                            dim3((unsigned)(want < most ? want : most)), dim3(block_of(TPR)), 0, st, a);
         timing_after(st);

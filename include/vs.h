@@ -676,13 +676,14 @@ int64_t vs_tile_rows(int64_t cache_bytes, int32_t d, int32_t bytes_per_value);
 /*
  * Measurement hook (host-only bookkeeping, no device memory): while enabled,
  * the dominant kernel of each call is bracketed by a pair of HIP events on
- * the call's stream.  vs_timing_enable(max_launches) (re)starts recording
- * for up to max_launches launches (0 disables); vs_timing_read() waits for
- * the recorded events, returns the summed kernel time in milliseconds and the
- * number of launches, and stops recording.  vs_timing_kernel_name() names the
- * last of them, the tiled products with their tile and the bytes that rows
- * move in (k_unit_rows<128x128,16>, across W k_unit_rows<128x128,16,across>;
- * 0: through registers).
+ * the call's stream (both products of vs_unit_products_backward; launches that
+ * prepare, or join partial sums behind it, are not).
+ * vs_timing_enable(max_launches) (re)starts recording for up to max_launches
+ * launches (0 disables); vs_timing_read() waits for the recorded events, returns
+ * the summed kernel time in milliseconds and the number of launches, and stops
+ * recording.  vs_timing_kernel_name() names the last of them, the tiled products
+ * with their tile and the bytes that rows move in (k_unit_rows<128x128,16>, across
+ * W k_unit_rows<128x128,16,across>; 0: through registers).
  */
 int vs_timing_enable(int32_t max_launches);
 int vs_timing_read(double *total_ms, int64_t *launches);

@@ -238,3 +238,18 @@ def test_few_queries_over_very_many_rows():
     assert name == "k_q8_scores_few"
     for lo in range(0, nc, 1 << 25):
         assert torch.equal(got[0, lo:lo + (1 << 25)], (t[lo:lo + (1 << 25)].float() * q.float()).sum(1))
+
+
+def test_timed_names():
+    """The timing hook names each call's own kernel; both gradients are timed."""
+    x = torch.ones(6, 64, device=dev())
+    w, rs = torch.ones(64, device=dev()), torch.ones(6, device=dev())
+    for call, name in ((lambda: vs.vs_norm_rows(x, w), "k_norm_rows"),
+                       (lambda: vs.vs_norm_rows_q8(x, w), "k_norm_rows_q8"),
+                       (lambda: vs.vs_q8_quantize(x), "k_q8_quantize"),
+                       (lambda: vs.vs_norm_rows_backward(x, x, w, rs), "k_norm_rows_bwd")):
+        assert named(call)[1] == name
+    W, off = torch.ones(2, 8, 64, device=dev()), i32(np.array([0, 2, 6]))
+    with vs.KernelTimer(8) as kt:
+        vs.vs_unit_products_backward(torch.ones(6, 8, device=dev()), x, W, off)
+    assert kt.launches == 2 and kt.ms > 0 and kt.name.startswith("k_unit_mats")
