@@ -11,8 +11,8 @@
 // sides' pieces of a step are brought into LDS (two buffers, one barrier a step)
 // while others are multiplied.  LDS holds a side as
 //   along   128 bytes for each of its rows; the eight 16-byte chunks of row r stand
-//           at chunk ^ (r & 7), so that 8 lanes reading one chunk of 8 rows meet 8
-//           different bank groups
+//           at chunk ^ (r / 2 & 7), so that 16 lanes reading one chunk of 16 rows meet 16
+//           different groups of banks (two rows fill the 64 banks)
 //   across  a row for each k; chunks of row k stand at chunk ^ 2 (k & 3) for 16-bit
 //           elements, chunk ^ (k & 4) for fp32, for the same reason
 // The matrix instruction takes 16 bytes of k a lane.  From an "along" side that is
