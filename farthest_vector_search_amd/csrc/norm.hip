@@ -517,6 +517,9 @@ __global__ __launch_bounds__(1024) void k_norm_join(const float *__restrict__ pa
 //                backward twice, 512 rows 62, 96, 2,048 rows 283, 223 (1,024 x 4 does not
 //                fit the registers); codes: twice by 256 against by 1,024, 2,048 rows 71, 74,
 //                64 rows 19, 10.6
+// A wave holds one row, however narrow, so below 512 columns of 16 bits some of its lanes
+// load nothing: 524,288 rows of 128 140 forward, 171 backward (1.9 and 2.4 TB/s), 262,144
+// of 64 63 and 82 (1.1 and 1.2 TB/s).
 enum Pass { kForward, kToCodes, kBackward };
 
 template <typename T, Pass PASS, typename F>

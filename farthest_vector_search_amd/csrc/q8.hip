@@ -4,8 +4,8 @@
 // The sum is a whole number below 2^31 (d <= 131,071 codes of -128 .. 127), taken
 // exactly; it is rounded to fp32 once, multiplied by both scales there, and the
 // result rounded to the output's type.  Bound by the matrix cores where queries are many
-// (8,192 over 8,192 x 8,192, bf16 scores: 418 us, 2,630 Top/s), by reading the table where
-// they are few (1 over 65,536 x 4,096: 50 us, 5.3 TB/s).
+// (8,192 over 8,192 x 8,192, bf16 scores: 455 us, 383 at best, 2,870 Top/s), by reading the
+// table where they are few (1 over 65,536 x 4,096: 51 us, 5.3 TB/s).
 #include <type_traits>
 
 #include "few.h"

@@ -87,8 +87,9 @@ __device__ __forceinline__ int scan(int v) {
 // 8,192 x 8,192 913 and 790; 10,240 to 64 of 1,024 x 1,024 58 and 50; 32 to 64 of 2,048 x
 // 1,024 24.9 and 21.2).  Counting takes every lane more loads the more units there are:
 // 65,536 rows to 300 of 2,048 x 2,048 707 and 707; 60,000 to 300 of 512 x 512 71 and 74,
-// to 1,000 137 and 165; 2,500 to 2,500 of 512 x 256 94 and 199.  Whole tiles first and units' last tiles behind them was slower (65,536 rows to
-// 128 of 2,048 x 2,048: 609, so 669), since W is then read twice.
+// to 1,000 137 and 165; 2,500 to 2,500 of 512 x 256 94 and 199.  Whole tiles first and
+// units' last tiles behind them was slower (65,536 rows to 128 of 2,048 x 2,048: 609, so
+// 669), since W is then read twice.
 constexpr int64_t kCounted = 256;
 __device__ __forceinline__ bool counted_tile(const int32_t *__restrict__ offsets, int64_t G,
                                              int64_t m, int rows, int64_t ctiles, int64_t id,
@@ -142,9 +143,9 @@ __device__ __forceinline__ bool counted_tile(const int32_t *__restrict__ offsets
 
 // out[p][j] = sum_k A[p][k] B(g)(j, k): B = W[g][j][k], or W[g][k][j] (ACROSS).  Bound
 // by the matrix cores where units have many rows (8,192 rows to one unit of 8,192 x 8,192
-// bf16: 790 us, 1,392 TFLOP/s, across 780 us, 1,410 TFLOP/s), with 65,536 rows to 128 of
-// 2,048 x 2,048 at random 600 us (916 TFLOP/s: units' last tiles); fp32 1,012 us for
-// 16,384 to 16 of 2,048 x 2,048 (136 TFLOP/s).  By reading W where they have few: 1,024
+// bf16: 810 us, 781 at best, 1,408 TFLOP/s; across 796 and 750 us, 1,466 TFLOP/s), with
+// 65,536 rows to 128 of 2,048 x 2,048 at random 600 us (916 TFLOP/s: units' last tiles); fp32
+// 971 us for 16,384 to 16 of 2,048 x 2,048 (142 TFLOP/s).  By reading W where they have few: 1,024
 // rows to 64 of 1,024 x 1,024 28 us (4.9 TB/s).
 template <typename T, int BM, int BN, int WM, int WN, bool ACROSS, int PIECE>
 __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_rows(
@@ -212,8 +213,8 @@ __global__ __launch_bounds__(few::kWaves * 64) void k_unit_rows_few(
 // dW[g][j][k] = sum over g's rows p of dY[p][j] X[p][k]: both sides across.  With
 // `parts` > 1 each unit's rows are cut into so many equal runs, whose sums stand one
 // array of matrices behind the other.  Bound by the matrix cores where units have many
-// rows (8,192 of one, 8,192 x 8,192 bf16: 770 us, 1,429 TFLOP/s), by writing dW where they
-// have few (64 rows to 64 of 1,024 x 1,024: 35 us, 3.8 TB/s).
+// rows (8,192 of one, 8,192 x 8,192 bf16: 819 us, 777 at best, 1,415 TFLOP/s), by writing
+// dW where they have few (64 rows to 64 of 1,024 x 1,024: 35 us, 3.8 TB/s).
 template <typename T, typename O, int BM, int BN, int WM, int WN, int PIECE>
 __global__ __launch_bounds__(WM *WN * 64, 2) void k_unit_mats(
     const T *__restrict__ dY, const T *__restrict__ X, int64_t m, int32_t d,
