@@ -433,11 +433,12 @@ static bool mats_large(int64_t G, int32_t cols, int32_t d) {
 }
 static int mats_parts(int64_t m, int64_t G, int32_t cols, int32_t d, int esize, int piece) {
     const int64_t tiles = mats_tiles(G, cols, d, mats_large(G, cols, d) ? 128 : 64);
+    const int64_t want = (512 + tiles - 1) / tiles;
+    if (want < 2) return 1;  // also: matrices whose elements 64 bits do not count
     const bool small = G * (int64_t)cols * d <= (1 << 18);
     const int64_t rows = small && esize == 4 ? 128 : 1024;
     const int64_t least = esize == 4 ? (small ? 4 : 2) : (small || piece != 16 ? 2 : 4);
-    const int64_t want = (512 + tiles - 1) / tiles, most = m / G / rows;
-    const int64_t parts = want < most ? want : most;
+    const int64_t most = m / G / rows, parts = want < most ? want : most;
     return (int)(most < least || parts < 1 ? 1 : parts > 32 ? 32 : parts);
 }
 
